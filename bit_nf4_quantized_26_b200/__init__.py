@@ -1,5 +1,5 @@
-"""Python binding of ``libqlora_nf4.so`` (the C ABI in ``include/qlora_nf4.h`` and
-``include/qlora_optim.h``).
+"""Python binding of ``libqlora_nf4.so`` (the C ABI in ``include/qlora_nf4.h``,
+``include/qlora_optim.h`` and ``include/qlora_train.h``).
 
 Argument marshalling only: every step of the computation runs in the
 library's CUDA kernels.  PyTorch provides device memory and the current
@@ -13,6 +13,9 @@ Functions keep the C names:
 * :func:`qlora_fwd_workspace_size` / :func:`qlora_bwd_workspace_size`
 * :func:`nf4_levels`, :func:`qlora_strerror`
 * :func:`qlora_adamw8_step` with :class:`AdamW8State` (``include/qlora_optim.h``)
+* :func:`qlora_head_loss_fwd` / :func:`qlora_head_loss_bwd` /
+  :func:`qlora_head_loss_step`, :func:`act8_quantize` / :func:`act8_dequantize`
+  and the ``*_bwd_act8`` backward passes (``include/qlora_train.h``)
 """
 
 import ctypes
@@ -559,3 +562,325 @@ def nf4_dequantize_centered(codes, c8, s2, mean, numel, out=None, stream=None):
     _check(_lib.nf4_dequantize_centered(_ptr(codes), _ptr(c8), _ptr(s2), _ptr(mean), numel, _ptr(out),
                                         _stream(stream)), "nf4_dequantize_centered")
     return out
+
+
+# ------------------------------------------------ 8-bit activation checkpoints
+# (include/qlora_train.h: E4M3 codes with a power of two per 64 elements)
+
+_lib.act8_quantize.argtypes = [_P, _I64, _I64, _I64, _P, _P, _P, _P]
+_lib.act8_quantize.restype = ctypes.c_int
+_lib.act8_dequantize.argtypes = [_P, _P, _I64, _I64, _P, _I64, _P]
+_lib.act8_dequantize.restype = ctypes.c_int
+_lib.qlora_linear_bwd_act8.argtypes = [_P, _P, _P, _P, _I64, _NF4Weight, _P, _P, _I32, _F, _P, _I32, _P, _P, _P, _SZ,
+                                       _P, _P]
+_lib.qlora_linear_bwd_act8.restype = ctypes.c_int
+_lib.qlora_group_bwd_act8.argtypes = [_P, _P, _P, _P, _I64, _NF4Weight, _I32, _P, _P, _P, _I32, _F, _P, _I32, _P, _P,
+                                      _P, _SZ, _P, _P]
+_lib.qlora_group_bwd_act8.restype = ctypes.c_int
+_lib.qlora_linear_bwd_dropout_act8.argtypes = [_P, _P, _P, _P, _I64, _NF4Weight, _P, _P, _I32, _F, _F, _U64, _P, _I32,
+                                               _P, _P, _P, _SZ, _P, _P]
+_lib.qlora_linear_bwd_dropout_act8.restype = ctypes.c_int
+
+EXPORTED_TRAIN = ("act8_quantize", "act8_dequantize", "qlora_linear_bwd_act8", "qlora_group_bwd_act8",
+                  "qlora_linear_bwd_dropout_act8")
+
+DEV_LABEL = 4
+ERR_SHAPE = 2
+ERR_DTYPE = 9
+
+#: 8-bit checkpoint of X [M, K]: ``codes`` uint8 [M, K], ``exps`` uint8 [M, K / 64].
+Act8 = namedtuple("Act8", "codes exps")
+
+
+class _On:
+    """The device of a call's tensors, and the stream it runs on: ``stream``, or
+    that device's current one.  What a call allocates belongs to that stream."""
+
+    def __init__(self, dev, stream):
+        self._guards = []
+        if dev.index is not None and dev.index != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(dev))
+        if stream is not None:
+            self._guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+def _need(ok, code, where, what):
+    if not ok:
+        raise QloraError(code, f"{where}: {what}")
+
+
+def _tensor(t, dtype, shape, dev, where, name):
+    """A contiguous tensor of this type and shape on this device."""
+    _need(t.dtype == dtype, ERR_DTYPE, where, f"{name} is {t.dtype}, not {dtype}")
+    _need(tuple(t.shape) == tuple(shape), ERR_SHAPE, where, f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+    _need(t.device == dev, ERR_SHAPE, where, f"{name} is on {t.device}, not {dev}")
+    _need(t.is_contiguous(), ERR_SHAPE, where, f"{name} is not contiguous")
+    return t
+
+
+def _vector(t, dtype, n, dev, where, name):
+    return _tensor(t, dtype, (n,), dev, where, name)
+
+
+def _rows(t, where, name, cols=None, rows=None, dev=None):
+    """(rows, columns, row stride) of a bf16 matrix whose rows are contiguous."""
+    _need(t.dtype == torch.bfloat16, ERR_DTYPE, where, f"{name} is {t.dtype}, not torch.bfloat16")
+    _need(t.dim() == 2, ERR_SHAPE, where, f"{name} has {t.dim()} dimensions, not 2")
+    _need(t.is_cuda and (dev is None or t.device == dev), ERR_SHAPE, where, f"{name} is on {t.device}")
+    M, K = t.shape
+    _need((cols is None or K == cols) and (rows is None or M == rows), ERR_SHAPE, where,
+          f"{name} is {tuple(t.shape)}, not {(rows if rows is not None else M, cols if cols is not None else K)}")
+    _need(K <= 1 or M == 0 or t.stride(1) == 1, ERR_SHAPE, where, f"{name}'s rows are not contiguous")
+    return M, K, t.stride(0) if M > 1 else K
+
+
+def _status_word(status, dev, where):
+    if status is not None:
+        _need(status.dtype == torch.int32 and status.numel() >= 1 and status.device == dev, ERR_DTYPE, where,
+              "status is not an int32 word on the call's device")
+
+
+def act8_quantize(X, codes=None, exps=None, status=None, stream=None):
+    """8-bit checkpoint of a bf16 CUDA matrix X [M, K] (K % 64 == 0, rows may be
+    strided); returns an :class:`Act8` (its tensors allocated if not given)."""
+    where = "act8_quantize"
+    M, K, ld = _rows(X, where, "X")
+    dev = X.device
+    _status_word(status, dev, where)
+    with _On(dev, stream) as st:
+        codes = (torch.empty((M, K), dtype=torch.uint8, device=dev) if codes is None
+                 else _tensor(codes, torch.uint8, (M, K), dev, where, "codes"))
+        exps = (torch.empty((M, K // 64), dtype=torch.uint8, device=dev) if exps is None
+                else _tensor(exps, torch.uint8, (M, K // 64), dev, where, "exps"))
+        _check(_lib.act8_quantize(_ptr(X), M, K, ld, _ptr(codes), _ptr(exps), _ptr(status), st), where)
+    return Act8(codes, exps)
+
+
+def act8_dequantize(X8, out=None, stream=None):
+    """The bf16 values [M, K] an :class:`Act8` stands for (``out`` may have strided rows)."""
+    where = "act8_dequantize"
+    codes, exps = X8
+    _need(codes.dim() == 2 and codes.is_cuda, ERR_SHAPE, where, "codes is not a CUDA matrix")
+    M, K = codes.shape
+    dev = codes.device
+    _act8(X8, M, K, dev, where)
+    with _On(dev, stream) as st:
+        if out is None:
+            out, ld = torch.empty((M, K), dtype=torch.bfloat16, device=dev), K
+        else:
+            ld = _rows(out, where, "out", K, M, dev)[2]
+        _check(_lib.act8_dequantize(_ptr(codes), _ptr(exps), M, K, _ptr(out), ld, st), where)
+    return out
+
+
+def _act8(X8, M, K, dev, where):
+    codes, exps = X8
+    _tensor(codes, torch.uint8, (M, K), dev, where, "codes")
+    _tensor(exps, torch.uint8, (M, K // 64), dev, where, "exps")
+
+
+def _bwd_act8(where, dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, ws_bytes, ws, status, stream, call):
+    """Checks, outputs and workspace shared by the ``*_bwd_act8`` passes."""
+    N, K = int(W.n_out), int(W.k_in)
+    M = dY.shape[0]
+    dev = dY.device
+    _need(A.dim() == 2 and A.shape[0] % G == 0, ERR_SHAPE, where, f"A is {tuple(A.shape)} for {G} members")
+    r = A.shape[0] // G
+    _tensor(dY, torch.bfloat16, (M, N), dev, where, "dY")
+    _act8(X8, M, K, dev, where)
+    _tensor(U, torch.float32, (M, G * r), dev, where, "U")
+    _tensor(A, torch.bfloat16, (G * r, K), dev, where, "A")
+    _tensor(B, torch.bfloat16, (N, r), dev, where, "B")
+    _need(dx_dtype in (DTYPE_BF16, DTYPE_F32), ERR_DTYPE, where, "dx_dtype")
+    _status_word(status, dev, where)
+    with _On(dev, stream) as st:
+        xt = torch.float32 if dx_dtype == DTYPE_F32 else torch.bfloat16
+        dX = torch.empty((M, K), dtype=xt, device=dev) if dX is None else _tensor(dX, xt, (M, K), dev, where, "dX")
+        dA = (torch.empty((G * r, K), dtype=torch.float32, device=dev) if dA is None
+              else _tensor(dA, torch.float32, (G * r, K), dev, where, "dA"))
+        dB = (torch.empty((N, r), dtype=torch.float32, device=dev) if dB is None
+              else _tensor(dB, torch.float32, (N, r), dev, where, "dB"))
+        if ws is None:
+            ws = torch.empty(max(ws_bytes(M, N, K, r), 16), dtype=torch.uint8, device=dev)
+        if M == 0:  # nothing to sum; the library's call is a no-op
+            dA.zero_()
+            dB.zero_()
+        else:
+            _check(call(M, r, dX, dA, dB, ws, st), where)
+    return dX, dA, dB
+
+
+def qlora_linear_bwd_act8(dY, X8, U, W, A, B, s, dx_dtype=DTYPE_BF16, dX=None, dA=None, dB=None, ws=None,
+                          status=None, stream=None):
+    """:func:`qlora_linear_bwd` with the input as its 8-bit checkpoint ``X8``;
+    returns ``(dX, dA, dB)``."""
+    def call(M, r, dX, dA, dB, ws, st):
+        return _lib.qlora_linear_bwd_act8(_ptr(dY), _ptr(X8[0]), _ptr(X8[1]), _ptr(U), M, _weight(W), _ptr(A),
+                                          _ptr(B), r, float(s), _ptr(dX), dx_dtype, _ptr(dA), _ptr(dB), _ptr(ws),
+                                          ws.numel(), _ptr(status), st)
+    return _bwd_act8("qlora_linear_bwd_act8", dY, X8, U, W, 1, A, B, dx_dtype, dX, dA, dB,
+                     qlora_bwd_workspace_size, ws, status, stream, call)
+
+
+def qlora_group_bwd_act8(dY, X8, U, W, n_member, A, B, s, dx_dtype=DTYPE_BF16, dX=None, dA=None, dB=None, ws=None,
+                         status=None, stream=None):
+    """:func:`qlora_group_bwd` with the shared input as its 8-bit checkpoint ``X8``."""
+    G, arr = _members(n_member)
+
+    def size(M, N, K, r):
+        return qlora_group_bwd_workspace_size(M, N, K, G, r)
+
+    def call(M, r, dX, dA, dB, ws, st):
+        return _lib.qlora_group_bwd_act8(_ptr(dY), _ptr(X8[0]), _ptr(X8[1]), _ptr(U), M, _weight(W), G,
+                                         ctypes.cast(arr, _P), _ptr(A), _ptr(B), r, float(s), _ptr(dX), dx_dtype,
+                                         _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _ptr(status), st)
+    return _bwd_act8("qlora_group_bwd_act8", dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, size, ws, status, stream,
+                     call)
+
+
+def qlora_linear_bwd_dropout_act8(dY, X8_drop, U, W, A, B, s, p, seed, dx_dtype=DTYPE_BF16, dX=None, dA=None,
+                                  dB=None, ws=None, status=None, stream=None):
+    """:func:`qlora_linear_bwd_dropout` with X_drop as its 8-bit checkpoint (same
+    ``p`` and ``seed`` as the forward)."""
+    def call(M, r, dX, dA, dB, ws, st):
+        return _lib.qlora_linear_bwd_dropout_act8(_ptr(dY), _ptr(X8_drop[0]), _ptr(X8_drop[1]), _ptr(U), M,
+                                                  _weight(W), _ptr(A), _ptr(B), r, float(s), float(p), int(seed),
+                                                  _ptr(dX), dx_dtype, _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(),
+                                                  _ptr(status), st)
+    return _bwd_act8("qlora_linear_bwd_dropout_act8", dY, X8_drop, U, W, 1, A, B, dx_dtype, dX, dA, dB,
+                     qlora_bwd_dropout_workspace_size, ws, status, stream, call)
+
+
+# ------------------------------------------------------------------ loss head
+# (include/qlora_train.h: softmax cross entropy in pieces of the vocabulary)
+
+
+class _Head(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("ld", ctypes.c_int64), ("codes", ctypes.c_void_p), ("c8", ctypes.c_void_p),
+                ("s2", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("vocab", ctypes.c_int64),
+                ("dim", ctypes.c_int64)]
+
+
+_lib.qlora_head_loss_workspace_size.argtypes = [_I64, _I64, _I64, _I32, _I32]
+_lib.qlora_head_loss_workspace_size.restype = _SZ
+_lib.qlora_head_loss_fwd.argtypes = [_P, _I64, _I64, _Head, _P, _I64, _P, _P, _P, _P, _SZ, _P, _P]
+_lib.qlora_head_loss_fwd.restype = ctypes.c_int
+_lib.qlora_head_loss_bwd.argtypes = [_P, _I64, _I64, _Head, _P, _I64, _P, _P, _P, _P, _I64, _P, _SZ, _P, _P]
+_lib.qlora_head_loss_bwd.restype = ctypes.c_int
+_lib.qlora_head_loss_step.argtypes = [_P, _I64, _I64, _Head, _P, _I64, _P, _F, _P, _P, _P, _P, _I64, _P, _SZ, _P, _P]
+_lib.qlora_head_loss_step.restype = ctypes.c_int
+
+EXPORTED_TRAIN = EXPORTED_TRAIN + ("qlora_head_loss_workspace_size", "qlora_head_loss_fwd", "qlora_head_loss_bwd",
+                                   "qlora_head_loss_step")
+
+HEAD_FWD, HEAD_BWD, HEAD_STEP = 0, 1, 2
+IGNORE_INDEX = -100
+
+
+def qlora_head_loss_workspace_size(T, vocab, dim, nf4, op):
+    """Workspace bytes of a loss-head call (``op`` one of HEAD_FWD, HEAD_BWD, HEAD_STEP)."""
+    return int(_lib.qlora_head_loss_workspace_size(T, vocab, dim, 1 if nf4 else 0, op))
+
+
+def _head(head, dev, where):
+    """(C struct, vocab, dim, nf4) of a bf16 matrix [vocab, dim] or an :class:`NF4Weight`."""
+    if isinstance(head, torch.Tensor):
+        V, D, ld = _rows(head, where, "head", dev=dev)
+        return _Head(head.data_ptr(), ld, None, None, None, None, V, D), V, D, False
+    V, D = int(head.n_out), int(head.k_in)
+    mean = getattr(head, "mean", None)
+    _need(head.codes.device == dev, ERR_SHAPE, where, f"head is on {head.codes.device}, not {dev}")
+    return _Head(None, 0, head.codes.data_ptr(), head.c8.data_ptr(), head.s2.data_ptr(),
+                 None if mean is None else mean.data_ptr(), V, D), V, D, True
+
+
+def _head_call(where, op, H, head, labels, ws, status):
+    T, D, ldh = _rows(H, where, "H")
+    dev = H.device
+    h, V, dim, nf4 = _head(head, dev, where)
+    _need(dim == D, ERR_SHAPE, where, f"H has {D} columns, the head {dim}")
+    _vector(labels, torch.int64, T, dev, where, "labels")
+    _status_word(status, dev, where)
+    size = qlora_head_loss_workspace_size(T, V, D, nf4, op) if ws is None else 0
+    return T, D, ldh, dev, h, size
+
+
+def _out(t, shape, dtype, dev, where, name):
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _tensor(t, dtype, shape, dev, where, name)
+
+
+def qlora_head_loss_fwd(H, head, labels, ignore_index=IGNORE_INDEX, loss=None, lse=None, stats=None, ws=None,
+                        status=None, stream=None):
+    """Cross entropy of ``H @ head.T`` against ``labels`` (int64 [T]) without the
+    logits; ``head`` is a bf16 matrix [vocab, dim] or an :class:`NF4Weight`.
+    Returns ``(loss [T], lse [T], stats [2])``: per-token losses (0 where the
+    label is ``ignore_index``), log-sum-exps (keep them for the backward), and
+    the mean over the tokens that count with their number."""
+    where = "qlora_head_loss_fwd"
+    T, D, ldh, dev, h, size = _head_call(where, HEAD_FWD, H, head, labels, ws, status)
+    with _On(dev, stream) as st:
+        loss = _out(loss, (T,), torch.float32, dev, where, "loss")
+        lse = _out(lse, (T,), torch.float32, dev, where, "lse")
+        stats = _out(stats, (2,), torch.float32, dev, where, "stats")
+        if ws is None:
+            ws = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+        _check(_lib.qlora_head_loss_fwd(_ptr(H), ldh, T, h, _ptr(labels), int(ignore_index), _ptr(loss), _ptr(lse),
+                                        _ptr(stats), _ptr(ws), ws.numel(), _ptr(status), st), where)
+    return loss, lse, stats
+
+
+def qlora_head_loss_bwd(H, head, labels, lse, dloss, stats=None, ignore_index=IGNORE_INDEX, dH=None, ws=None,
+                        status=None, stream=None):
+    """Gradient of the losses of :func:`qlora_head_loss_fwd` towards ``H`` (bf16
+    [T, dim]): ``dloss`` [T] holds the gradient of every token's loss, or, with
+    the forward's ``stats`` given, ``dloss`` [1] the gradient of the mean."""
+    where = "qlora_head_loss_bwd"
+    T, D, ldh, dev, h, size = _head_call(where, HEAD_BWD, H, head, labels, ws, status)
+    _vector(lse, torch.float32, T, dev, where, "lse")
+    _vector(dloss, torch.float32, T if stats is None else 1, dev, where, "dloss")
+    if stats is not None:
+        _vector(stats, torch.float32, 2, dev, where, "stats")
+    with _On(dev, stream) as st:
+        if dH is None:
+            dH, ldd = torch.empty((T, D), dtype=torch.bfloat16, device=dev), D
+        else:
+            ldd = _rows(dH, where, "dH", D, T, dev)[2]
+        if ws is None:
+            ws = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+        _check(_lib.qlora_head_loss_bwd(_ptr(H), ldh, T, h, _ptr(labels), int(ignore_index), _ptr(lse), _ptr(dloss),
+                                        _ptr(stats), _ptr(dH), ldd, _ptr(ws), ws.numel(), _ptr(status), st), where)
+    return dH
+
+
+def qlora_head_loss_step(H, head, labels, weight=None, scale=1.0, ignore_index=IGNORE_INDEX, loss=None, lse=None,
+                         stats=None, dH=None, ws=None, status=None, stream=None):
+    """The losses and their gradient in one call; returns ``(loss, lse, stats,
+    dH)``.  ``dH`` is the gradient of ``scale`` times the mean loss, or, with
+    ``weight`` (fp32 [T]), of ``scale * sum(weight * loss)``."""
+    where = "qlora_head_loss_step"
+    T, D, ldh, dev, h, size = _head_call(where, HEAD_STEP, H, head, labels, ws, status)
+    if weight is not None:
+        _vector(weight, torch.float32, T, dev, where, "weight")
+    with _On(dev, stream) as st:
+        loss = _out(loss, (T,), torch.float32, dev, where, "loss")
+        lse = _out(lse, (T,), torch.float32, dev, where, "lse")
+        stats = _out(stats, (2,), torch.float32, dev, where, "stats")
+        if dH is None:
+            dH, ldd = torch.empty((T, D), dtype=torch.bfloat16, device=dev), D
+        else:
+            ldd = _rows(dH, where, "dH", D, T, dev)[2]
+        if ws is None:
+            ws = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+        _check(_lib.qlora_head_loss_step(_ptr(H), ldh, T, h, _ptr(labels), int(ignore_index), _ptr(weight),
+                                         float(scale), _ptr(loss), _ptr(lse), _ptr(stats), _ptr(dH), ldd, _ptr(ws),
+                                         ws.numel(), _ptr(status), st), where)
+    return loss, lse, stats, dH

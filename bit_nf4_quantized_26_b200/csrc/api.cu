@@ -8,7 +8,7 @@
 #include <mutex>
 #include <vector>
 
-#include "kernels.h"
+#include "train.h"
 #include "../../include/qlora_optim.h"
 
 using namespace qnf4;
@@ -132,6 +132,12 @@ bool map_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, uint
                   swizzle_bytes);
 }
 
+// The same with a row stride of `ld` elements (a multiple of 8).
+bool map_bf16_ld(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, uint32_t box_cols,
+                 uint32_t box_rows) {
+  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cols, rows, ld * 2, box_cols, box_rows, 128);
+}
+
 bool map_u8(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, uint32_t box_cols, uint32_t box_rows,
             int swizzle_bytes = 0) {
   return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, cols, rows, cols, box_cols, box_rows, swizzle_bytes);
@@ -229,11 +235,13 @@ qlora_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLORA_OK : QLO
 
 enum KernelId {
   kKQuantize = 0, kKDequantize, kKDown, kKFusedFwd, kKFinishFwd, kKLowFwd, kKLowFinish, kKDU, kKDB, kKFusedDX,
-  kKDA, kKAdamW8, kKDropout, kKDropoutDx, kKCount
+  kKDA, kKAdamW8, kKDropout, kKDropoutDx, kKActQuantize, kKActDequantize, kKActDA, kKHeadLogits, kKHeadGrad,
+  kKHeadCombine, kKCount
 };
 const char* const kKernelNames[kKCount] = {
     "nf4_quantize", "nf4_dequantize", "lora_down", "fused_fwd", "finish_fwd", "lowm_fwd", "lowm_finish",
-    "lora_du", "lora_db", "fused_dx", "lora_da", "adamw8", "dropout", "dropout_dx"};
+    "lora_du", "lora_db", "fused_dx", "lora_da", "adamw8", "dropout", "dropout_dx", "act8_quantize",
+    "act8_dequantize", "act8_da", "head_logits", "head_grad", "head_combine"};
 
 struct ProfRecord {
   int id;
@@ -891,17 +899,24 @@ qlora_status qlora_linear_fwd(const uint16_t* X, int64_t M, nf4_weight W, const 
 // U [M, G r], A [G r, K], B [N, r], dA [G r, K], dB [N, r]; dX [M, K] is the
 // sum over the members.  With `drop`, the GEMM's adapter stages are left out:
 // dX's frozen-path term goes to an fp32 buffer after the caller's workspace
-// and a second pass adds keep * c * (dU A) and writes dX.
-static qlora_status linear_bwd_impl(const uint16_t* dY, const uint16_t* X, const float* U, int64_t M, nf4_weight W,
+// and a second pass adds keep * c * (dU A) and writes dX.  The adapter's input
+// is given as bf16 (`X.x`) or as its 8-bit checkpoint; only dA reads it.
+struct SavedInput {
+  const uint16_t* x;
+  const uint8_t* codes;
+  const uint8_t* exps;
+};
+
+static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, const float* U, int64_t M, nf4_weight W,
                                     const Group& grp, const uint16_t* A, const uint16_t* B, int32_t r, float s,
                                     void* dX, int32_t dx_dtype, float* dA, float* dB, void* ws, size_t ws_bytes,
                                     int32_t* d_status, void* stream, const DropoutArgs* drop) {
   if (qlora_status st = check_linear_shape(M, W, r)) return st;
   if (dx_dtype != QLORA_DTYPE_BF16 && dx_dtype != QLORA_DTYPE_F32) return QLORA_ERR_DTYPE;
   if (M == 0) return QLORA_OK;
-  if (!dY || !X || !U || !A || !B || !dX || !dA || !dB) return QLORA_ERR_NULL;
+  if (!dY || (!X.x && (!X.codes || !X.exps)) || !U || !A || !B || !dX || !dA || !dB) return QLORA_ERR_NULL;
   if (qlora_status st = check_weight_ptrs(W)) return st;
-  if (!aligned16(dY) || !aligned16(X) || !aligned16(U) || !aligned16(A) || !aligned16(B) || !aligned16(dX) ||
+  if (!aligned16(dY) || !aligned16(X.x) || !aligned16(X.codes) || !aligned16(X.exps) || !aligned16(U) || !aligned16(A) || !aligned16(B) || !aligned16(dX) ||
       !aligned16(dA) || !aligned16(dB) || (d_status && !aligned16(d_status)))
     return QLORA_ERR_ALIGN;
   const int64_t N = W.n_out, K = W.k_in;
@@ -1045,7 +1060,9 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const uint16_t* X, const
 
   // dA = dU^T X per member (contraction over M split over a cluster)
   CUtensorMap mduc, mx;
-  if (!map_bf16(&mduc, ducat, M, 2 * ra, 64, 64) || !map_bf16(&mx, X, M, K, 64, 64)) return QLORA_ERR_CUDA;
+  if (!map_bf16(&mduc, ducat, M, 2 * ra, 64, 64) ||
+      !(X.x ? map_bf16(&mx, X.x, M, K, 64, 64) : map_u8(&mx, X.codes, M, K, 128, 64)))
+    return QLORA_ERR_CUDA;
   {
     SkinnyArgs da = sa;
     da.stages_total = static_cast<int>(cdiv(M, 64));
@@ -1053,9 +1070,10 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const uint16_t* X, const
     da.s = 1.0f;
     da.out_f32 = dA;
     da.out_cat = nullptr;
-    ProfScope ps(kKDA, side);
-    if (qlora_status st = from_cuda(
-            launch_skinny(kSkDA, mduc, mx, da, static_cast<int>(cdiv(K, 128)) * Gs, p.s_da, side)))
+    const int rows = static_cast<int>(cdiv(K, 128)) * Gs;
+    ProfScope ps(X.x ? kKDA : kKActDA, side);
+    if (qlora_status st = from_cuda(X.x ? launch_skinny(kSkDA, mduc, mx, da, rows, p.s_da, side)
+                                        : launch_act8_da(mduc, mx, X.exps, da, rows, p.s_da, side)))
       return st;
   }
 
@@ -1065,7 +1083,7 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const uint16_t* X, const
 qlora_status qlora_linear_bwd(const uint16_t* dY, const uint16_t* X, const float* U, int64_t M, nf4_weight W,
                               const uint16_t* A, const uint16_t* B, int32_t r, float s, void* dX, int32_t dx_dtype,
                               float* dA, float* dB, void* ws, size_t ws_bytes, int32_t* d_status, void* stream) {
-  return linear_bwd_impl(dY, X, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes,
+  return linear_bwd_impl(dY, {X, nullptr, nullptr}, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes,
                          d_status, stream, nullptr);
 }
 
@@ -1099,7 +1117,7 @@ qlora_status qlora_group_bwd(const uint16_t* dY, const uint16_t* X, const float*
   if (members > 1 && r > kChunkRank) return QLORA_ERR_SHAPE;  // members' ranks are at most 64
   Group grp;
   if (qlora_status st = make_group(members, n_member, W.n_out, &grp)) return st;
-  return linear_bwd_impl(dY, X, U, M, W, grp, A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes, d_status, stream,
+  return linear_bwd_impl(dY, {X, nullptr, nullptr}, U, M, W, grp, A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes, d_status, stream,
                          nullptr);
 }
 
@@ -1165,7 +1183,7 @@ qlora_status qlora_linear_bwd_dropout(const uint16_t* dY, const uint16_t* X_drop
                                       size_t ws_bytes, int32_t* d_status, void* stream) {
   DropoutArgs d{};
   if (!dropout_args(p, seed, &d)) return QLORA_ERR_SHAPE;
-  return linear_bwd_impl(dY, X_drop, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes,
+  return linear_bwd_impl(dY, {X_drop, nullptr, nullptr}, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes,
                          d_status, stream, &d);
 }
 
@@ -1237,6 +1255,360 @@ qlora_status qlora_paged_prefetch(const void* ptr, size_t bytes, int32_t to_host
 qlora_status qlora_paged_free(void* ptr) {
   if (!ptr) return QLORA_OK;
   return from_cuda(cudaFree(ptr));
+}
+
+// ------------------------------------------------ 8-bit activation checkpoints
+
+static qlora_status check_act8(int64_t M, int64_t K, int64_t ldx) {
+  if (M < 0 || M >= (int64_t(1) << 31) || K < 64 || K % 64 != 0 || K >= (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
+  if (M * K >= (int64_t(1) << 40) || ldx < K || ldx % 8 != 0 || ldx >= (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+qlora_status act8_quantize(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, uint8_t* codes, uint8_t* exps,
+                           int32_t* d_status, void* stream) {
+  if (qlora_status st = check_act8(M, K, ldx)) return st;
+  if (M == 0) return QLORA_OK;
+  if (!X || !codes || !exps) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(exps) || (d_status && !aligned16(d_status)))
+    return QLORA_ERR_ALIGN;
+  if (qlora_status st = check_device()) return st;
+  ProfScope ps(kKActQuantize, static_cast<cudaStream_t>(stream));
+  return from_cuda(launch_act8_quantize(X, M, K, ldx, codes, exps, d_status, static_cast<cudaStream_t>(stream)));
+}
+
+qlora_status act8_dequantize(const uint8_t* codes, const uint8_t* exps, int64_t M, int64_t K, uint16_t* X, int64_t ldx,
+                             void* stream) {
+  if (qlora_status st = check_act8(M, K, ldx)) return st;
+  if (M == 0) return QLORA_OK;
+  if (!X || !codes || !exps) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(exps)) return QLORA_ERR_ALIGN;
+  if (qlora_status st = check_device()) return st;
+  ProfScope ps(kKActDequantize, static_cast<cudaStream_t>(stream));
+  return from_cuda(launch_act8_dequantize(codes, exps, M, K, X, ldx, static_cast<cudaStream_t>(stream)));
+}
+
+qlora_status qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* codes, const uint8_t* exps, const float* U,
+                                   int64_t M, nf4_weight W, const uint16_t* A, const uint16_t* B, int32_t r, float s,
+                                   void* dX, int32_t dx_dtype, float* dA, float* dB, void* ws, size_t ws_bytes,
+                                   int32_t* d_status, void* stream) {
+  return linear_bwd_impl(dY, {nullptr, codes, exps}, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA, dB,
+                         ws, ws_bytes, d_status, stream, nullptr);
+}
+
+qlora_status qlora_group_bwd_act8(const uint16_t* dY, const uint8_t* codes, const uint8_t* exps, const float* U,
+                                  int64_t M, nf4_weight W, int32_t members, const int64_t* n_member, const uint16_t* A,
+                                  const uint16_t* B, int32_t r, float s, void* dX, int32_t dx_dtype, float* dA,
+                                  float* dB, void* ws, size_t ws_bytes, int32_t* d_status, void* stream) {
+  if (qlora_status st = check_linear_shape(M, W, r)) return st;
+  if (members > 1 && r > kChunkRank) return QLORA_ERR_SHAPE;  // members' ranks are at most 64
+  Group grp;
+  if (qlora_status st = make_group(members, n_member, W.n_out, &grp)) return st;
+  return linear_bwd_impl(dY, {nullptr, codes, exps}, U, M, W, grp, A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes,
+                         d_status, stream, nullptr);
+}
+
+qlora_status qlora_linear_bwd_dropout_act8(const uint16_t* dY, const uint8_t* codes, const uint8_t* exps,
+                                           const float* U, int64_t M, nf4_weight W, const uint16_t* A,
+                                           const uint16_t* B, int32_t r, float s, float p, uint64_t seed, void* dX,
+                                           int32_t dx_dtype, float* dA, float* dB, void* ws, size_t ws_bytes,
+                                           int32_t* d_status, void* stream) {
+  DropoutArgs d{};
+  if (!dropout_args(p, seed, &d)) return QLORA_ERR_SHAPE;
+  return linear_bwd_impl(dY, {nullptr, codes, exps}, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA, dB,
+                         ws, ws_bytes, d_status, stream, &d);
+}
+
+// ------------------------------------------------------------------ loss head
+
+// How a call walks the vocabulary, and its workspace.  The backward and the
+// step hold a piece's bf16 [T, piece] operand: about 2^26 elements (128 MB,
+// near the L2's size, and deep enough a contraction that reading and writing
+// the fp32 sum of dH between pieces stays well below its products' time), but
+// at least 2048 columns.  An NF4 head is dequantised a piece at a time: at
+// most 2^26 elements.  A forward over a bf16 head has one piece.
+struct HeadPlanHost {
+  int64_t piece = 0;  // vocabulary rows per piece (a multiple of the tile)
+  int64_t pieces = 0;
+  size_t off_cnt = 0, off_z = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_sum = 0, off_pl = 0;
+  size_t off_g = 0, off_acc = 0, off_w = 0, total = 0;
+};
+
+static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op) {
+  HeadPlanHost p;
+  const int64_t tile = kHeadTile;
+  const int64_t vt = cdiv(V, tile), mt = cdiv(T, tile);
+  int64_t piece = vt * tile;
+  if (op != QLORA_HEAD_FWD) {
+    const int64_t fit = (int64_t(1) << 26) / (mt * tile) / tile * tile;
+    piece = std::min(piece, std::max<int64_t>(fit, 2048));
+  }
+  if (nf4) {
+    const int64_t fit = (int64_t(1) << 26) / D / tile * tile;
+    piece = std::min(piece, std::max<int64_t>(fit, 2048));
+  }
+  p.pieces = cdiv(vt * tile, piece);
+  p.piece = cdiv(vt, p.pieces) * tile;  // even pieces
+  p.pieces = cdiv(vt * tile, p.piece);
+  size_t off = 0;
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  const size_t t = static_cast<size_t>(T);
+  if (op != QLORA_HEAD_BWD) {
+    const int64_t part_tiles = op == QLORA_HEAD_FWD ? vt : p.piece / tile;
+    p.off_cnt = take(8);
+    p.off_z = take(4 * t);
+    p.off_part = take(8 * t * static_cast<size_t>(part_tiles));
+    p.off_bsum = take(8 * static_cast<size_t>(head_combine_blocks(T)));
+  }
+  if (op == QLORA_HEAD_STEP) {
+    p.off_run = take(8 * t);
+    p.off_alpha = take(4 * t);
+    p.off_sum = take(4 * t);
+    p.off_pl = take(4 * t);
+  }
+  if (op != QLORA_HEAD_FWD) {
+    p.off_g = take(2 * t * static_cast<size_t>(p.piece));
+    if (p.pieces > 1) p.off_acc = take(4 * static_cast<size_t>(mt * tile) * static_cast<size_t>(cdiv(D, tile) * tile));
+  }
+  if (nf4) p.off_w = take(2 * static_cast<size_t>(std::min(p.piece, V)) * static_cast<size_t>(D));
+  p.total = off;
+  return p;
+}
+
+static qlora_status check_head_shape(int64_t T, int64_t V, int64_t D, bool nf4) {
+  const int64_t big = int64_t(1) << 31;
+  if (T < 0 || T >= big - kHeadTile || V < 1 || V >= big - kHeadTile) return QLORA_ERR_SHAPE;
+  if (D < 8 || D > (int64_t(1) << 20) || D % (nf4 ? 64 : 8) != 0 || V * D >= (int64_t(1) << 40)) return QLORA_ERR_SHAPE;
+  // tiles of every product are counted in 32 bits
+  if (cdiv(T, kHeadTile) * cdiv(std::max(V, D), kHeadTile) >= big / 64) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+size_t qlora_head_loss_workspace_size(int64_t T, int64_t vocab, int64_t dim, int32_t nf4, int32_t op) {
+  if (T <= 0 || op < QLORA_HEAD_FWD || op > QLORA_HEAD_STEP || check_head_shape(T, vocab, dim, nf4 != 0)) return 0;
+  return plan_head(T, vocab, dim, nf4 != 0, op).total;
+}
+
+struct HeadCall {
+  const uint16_t* H;
+  int64_t ldh, T;
+  qlora_head head;
+  const int64_t* labels;
+  int64_t ignore;
+  float* loss;
+  float* lse;          // written by the forward and the step
+  const float* lse_in; // read by the backward
+  float* stats;
+  const float* stats_in;
+  const float* dloss;
+  const float* weight;
+  float scale;
+  uint16_t* dH;
+  int64_t lddh;
+};
+
+static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t ws_bytes, int32_t* d_status,
+                                   void* stream) {
+  const qlora_head& hd = c.head;
+  const bool nf4 = hd.w == nullptr;
+  const int64_t T = c.T, V = hd.vocab, D = hd.dim;
+  const int64_t big = int64_t(1) << 31;
+  if (qlora_status st = check_head_shape(T, V, D, nf4)) return st;
+  if (c.ldh < D || c.ldh % 8 != 0 || c.ldh >= big) return QLORA_ERR_SHAPE;
+  if (!nf4 && (hd.ld < D || hd.ld % 8 != 0 || hd.ld >= big)) return QLORA_ERR_SHAPE;
+  if (op != QLORA_HEAD_FWD && (c.lddh < D || c.lddh % 8 != 0 || c.lddh >= big)) return QLORA_ERR_SHAPE;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (op == QLORA_HEAD_BWD) return QLORA_OK;
+    if (!c.stats) return QLORA_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(c.stats) & 3u) return QLORA_ERR_ALIGN;
+    if (qlora_status st = check_device()) return st;
+    return from_cuda(cudaMemsetAsync(c.stats, 0, 2 * sizeof(float), cs));
+  }
+  if (!c.H || !c.labels || (nf4 && (!hd.codes || !hd.c8 || !hd.s2))) return QLORA_ERR_NULL;
+  if (op == QLORA_HEAD_BWD ? (!c.lse_in || !c.dloss) : (!c.loss || !c.lse || !c.stats)) return QLORA_ERR_NULL;
+  if (op != QLORA_HEAD_FWD && !c.dH) return QLORA_ERR_NULL;
+  const void* wide[] = {c.H, hd.w, hd.codes, hd.c8, hd.s2, hd.mean, c.dH, d_status};
+  for (const void* q : wide)
+    if (!aligned16(q)) return QLORA_ERR_ALIGN;
+  // per-token vectors are read a word at a time: a shifted view is fine
+  const void* vec[] = {c.loss, c.lse, c.lse_in, c.stats, c.stats_in, c.dloss, c.weight};
+  for (const void* q : vec)
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return QLORA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(c.labels) & 7u) return QLORA_ERR_ALIGN;
+  const HeadPlanHost p = plan_head(T, V, D, nf4, op);
+  if (!ws || ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (qlora_status st = check_device()) return st;
+
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  auto at = [wsb](size_t off) { return wsb + off; };
+  uint16_t* g = reinterpret_cast<uint16_t*>(at(p.off_g));
+  uint16_t* wbuf = reinterpret_cast<uint16_t*>(at(p.off_w));
+
+  HeadArgs a{};
+  a.T = static_cast<int>(T);
+  a.vocab = V;
+  a.mtiles = static_cast<int>(cdiv(T, kHeadTile));
+  a.labels = c.labels;
+  a.ignore = c.ignore;
+  a.g = g;
+  a.ldg = p.piece;
+  a.lse = c.lse_in;
+  a.status = d_status;
+  a.tab = tables();
+  a.head = hd;
+  HeadCombineArgs cb{};
+  if (op != QLORA_HEAD_BWD) {
+    a.label_logit = reinterpret_cast<float*>(at(p.off_z));
+    a.zero = reinterpret_cast<uint32_t*>(at(p.off_cnt));
+    a.zero_count = 2;
+    cb.T = a.T;
+    cb.label_logit = a.label_logit;
+    cb.labels = c.labels;
+    cb.ignore = c.ignore;
+    cb.vocab = V;
+    cb.counters = reinterpret_cast<int32_t*>(at(p.off_cnt));
+    cb.block_sum = reinterpret_cast<double*>(at(p.off_bsum));
+    cb.part = reinterpret_cast<const float2*>(at(p.off_part));
+    cb.loss = c.loss;
+    cb.lse = c.lse;
+    cb.stats = c.stats;
+    cb.status = d_status;
+  }
+
+  CUtensorMap mh, mg, mw, mwt;
+  if (!map_bf16_ld(&mh, c.H, T, D, c.ldh, 64, 128)) return QLORA_ERR_CUDA;
+  if (op != QLORA_HEAD_FWD && !map_bf16_ld(&mg, g, T, p.piece, p.piece, 64, 128)) return QLORA_ERR_CUDA;
+  if (!nf4 && (!map_bf16_ld(&mw, hd.w, V, D, hd.ld, 64, 128) || !map_bf16_ld(&mwt, hd.w, V, D, hd.ld, 64, 64)))
+    return QLORA_ERR_CUDA;
+
+  for (int64_t i = 0; i < p.pieces; ++i) {
+    const int64_t v0 = i * p.piece, pv = std::min(p.piece, V - v0);
+    const bool first = i == 0, last = i == p.pieces - 1;
+    if (nf4) {  // v0 * D is a whole number of double-quantisation groups: v0 % 256 == 0, D % 64 == 0
+      const int64_t e0 = v0 * D;
+      CUtensorMap out;
+      if (!map_bf16(&out, wbuf, pv * D / 64, 64, 64, 32, 128) || !map_bf16_ld(&mw, wbuf, pv, D, D, 64, 128) ||
+          !map_bf16_ld(&mwt, wbuf, pv, D, D, 64, 64))
+        return QLORA_ERR_CUDA;
+      ProfScope ps(kKDequantize, cs);
+      if (qlora_status st = from_cuda(launch_nf4_dequantize(hd.codes + e0 / 2, hd.c8 + e0 / 64, hd.s2 + e0 / 16384,
+                                                            hd.mean, pv * D, wbuf, &out, tables(), cs)))
+        return st;
+    }
+    a.b_row0 = nf4 ? 0 : static_cast<int>(v0);
+    a.v0 = v0;
+    a.ncols = static_cast<int>(pv);
+    a.ntiles = static_cast<int>(cdiv(pv, kHeadTile));
+    a.kst = static_cast<int>(cdiv(D, 64));
+    float2* part = reinterpret_cast<float2*>(at(p.off_part));
+    a.part = op == QLORA_HEAD_FWD ? part + v0 / kHeadTile * T : part;
+    {
+      const int mode = op == QLORA_HEAD_FWD ? kHeadLoss : op == QLORA_HEAD_BWD ? kHeadProb : kHeadExp;
+      ProfScope ps(kKHeadLogits, cs);
+      if (qlora_status st = from_cuda(launch_head_gemm(mode, mh, mw, a, cs))) return st;
+    }
+    if (op == QLORA_HEAD_STEP || (op == QLORA_HEAD_FWD && last)) {
+      cb.ntiles = op == QLORA_HEAD_FWD ? static_cast<int>(cdiv(V, kHeadTile)) : a.ntiles;
+      cb.first = op == QLORA_HEAD_FWD || first;
+      cb.last = last;
+      if (op == QLORA_HEAD_STEP) {
+        cb.run = reinterpret_cast<float2*>(at(p.off_run));
+        cb.alpha = reinterpret_cast<float*>(at(p.off_alpha));
+        cb.row_sum = reinterpret_cast<float*>(at(p.off_sum));
+        cb.p_label = reinterpret_cast<float*>(at(p.off_pl));
+        cb.e = g;
+        cb.lde = p.piece;
+      }
+      ProfScope ps(kKHeadCombine, cs);
+      if (qlora_status st = from_cuda(launch_head_combine(cb, cs))) return st;
+    }
+    if (op != QLORA_HEAD_FWD) {
+      HeadArgs d = a;
+      d.ncols = static_cast<int>(D);
+      d.ntiles = static_cast<int>(cdiv(D, kHeadTile));
+      d.kst = static_cast<int>(cdiv(pv, 64));
+      d.first = first;
+      d.last = last;
+      d.acc = reinterpret_cast<float*>(at(p.off_acc));
+      d.dh = c.dH;
+      d.ldd = c.lddh;
+      d.dloss = c.dloss;
+      d.stats = c.stats_in;
+      if (op == QLORA_HEAD_STEP) {
+        d.alpha = cb.alpha;
+        d.row_sum = cb.row_sum;
+        d.p_label = cb.p_label;
+        d.weight = c.weight;
+        d.scale = c.scale;
+        d.count = cb.counters;
+      }
+      ProfScope ps(kKHeadGrad, cs);
+      if (qlora_status st = from_cuda(launch_head_gemm(kHeadGrad, mg, mwt, d, cs))) return st;
+    }
+  }
+  return QLORA_OK;
+}
+
+qlora_status qlora_head_loss_fwd(const uint16_t* H, int64_t ldh, int64_t T, qlora_head head, const int64_t* labels,
+                                 int64_t ignore_index, float* loss, float* lse, float* stats, void* ws,
+                                 size_t ws_bytes, int32_t* d_status, void* stream) {
+  HeadCall c{};
+  c.H = H;
+  c.ldh = ldh;
+  c.T = T;
+  c.head = head;
+  c.labels = labels;
+  c.ignore = ignore_index;
+  c.loss = loss;
+  c.lse = lse;
+  c.stats = stats;
+  return head_loss_impl(QLORA_HEAD_FWD, c, ws, ws_bytes, d_status, stream);
+}
+
+qlora_status qlora_head_loss_bwd(const uint16_t* H, int64_t ldh, int64_t T, qlora_head head, const int64_t* labels,
+                                 int64_t ignore_index, const float* lse, const float* dloss, const float* stats,
+                                 uint16_t* dH, int64_t lddh, void* ws, size_t ws_bytes, int32_t* d_status,
+                                 void* stream) {
+  HeadCall c{};
+  c.H = H;
+  c.ldh = ldh;
+  c.T = T;
+  c.head = head;
+  c.labels = labels;
+  c.ignore = ignore_index;
+  c.lse_in = lse;
+  c.dloss = dloss;
+  c.stats_in = stats;
+  c.dH = dH;
+  c.lddh = lddh;
+  return head_loss_impl(QLORA_HEAD_BWD, c, ws, ws_bytes, d_status, stream);
+}
+
+qlora_status qlora_head_loss_step(const uint16_t* H, int64_t ldh, int64_t T, qlora_head head, const int64_t* labels,
+                                  int64_t ignore_index, const float* weight, float scale, float* loss, float* lse,
+                                  float* stats, uint16_t* dH, int64_t lddh, void* ws, size_t ws_bytes,
+                                  int32_t* d_status, void* stream) {
+  HeadCall c{};
+  c.H = H;
+  c.ldh = ldh;
+  c.T = T;
+  c.head = head;
+  c.labels = labels;
+  c.ignore = ignore_index;
+  c.weight = weight;
+  c.scale = scale;
+  c.loss = loss;
+  c.lse = lse;
+  c.stats = stats;
+  c.dH = dH;
+  c.lddh = lddh;
+  return head_loss_impl(QLORA_HEAD_STEP, c, ws, ws_bytes, d_status, stream);
 }
 
 }  // extern "C"

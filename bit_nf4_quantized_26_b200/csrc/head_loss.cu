@@ -1,0 +1,614 @@
+// head_loss.cu — softmax cross entropy of the head's logits and its gradient
+// towards the hidden states, in pieces of the vocabulary ("QLoRA" encyclopedia
+// entry, tonho.wtf, section "a ideia": the base is frozen and the gradient
+// crosses it into the adapters).
+//
+//   l = H W^T    lse = log sum exp l    loss = lse - l[label]
+//   dH = g (exp(l - lse) - onehot) W
+//
+// The logits exist only as 256 x 256 fp32 tiles in tensor memory.  One GEMM
+// kernel on CTA pairs makes every product; what its epilogue does with a tile
+// is the mode:
+//
+//   Loss  per row and tile the maximum m and sum exp(l - m): 8 bytes per 256 logits
+//   Prob  exp(l - lse), less 1 at the label (in fp32), rounded to bf16
+//   Exp   exp(l - ref), 0 at the label, rounded to bf16, and (ref, sum): the
+//         gradient's operand before lse is known.  ref is 0 while the tile's
+//         maximum lies within +-40 (exp then stays far inside bf16's and
+//         fp32's range, and the reference costs no precision: both types
+//         float), else that maximum
+//   Grad  (second product) the piece's bf16 [T, piece] operand times W's rows
+//         of the piece, added to the fp32 sum of the pieces before
+//
+// The step joins each piece's (ref, sum) per row (head_combine_kernel); rows
+// whose tiles took different references have those tiles' exponentials
+// rescaled to a common one, and `alpha` rescales the sum of earlier pieces:
+// both leave ordinary rows alone.  The label's column is left out of Exp and
+// added after the last piece in fp32, (p_label - 1) W[label] with p_label - 1 =
+// expm1(l_label - lse): rounding p to bf16 first would lose the gradient of a
+// well-predicted token.
+#include <algorithm>
+
+#include "train.h"
+
+namespace qnf4 {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRefRange = 40.0f;  // tile maxima within +-kRefRange share the reference 0
+
+struct HeadPlan {
+  static constexpr uint32_t kA = 16384;  // 128 tokens x 64
+  static constexpr uint32_t kB = 16384;  // 128 columns x 64
+  static constexpr uint32_t kStage = kA + kB;
+  static constexpr uint32_t kStages = 6;
+  static constexpr uint32_t kBarOff = kStages * kStage;
+  static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
+  static_assert(kSmem <= 232448u, "too much shared memory");
+};
+
+// Warp 0: copies; warp 1: MMAs (leader CTA); warps 2..5: epilogue.
+constexpr int kHeadThreads = 192;
+constexpr int kEpiWarps = 4;
+constexpr int kGroupM = 8;  // token tiles walked together (raster)
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Tile order: groups of kGroupM token tiles, tokens first within a group, so
+// the pairs at work share a few panels of each operand in L2.
+__device__ __forceinline__ void head_tile(int tile, int mtiles, int ntiles, int& m, int& n) {
+  const int per = kGroupM * ntiles;
+  const int grp = tile / per, rem = tile - grp * per;
+  const int gsz = min(kGroupM, mtiles - grp * kGroupM);
+  n = rem / gsz;
+  m = grp * kGroupM + rem - n * gsz;
+}
+
+__device__ __forceinline__ bool counts(int64_t label, int64_t ignore, int64_t vocab) {
+  return label != ignore && label >= 0 && label < vocab;
+}
+
+// 32 columns of the accumulator, fp32 bits; columns >= nv become -inf.
+__device__ __forceinline__ void load_logits(uint32_t taddr, int nv, float (&l)[32]) {
+  uint32_t v[32];
+  tmem_ld_32x32b_x32(taddr, v);
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < 32; ++j) l[j] = __uint_as_float(v[j]);
+  if (nv < 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j >= nv) l[j] = -INFINITY;
+  }
+}
+
+__device__ __forceinline__ float max32(const float (&l)[32]) {
+  float m[4] = {l[0], l[1], l[2], l[3]};
+#pragma unroll
+  for (int j = 4; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], l[j]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// 32 bf16 (64 bytes, 16-byte aligned) from fp32; `n` valid (a multiple of 8).
+__device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32], int n) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (8 * j < n)
+      reinterpret_cast<uint4*>(dst)[j] =
+          make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                     pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+}
+
+// Columns d .. d + 31 of row `row` of the head as fp32 (`n` valid, a multiple of 8).
+__device__ __forceinline__ void load_head_row(const qlora_head& h, const Nf4Tables& tab, int64_t row, int d, int n,
+                                              float (&w)[32]) {
+  uint4 v[4];
+  if (h.w) {
+    const uint4* src = reinterpret_cast<const uint4*>(h.w + row * h.ld + d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = 8 * j < n ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+  } else {  // half of a 64-element block
+    const int64_t e = row * h.dim + d, b = e >> 6;
+    const float chat = nf4_block_scale(__ldg(h.c8 + b), __ldg(h.s2 + (b >> 8)), nf4_load_mean(h.mean));
+    const Nf4Lut lut = nf4_make_lut(tab, chat);
+    const uint4 c = __ldg(reinterpret_cast<const uint4*>(h.codes + (e >> 1)));
+    v[0] = nf4_lookup8(c.x, lut);
+    v[1] = nf4_lookup8(c.y, lut);
+    v[2] = nf4_lookup8(c.z, lut);
+    v[3] = nf4_lookup8(c.w, lut);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[8 * j + 2 * i] = __uint_as_float(u[i] << 16);
+      w[8 * j + 2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+}  // namespace
+
+// A cluster of two CTAs computes 256 tokens x 256 columns per tile: each CTA
+// holds 128 token rows (A) and half of the columns (B) of a 64-deep stage, one
+// thread of the leader issues M = 256, N = 256 MMAs, and each CTA's tensor
+// memory gets its 128 rows.  Two accumulators: the epilogue of a tile runs
+// beside the next tile's MMAs.  Persistent: one pair per TPC.
+//
+// Barriers: full[s] (leader: both CTAs' tiles landed), empty[s] (both: the
+// stage's MMAs are done), accf[b] (both: accumulator final), acce[b] (leader:
+// all epilogue warps of both CTAs have read it), done (leader: the last
+// commit).  What an earlier kernel of the same call wrote is read past L1
+// (__ldcg): launches overlap, and nothing is kept there from one to the next.
+template <int MODE>
+__global__ void __launch_bounds__(kHeadThreads, 1)
+    head_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ HeadArgs a) {
+  using P = HeadPlan;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBarOff);
+  uint64_t* empty = full + P::kStages;
+  uint64_t* accf = empty + P::kStages;
+  uint64_t* acce = accf + 2;
+  uint64_t* done = acce + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles = a.mtiles * a.ntiles;
+
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < P::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], 2 * kEpiWarps);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_d = *tmem_slot;
+  const WaitCtx wc{abort_flag, a.status};
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if ((MODE == kHeadLoss || MODE == kHeadExp) && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.zero_count; i += blockDim.x) a.zero[i] = 0u;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int64_t it = 0;  // stages issued
+      bool ok = true;
+      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+        int m, n;
+        head_tile(tile, a.mtiles, a.ntiles, m, n);
+        const int arow = m * kHeadTile + static_cast<int>(rank) * 128;
+        const int bcol = n * kHeadTile + static_cast<int>(rank) * 128;
+        for (int kt = 0; kt < a.kst; ++kt, ++it) {
+          const uint32_t s = static_cast<uint32_t>(it % P::kStages);
+          const uint32_t u = static_cast<uint32_t>(it / P::kStages);
+          if (it >= P::kStages && !mbar_wait(&empty[s], (u - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * P::kStage;
+          const uint32_t full0 = dsmem_addr(&full[s], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * P::kStage);
+          tma_load_2d_pair(st, &tm_a, full0, kt * 64, arow);
+          if (MODE == kHeadGrad) {  // W's rows are the contraction: two 64-column atoms
+            tma_load_2d_pair(st + P::kA, &tm_b, full0, bcol, a.b_row0 + kt * 64);
+            tma_load_2d_pair(st + P::kA + 8192, &tm_b, full0, bcol + 64, a.b_row0 + kt * 64);
+          } else {
+            tma_load_2d_pair(st + P::kA, &tm_b, full0, kt * 64, a.b_row0 + bcol);
+          }
+        }
+      }
+      if (rank == 0)
+        for (int64_t t = it > P::kStages ? it - P::kStages : 0; t < it; ++t)
+          mbar_drain(&full[t % P::kStages], static_cast<uint32_t>(t / P::kStages) & 1, a.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA (leader)
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, 0, MODE == kHeadGrad ? 1 : 0);
+      constexpr uint32_t b_step = MODE == kHeadGrad ? (2048u >> 4) : (32u >> 4);
+      int64_t it = 0;
+      int acc = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < tiles; tile += pairs, ++acc) {
+        const int buf = acc & 1;
+        if (acc >= 2 && !mbar_wait_all(&acce[buf], ((acc >> 1) - 1) & 1, wc)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_d + buf * 256;
+        for (int kt = 0; kt < a.kst; ++kt, ++it) {
+          const uint32_t s = static_cast<uint32_t>(it % P::kStages);
+          if (!mbar_wait_all(&full[s], static_cast<uint32_t>(it / P::kStages) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + s * P::kStage);
+          const uint64_t ad = sdesc_sw128(sa, 16, 1024);
+          const uint64_t bd = MODE == kHeadGrad ? sdesc_sw128(sa + P::kA, 8192, 1024)
+                                                : sdesc_sw128(sa + P::kA, 16, 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (uint32_t kk = 0; kk < 4; ++kk)
+              umma_bf16_pair(d, ad + kk * 2, bd + kk * b_step, idesc, (kt | static_cast<int>(kk)) != 0 ? 1u : 0u);
+            umma_commit_pair(&empty[s], 0x3);
+            if (kt == a.kst - 1) umma_commit_pair(&accf[buf], 0x3);
+          }
+          __syncwarp();
+        }
+      }
+      if (elect_one()) {
+        umma_commit_pair(done, 0x1);
+        mbar_drain(done, 0, a.status);  // nothing of the pair is in flight when the tensor memory is freed
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // TMEM lanes 32 q ..
+    const int et = threadIdx.x - 64;
+    const uint32_t tq = tmem_d + (static_cast<uint32_t>(q * 32) << 16);
+    int acc = 0;
+    for (int tile = pair; tile < tiles; tile += pairs, ++acc) {
+      int m, n;
+      head_tile(tile, a.mtiles, a.ntiles, m, n);
+      const int buf = acc & 1;
+      const int t = m * kHeadTile + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const bool rok = t < a.T;
+      const int n0 = n * kHeadTile;
+      const int nv = min(kHeadTile, a.ncols - n0);  // columns of the tile
+      const uint32_t tb = tq + buf * 256;
+      int64_t label = -1;
+      bool counted = false;
+      if (rok && a.labels) {
+        label = __ldg(a.labels + t);
+        counted = counts(label, a.ignore, a.vocab);
+      }
+      // the label's column of this tile, or none
+      const int64_t lc = MODE != kHeadGrad && counted ? label - a.v0 - n0 : -1;
+
+      if (!mbar_wait_warp(&accf[buf], (acc >> 1) & 1, wc)) break;
+      tc_fence_after();
+
+      if (MODE == kHeadLoss) {
+        float mx = -INFINITY, s = 0.0f, z = 0.0f;
+        for (int cb = 0; cb * 32 < nv; ++cb) {
+          float l[32];
+          load_logits(tb + cb * 32, nv - cb * 32, l);
+          const float cm = max32(l);
+          if (cm > mx) {
+            s *= exp2_fast((mx - cm) * kLog2e);
+            mx = cm;
+          }
+          const float base = mx == -INFINITY ? 0.0f : mx * kLog2e;
+          float p[4] = {};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) p[j & 3] += exp2_fast(fmaf(l[j], kLog2e, -base));
+          s += (p[0] + p[1]) + (p[2] + p[3]);
+          const int lj = (lc >> 5) == cb ? static_cast<int>(lc & 31) : -1;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j == lj) z = l[j];
+        }
+        if (rok) {
+          a.part[static_cast<int64_t>(n) * a.T + t] = make_float2(mx, s);
+          if (lc >= 0 && lc < nv) a.label_logit[t] = z;
+        }
+      } else if (MODE == kHeadExp) {
+        float mx = -INFINITY;
+        for (int cb = 0; cb * 32 < nv; ++cb) {
+          float l[32];
+          load_logits(tb + cb * 32, nv - cb * 32, l);
+          mx = fmaxf(mx, max32(l));
+        }
+        const float ref = (fabsf(mx) <= kRefRange || mx == -INFINITY) ? 0.0f : mx;
+        const float base = ref * kLog2e;
+        float s = 0.0f, z = 0.0f;
+        uint16_t* grow = a.g + static_cast<int64_t>(t) * a.ldg + n0;
+        for (int cb = 0; cb < kHeadTile / 32; ++cb) {
+          float l[32];
+          load_logits(tb + cb * 32, nv - cb * 32, l);
+          const int lj = (lc >> 5) == cb ? static_cast<int>(lc & 31) : -1;
+          float p[4] = {};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float x = l[j];
+            l[j] = exp2_fast(fmaf(x, kLog2e, -base));
+            p[j & 3] += l[j];
+            if (j == lj) {
+              z = x;
+              l[j] = 0.0f;
+            }
+          }
+          s += (p[0] + p[1]) + (p[2] + p[3]);
+          if (rok) store_bf16x32(grow + cb * 32, l, 32);
+        }
+        if (rok) {
+          a.part[static_cast<int64_t>(n) * a.T + t] = make_float2(ref, s);
+          if (lc >= 0 && lc < nv) a.label_logit[t] = z;
+        }
+      } else if (MODE == kHeadProb) {
+        const float lse = rok ? __ldcg(a.lse + t) : 0.0f;
+        const float base = lse * kLog2e;
+        uint16_t* grow = a.g + static_cast<int64_t>(t) * a.ldg + n0;
+        for (int cb = 0; cb < kHeadTile / 32; ++cb) {
+          float l[32];
+          load_logits(tb + cb * 32, nv - cb * 32, l);
+          const int lj = (lc >> 5) == cb ? static_cast<int>(lc & 31) : -1;
+          float z = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float x = l[j];
+            if (j == lj) z = x;
+            l[j] = counted ? exp2_fast(fmaf(x, kLog2e, -base)) : 0.0f;
+          }
+          if (lj >= 0) {
+            z = expm1f(z - lse);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j == lj) l[j] = z;
+          }
+          if (rok) store_bf16x32(grow + cb * 32, l, 32);
+        }
+        if (rok && n == 0 && a.v0 == 0 && !counted && label != a.ignore && a.status)
+          atomicOr(a.status, QLORA_DEV_LABEL);
+      } else {
+        // dH = ca * sum + cl * W[label]
+        float ca = 0.0f, cl = 0.0f;
+        if (a.last && counted) {
+          if (a.row_sum) {
+            const float g = a.weight ? a.scale * __ldcg(a.weight + t) : a.scale / static_cast<float>(__ldcg(a.count));
+            ca = g / __ldcg(a.row_sum + t);
+            cl = g * __ldcg(a.p_label + t);
+          } else {
+            ca = a.stats ? __ldcg(a.dloss) / __ldcg(a.stats + 1) : __ldcg(a.dloss + t);
+          }
+        }
+        const float al = (!a.first && a.alpha && rok) ? __ldcg(a.alpha + t) : 1.0f;
+        float4* sum = reinterpret_cast<float4*>(a.acc) +
+                      ((static_cast<int64_t>(m) * a.ntiles + n) * 2 + rank) * (8 * 8 * 128) + et;
+        for (int cb = 0; cb * 32 < nv; ++cb) {
+          float l[32];
+          {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tb + cb * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) l[j] = __uint_as_float(v[j]);
+          }
+          float4* at = sum + cb * (8 * 128);
+          if (!a.first) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 o = __ldcg(at + j * 128);
+              l[4 * j] = fmaf(al, o.x, l[4 * j]);
+              l[4 * j + 1] = fmaf(al, o.y, l[4 * j + 1]);
+              l[4 * j + 2] = fmaf(al, o.z, l[4 * j + 2]);
+              l[4 * j + 3] = fmaf(al, o.w, l[4 * j + 3]);
+            }
+          }
+          if (!a.last) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) __stcg(at + j * 128, make_float4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]));
+          } else if (rok) {
+            const int nc = min(32, nv - cb * 32);
+            if (counted) {
+              if (a.row_sum) {
+                float w[32];
+                load_head_row(a.head, a.tab, label, n0 + cb * 32, nc, w);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) l[j] = fmaf(cl, w[j], ca * l[j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) l[j] *= ca;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) l[j] = 0.0f;
+            }
+            store_bf16x32(a.dh + static_cast<int64_t>(t) * a.ldd + n0 + cb * 32, l, nc);
+          }
+        }
+      }
+      tc_fence_before();  // this warp's reads of the accumulator are done
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(dsmem_addr(&acce[buf], 0));
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_d, 512);
+  }
+}
+
+// ------------------------------------------------------------------ combine
+//
+// Joins the (reference, sum) pairs of a row's tiles: R = max ref, S = sum of
+// s exp(ref - R).  A block takes 32 tokens (a lane each) and splits the tiles
+// over 16 warps.  Step: R and S run over the pieces, exponentials of tiles
+// whose reference is not R are rescaled in place, and alpha = exp(R_old - R).
+// With the last piece: lse, loss, and the mean in fp64 (per-block sums, added
+// in block order by the block that finishes last).
+
+namespace {
+
+constexpr int kCombineWarps = 16;
+
+__device__ __forceinline__ void join(float& R, float& S, float ref, float s) {
+  if (s == 0.0f) return;  // (a NaN is not equal and joins)
+  if (ref > R) {
+    S = S * expf(R - ref) + s;  // R = -inf: the factor is 0
+    R = ref;
+  } else {
+    S += s * (ref == R ? 1.0f : expf(ref - R));
+  }
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const HeadCombineArgs a) {
+  __shared__ float2 sm[kCombineWarps][32];
+  __shared__ float ref_s[32];
+  __shared__ bool last_block;
+  __shared__ double sums[kCombineWarps];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * 32 + lane;
+  const bool rok = t < a.T;
+
+  float R = -INFINITY, S = 0.0f;
+  if (rok) {
+#pragma unroll 4
+    for (int j = warp; j < a.ntiles; j += kCombineWarps) {
+      const float2 p = a.part[static_cast<int64_t>(j) * a.T + t];
+      join(R, S, p.x, p.y);
+    }
+  }
+  sm[warp][lane] = make_float2(R, S);
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < kCombineWarps; ++w) join(R, S, sm[w][lane].x, sm[w][lane].y);
+    if (a.run && rok) {
+      if (!a.first) {
+        const float2 old = a.run[t];
+        join(R, S, old.x, old.y);
+        a.alpha[t] = (old.y == 0.0f || old.x == R) ? 1.0f : expf(old.x - R);
+      }
+      a.run[t] = make_float2(R, S);
+    }
+    ref_s[lane] = R;
+    if (a.last) {
+      double sum = 0.0;
+      bool counted = false;
+      if (rok) {
+        const int64_t label = a.labels[t];
+        counted = label != a.ignore && label >= 0 && label < a.vocab;
+        const float lse = R + logf(S);
+        const float z = counted ? a.label_logit[t] : lse;
+        const float loss = counted ? lse - z : 0.0f;
+        a.lse[t] = lse;
+        a.loss[t] = loss;
+        if (a.row_sum) {
+          a.row_sum[t] = S;
+          a.p_label[t] = expm1f(z - lse);
+        }
+        sum = loss;
+        if (a.status) {
+          if (counted && !isfinite(lse)) atomicOr(a.status, QLORA_DEV_NONFINITE);
+          if (!counted && label != a.ignore) atomicOr(a.status, QLORA_DEV_LABEL);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      const uint32_t votes = __ballot_sync(0xFFFFFFFFu, counted);
+      if (lane == 0) {
+        a.block_sum[blockIdx.x] = sum;
+        atomicAdd(&a.counters[0], __popc(votes));
+        __threadfence();
+        last_block = atomicAdd(&a.counters[1], 1) == static_cast<int>(gridDim.x) - 1;
+      }
+    }
+  }
+  __syncthreads();
+  if (a.e) {
+    const float ref = ref_s[lane];
+    for (int j = warp; j < a.ntiles; j += kCombineWarps) {
+      const float2 p = rok ? a.part[static_cast<int64_t>(j) * a.T + t] : make_float2(0.0f, 0.0f);
+      uint32_t todo = __ballot_sync(0xFFFFFFFFu, rok && p.y != 0.0f && p.x != ref);
+      const float f = expf(p.x - ref);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const float fr = __shfl_sync(0xFFFFFFFFu, f, src);
+        uint4* at = reinterpret_cast<uint4*>(a.e + static_cast<int64_t>(blockIdx.x * 32 + src) * a.lde +
+                                             static_cast<int64_t>(j) * kHeadTile) + lane;
+        const uint4 v = *at;
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = pack_bf16x2(__uint_as_float(w[i] << 16) * fr, __uint_as_float(w[i] & 0xFFFF0000u) * fr);
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  if (a.last && last_block) {
+    __threadfence();
+    double sum = 0.0;
+    for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += kCombineWarps * 32) sum += __ldcg(a.block_sum + b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kCombineWarps; ++w) sum += sums[w];
+      const int count = __ldcg(a.counters);
+      a.stats[0] = count > 0 ? static_cast<float>(sum / count) : 0.0f;
+      a.stats[1] = static_cast<float>(count);
+    }
+  }
+}
+
+template <int MODE>
+static cudaError_t launch_head_gemm_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
+                                         cudaStream_t stream) {
+  static uint64_t done = 0;
+  if (cudaError_t e = allow_smem(head_gemm_kernel<MODE>, HeadPlan::kSmem, done)) return e;
+  const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles;
+  const int pairs = static_cast<int>(std::min<int64_t>(tiles, 74));  // one pair per TPC
+  return launch_kernel(head_gemm_kernel<MODE>, dim3(2 * pairs), dim3(kHeadThreads), HeadPlan::kSmem, stream,
+                       dim3(2, 1, 1), tm_a, tm_b, a);
+}
+
+cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
+                             cudaStream_t stream) {
+  switch (mode) {
+    case kHeadLoss: return launch_head_gemm_impl<kHeadLoss>(tm_a, tm_b, a, stream);
+    case kHeadProb: return launch_head_gemm_impl<kHeadProb>(tm_a, tm_b, a, stream);
+    case kHeadExp: return launch_head_gemm_impl<kHeadExp>(tm_a, tm_b, a, stream);
+    case kHeadGrad: return launch_head_gemm_impl<kHeadGrad>(tm_a, tm_b, a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+int head_combine_blocks(int64_t T) { return static_cast<int>((T + 31) / 32); }
+
+cudaError_t launch_head_combine(const HeadCombineArgs& a, cudaStream_t stream) {
+  return launch_kernel(head_combine_kernel, dim3(head_combine_blocks(a.T)), dim3(kCombineWarps * 32), 0, stream,
+                       dim3(1, 1, 1), a);
+}
+
+}  // namespace qnf4

@@ -1,0 +1,114 @@
+// train.h — host-side launch functions of the training-step kernels (internal
+// to the library): 8-bit activation checkpoints (act8.cu) and the loss head
+// (head_loss.cu).
+#pragma once
+
+#include "../../include/qlora_train.h"
+#include "kernels.h"
+
+namespace qnf4 {
+
+// Raises a kernel's dynamic shared-memory limit once per device (a kernel's
+// attributes belong to the device that is current when they are set).
+template <typename F>
+inline cudaError_t allow_smem(F kernel, uint32_t bytes, uint64_t& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (__atomic_load_n(&done, __ATOMIC_RELAXED) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) __atomic_fetch_or(&done, bit, __ATOMIC_RELAXED);
+  return e;
+}
+
+// ------------------------------------------------------------------ act8.cu
+
+cudaError_t launch_act8_quantize(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, uint8_t* codes, uint8_t* exps,
+                                 int32_t* status, cudaStream_t stream);
+cudaError_t launch_act8_dequantize(const uint8_t* codes, const uint8_t* exps, int64_t M, int64_t K, uint16_t* x,
+                                   int64_t ldx, cudaStream_t stream);
+
+// dA[j, k] = sum_m dU[m, j] X'[m, k] from the checkpoint (SkinnyArgs as for
+// mode DA of skinny.cu): tm_du the bf16 hi/lo of dU [M, 2 ra] box {64, 64}
+// SW128, tm_x the codes [M, K] u8 box {128, 64}; exps [M, K / 64].
+cudaError_t launch_act8_da(const CUtensorMap& tm_du, const CUtensorMap& tm_x, const uint8_t* exps,
+                           const SkinnyArgs& a, int grid_rows, int splits, cudaStream_t stream);
+
+// ------------------------------------------------------------- head_loss.cu
+
+constexpr int kHeadTile = 256;  // tokens, and columns, of a CTA pair's tile
+
+enum HeadMode {
+  kHeadLoss = 0,  // logits of a piece -> per-tile softmax statistics
+  kHeadProb = 1,  // logits of a piece -> probabilities less the label's one, bf16
+  kHeadExp = 2,   // logits of a piece -> exponentials, bf16, and the statistics
+  kHeadGrad = 3   // those times the piece's weight -> dH (or its fp32 sum so far)
+};
+
+struct HeadArgs {
+  int T;                  // tokens
+  int ncols;              // columns of this product: the piece's vocabulary rows, or dim (Grad)
+  int kst;                // 64-deep contraction stages
+  int b_row0;             // the piece's first row in W's tensor map
+  int64_t v0;             // the piece's first vocabulary index
+  int64_t vocab;
+  int mtiles, ntiles;
+  const int64_t* labels;
+  int64_t ignore;
+  float* label_logit;     // Loss, Exp: [T]
+  float2* part;           // Loss, Exp: (reference, sum of exponentials) [tile][T], from the piece's first tile
+  const float* lse;       // Prob: [T]
+  uint16_t* g;            // Prob, Exp: [T, ldg]
+  int64_t ldg;
+  uint32_t* zero;         // Loss, Exp: words cleared by the first CTA (combine's counters)
+  int zero_count;
+  // Grad
+  int first, last;        // of the pieces
+  float* acc;             // fp32 sum over the pieces so far, tile-blocked
+  const float* alpha;     // [T] factor of the sum so far (null: 1)
+  uint16_t* dh;           // [T, ldd]
+  int64_t ldd;
+  const float* dloss;     // per-token gradients, or one number with `stats` (backward)
+  const float* stats;
+  const float* row_sum;   // [T] softmax denominators (step), null in the backward
+  const float* p_label;   // [T] probability of the label less 1 (step)
+  const float* weight;    // [T] or null (step)
+  float scale;
+  const int32_t* count;   // tokens that count (step, weight null)
+  qlora_head head;        // step: the label's row of W
+  Nf4Tables tab;
+  int32_t* status;
+};
+
+//   tm_a: H [T, dim] (Grad: the piece's [T, ldg]) box {64, 128} SW128;
+//   tm_b: W rows, box {64, 128} SW128 (Grad: {64, 64}).
+cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
+                             cudaStream_t stream);
+
+// Joins the per-tile statistics of every row; see head_loss.cu.
+struct HeadCombineArgs {
+  int T, ntiles;
+  const float2* part;      // [ntiles][T]
+  const float* label_logit;
+  const int64_t* labels;
+  int64_t ignore;
+  int64_t vocab;
+  int first, last;         // of the pieces (the forward combines once: both)
+  float2* run;             // step: running (reference, sum) [T]
+  float* alpha;            // step: [T]
+  uint16_t* e;             // step: the piece's exponentials [T, lde], or null
+  int64_t lde;
+  float* row_sum;          // step: [T]
+  float* p_label;          // step: [T]
+  int32_t* counters;       // [2]: tokens that count, blocks done; cleared before
+  double* block_sum;       // [blocks]
+  float* loss;
+  float* lse;
+  float* stats;
+  int32_t* status;
+};
+int head_combine_blocks(int64_t T);
+cudaError_t launch_head_combine(const HeadCombineArgs& a, cudaStream_t stream);
+
+}  // namespace qnf4

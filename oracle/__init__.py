@@ -38,10 +38,14 @@ Modules:
   products within the GEMM tolerances).
 * :mod:`oracle.dq_centered` — double quantisation with mean centring, for an
   error ablation against the plain scheme (no CUDA path).
+* :mod:`oracle.act8` — 8-bit checkpoints of a linear's input (the GPU must
+  match codes and exponents bit for bit).
+* :mod:`oracle.head_loss` — softmax cross entropy of the head's logits and its
+  gradient in fp64.
 
 Parity status per function is listed in each module header.  Every function
 here is pinned by ``tests/test_oracle_*.py`` to facts the pages or
 mathematics fix; functions whose pin is partial say so.
 """
 
-from . import numerics, nf4, linear, optim, dropout, dq_centered  # noqa: F401
+from . import numerics, nf4, linear, optim, dropout, dq_centered, act8, head_loss  # noqa: F401

@@ -1,0 +1,173 @@
+"""GPU parity of the 8-bit activation checkpoints: codes and exponents bit for
+bit, decoded values exactly, and the backward passes that read them: dX and dB
+bitwise those of the plain passes, dA bitwise that of the plain pass on the
+decoded input (the same operand values in the same order) and within 1e-4 of
+the fp64 oracle, as every fp32 output of the linears."""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_26_b200 as q
+import synth
+from oracle import act8
+from oracle import linear as ol
+from oracle import nf4
+from tests._util import bits
+
+pytestmark = pytest.mark.gpu
+
+
+def _same(a, b):
+    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def _x(M, K, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, K, generator=g) * torch.exp(4 * torch.randn(M, 1, generator=g))
+    x[:, K // 3] *= 300.0
+    return x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,K", [(1, 64), (3, 128), (64, 512), (1001, 4096), (7, 11008), (4097, 192)])
+def test_quantize_and_dequantize_match_oracle(M, K):
+    x = _x(M, K)
+    x8 = q.act8_quantize(x.cuda())
+    codes, exps = act8.quantize(bits(x))
+    assert np.array_equal(x8.codes.cpu().numpy(), codes) and np.array_equal(x8.exps.cpu().numpy(), exps)
+    out = q.act8_dequantize(x8)
+    assert np.array_equal(out.double().cpu().numpy(), act8.dequantize(codes, exps))
+
+
+def test_every_finite_bf16_value():
+    b = np.arange(1 << 16, dtype=np.uint16)
+    b = b[(b & 0x7F80) != 0x7F80]
+    rng = np.random.default_rng(0)
+    b = np.concatenate([b, rng.permutation(b), np.zeros(-2 * b.size % 128, dtype=np.uint16)]).reshape(-1, 128)
+    x = torch.from_numpy(b.view(np.int16)).view(torch.bfloat16)
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    x8 = q.act8_quantize(x.cuda(), status=status)
+    codes, exps = act8.quantize(b)
+    assert np.array_equal(x8.codes.cpu().numpy(), codes) and np.array_equal(x8.exps.cpu().numpy(), exps)
+    v = act8.dequantize(codes, exps)
+    v = np.where(np.abs(v) >= 2.0 ** 128, np.copysign(np.inf, v), v)
+    assert np.array_equal(q.act8_dequantize(x8).double().cpu().numpy(), v)
+    assert int(status[0]) == 0
+
+
+def test_strided_rows_and_the_gap_between_them():
+    M, K, ld = 37, 192, 320
+    buf = torch.full((M, ld), 7.0, dtype=torch.bfloat16, device="cuda")
+    x = _x(M, K, 3)
+    buf[:, 64:64 + K] = x.cuda()
+    x8 = q.act8_quantize(buf[:, 64:64 + K])
+    codes, exps = act8.quantize(bits(x))
+    assert np.array_equal(x8.codes.cpu().numpy(), codes) and np.array_equal(x8.exps.cpu().numpy(), exps)
+    out = torch.full((M, ld), 9.0, dtype=torch.bfloat16, device="cuda")
+    q.act8_dequantize(x8, out=out[:, 64:64 + K])
+    assert np.array_equal(out[:, 64:64 + K].double().cpu().numpy(), act8.dequantize(codes, exps))
+    assert bool((out[:, :64] == 9).all()) and bool((out[:, 64 + K:] == 9).all())
+
+
+def test_non_finite_values_keep_their_place():
+    x = torch.ones(4, 128, dtype=torch.bfloat16)
+    x[1, 5], x[2, 70], x[3, 0] = float("nan"), float("inf"), -float("inf")
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    out = q.act8_dequantize(q.act8_quantize(x.cuda(), status=status)).float().cpu()
+    assert int(status[0]) == q.DEV_NONFINITE
+    assert torch.isnan(out[1, 5]) and out[2, 70] == float("inf") and out[3, 0] == -float("inf")
+    assert int(torch.isnan(out).sum()) == 1 and int(torch.isinf(out).sum()) == 2
+    assert bool((out[0] == 1).all()) and bool((out[1, 64:] == 1).all())
+
+
+def test_no_rows():
+    x8 = q.act8_quantize(torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"))
+    assert x8.codes.shape == (0, 128) and q.act8_dequantize(x8).shape == (0, 128)
+
+
+# tokens, outputs, inputs, rank: every GEMM path, ragged stages and tiles, rank chunks
+SHAPES = [(1, 64, 64, 16), (64, 512, 512, 16), (65, 192, 320, 48), (200, 512, 640, 32), (600, 512, 768, 64),
+          (1000, 384, 448, 64), (150, 384, 448, 144), (700, 512, 768, 256), (4096, 4096, 4096, 64)]
+
+
+@pytest.mark.parametrize("M,N,K,r", SHAPES)
+@pytest.mark.parametrize("dt", [q.DTYPE_BF16, q.DTYPE_F32])
+def test_linear_bwd_act8(M, N, K, r, dt):
+    d = synth.linear_inputs(synth.Linear("a8", N, K), M, r, 1)
+    g = {k: v.cuda() for k, v in d.items()}
+    W, s = q.quantize_weight(g["W"]), 16.0 / r
+    U = g["X"].float() @ g["A"].float().t()
+    x8 = q.act8_quantize(g["X"])
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    dX, dA, dB = q.qlora_linear_bwd_act8(g["dY"], x8, U, W, g["A"], g["B"], s, dx_dtype=dt, status=status)
+    pX, _, pB = q.qlora_linear_bwd(g["dY"], g["X"], U, W, g["A"], g["B"], s, dx_dtype=dt)
+    _, pA, _ = q.qlora_linear_bwd(g["dY"], q.act8_dequantize(x8), U, W, g["A"], g["B"], s, dx_dtype=dt)
+    assert int(status[0]) == 0
+    assert _same(dX, pX) and _same(dB, pB) and _same(dA, pA)
+    dU = s * (ol._f64(bits(d["dY"])) @ ol._f64(bits(d["B"])))
+    ref = dU.T @ act8.dequantize(*act8.quantize(bits(d["X"])))
+    assert ol.rel_frobenius(dA.cpu().numpy(), ref) <= 1e-4
+    again = q.qlora_linear_bwd_act8(g["dY"], x8, U, W, g["A"], g["B"], s, dx_dtype=dt)
+    assert _same(again[1], dA)
+
+
+@pytest.mark.parametrize("M,members,K,r", [(333, (256, 128), 512, 16), (1030, (512, 512, 256), 768, 64),
+                                           (40, (128, 128, 128, 128), 192, 32), (512, (320,), 256, 128)])
+def test_group_bwd_act8(M, members, K, r):
+    G, N = len(members), sum(members)
+    gen = torch.Generator().manual_seed(M)
+    def rnd(*s, std=1.0):
+        return (torch.randn(*s, generator=gen) * std).to(torch.bfloat16).cuda()
+    W = q.quantize_weight(rnd(N, K, std=0.02))
+    A, B, X, dY = rnd(G * r, K, std=K ** -0.5), rnd(N, r, std=0.1), rnd(M, K), rnd(M, N)
+    U = X.float() @ A.float().t()
+    x8 = q.act8_quantize(X)
+    got = q.qlora_group_bwd_act8(dY, x8, U, W, members, A, B, 0.5)
+    want = q.qlora_group_bwd(dY, q.act8_dequantize(x8), U, W, members, A, B, 0.5)
+    for a, b in zip(got, want):
+        assert _same(a, b)
+
+
+@pytest.mark.parametrize("M,N,K,r,p", [(200, 512, 640, 32, 0.05), (600, 512, 768, 64, 0.5), (150, 384, 448, 144, 0.1)])
+def test_dropout_bwd_act8(M, N, K, r, p):
+    d = synth.linear_inputs(synth.Linear("a8d", N, K), M, r, 2)
+    g = {k: v.cuda() for k, v in d.items()}
+    W = q.quantize_weight(g["W"])
+    Y, U, Xd = q.qlora_linear_fwd_dropout(g["X"], W, g["A"], g["B"], 0.25, p, 11)
+    x8 = q.act8_quantize(Xd)
+    back = q.act8_dequantize(x8)
+    assert bool((back[Xd == 0] == 0).all())
+    got = q.qlora_linear_bwd_dropout_act8(g["dY"], x8, U, W, g["A"], g["B"], 0.25, p, 11)
+    want = q.qlora_linear_bwd_dropout(g["dY"], back, U, W, g["A"], g["B"], 0.25, p, 11)
+    for a, b in zip(got, want):
+        assert _same(a, b)
+
+
+def test_no_tokens_give_zero_gradients():
+    W = q.quantize_weight(torch.randn(128, 128).to(torch.bfloat16).cuda())
+    e = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    A = torch.zeros(16, 128, dtype=torch.bfloat16, device="cuda")
+    B = torch.zeros(128, 16, dtype=torch.bfloat16, device="cuda")
+    dX, dA, dB = q.qlora_linear_bwd_act8(e, q.act8_quantize(e), torch.empty(0, 16, device="cuda"), W, A, B, 1.0)
+    assert dX.shape == (0, 128) and not dA.any() and not dB.any()
+
+
+def test_refusals_on_device_tensors():
+    x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    x8 = q.act8_quantize(x)
+    for bad in (x[:, :100], x.t(), torch.zeros(4, 132, dtype=torch.bfloat16, device="cuda")[:, :128],
+                x[:1].expand(4, 128), torch.zeros(4, 136, dtype=torch.bfloat16, device="cuda")[:, 4:132]):
+        with pytest.raises(q.QloraError):
+            q.act8_quantize(bad)
+    with pytest.raises(q.QloraError):
+        q.act8_dequantize(q.Act8(x8.codes, x8.exps[:, :1]))
+    with pytest.raises(q.QloraError):
+        q.act8_dequantize(x8, out=torch.zeros(3, 128, dtype=torch.bfloat16, device="cuda"))
+    W = q.quantize_weight(torch.zeros(128, 128, dtype=torch.bfloat16, device="cuda"))
+    A = torch.zeros(16, 128, dtype=torch.bfloat16, device="cuda")
+    B = torch.zeros(128, 16, dtype=torch.bfloat16, device="cuda")
+    dY, U = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 16, device="cuda")
+    for args in ((dY.float(), x8, U, W, A, B), (dY, x8, U[:3], W, A, B), (dY, x8, U, W, A[:, :64], B),
+                 (dY, q.Act8(x8.codes[:2], x8.exps), U, W, A, B), (dY.t().contiguous().t(), x8, U, W, A, B)):
+        with pytest.raises(q.QloraError):
+            q.qlora_linear_bwd_act8(*args, 1.0)

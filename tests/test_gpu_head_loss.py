@@ -1,0 +1,335 @@
+"""GPU parity of the loss head against the fp64 oracle on the exact bf16 inputs.
+
+Tolerances, per element and derived:
+
+* a logit is a sum of dim exact products in fp32, in any order: off by at most
+  d_tv = 2 dim 2^-24 sum_d |h_td w_vd| (2^-24 half a step, twice for a sum that
+  truncates), and d_t is the largest over v;
+* lse is a weighted mean away from the logits' errors: off by d_t plus the
+  fp32 exponentials (relative 2^-22, and the argument's rounding, 2^-23 of the
+  largest |l| log2 e) and its own rounding: d_t + 2^-21 (4 + max|l|);
+* the loss by that and the label logit's error: 2 d_t + 2^-21 (4 + 2 max|l|);
+* dH: a probability is off by rel = 2 d_t + 2^-20 (4 + max|l|) relative.  At the
+  label p - 1 = expm1(l - lse) is taken in fp32 first, so its error is that of
+  p, rel p, and not rel (1 - p): with V = 1, where p = 1 and the gradient is 0,
+  an lse half an ulp off gives rel.  Then G = p - onehot is rounded to bf16
+  (2^-8 relative; twice where the step rescales a row) and the output once
+  more: |g_t| sum_v (rel p_tv + 2^-8 |G_tv|) |W_vd| + 2^-8 |dH_td|.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_26_b200 as q
+from oracle import head_loss as hl
+from oracle import nf4
+from tests._util import bits
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(T, V, D, seed=0, scale=1.0, ignored=0.25, lean=0.0):
+    g = torch.Generator().manual_seed(seed)
+    w = (torch.randn(V, D, generator=g) * 0.02).to(torch.bfloat16)
+    y = torch.randint(0, V, (T,), generator=g)
+    h = torch.randn(T, D, generator=g) * scale
+    if lean:
+        h = h + lean * torch.rand(T, 1, generator=g) * w[y].float() / (4e-4 * D)
+    out = torch.rand(T, generator=g) < ignored
+    return h.to(torch.bfloat16), w, torch.where(out, torch.full_like(y, -100), y)
+
+
+class Ref:
+    """The oracle's answers and the bounds above."""
+
+    def __init__(self, h, w, y):
+        hb, wb, self.y = bits(h), bits(w), y.numpy()
+        H, W = hl._f64(hb), hl._f64(wb)
+        D = H.shape[1]
+        self.loss, self.lse, self.mean, self.count = hl.fwd(hb, wb, self.y)
+        d = 2 * D * 2.0 ** -24 * (np.abs(H) @ np.abs(W).T).max(1)
+        top = np.abs(H @ W.T).max(1)
+        self.lse_tol = d + 2.0 ** -21 * (4 + top)
+        self.loss_tol = 2 * d + 2.0 ** -21 * (4 + 2 * top)
+        self.p = hl.probabilities(hb, wb, self.y)
+        self.W, self.rel = W, 2 * d + 2.0 ** -20 * (4 + top)
+        self.soft = np.exp(H @ W.T - self.lse[:, None])
+
+    def check_loss(self, loss, lse, stats):
+        loss, lse, stats = (v.double().cpu().numpy() for v in (loss, lse, stats))
+        assert np.all(np.abs(lse - self.lse) <= self.lse_tol)
+        assert np.all(np.abs(loss - self.loss) <= self.loss_tol)
+        assert not loss[self.y == -100].any()
+        assert stats[1] == self.count
+        assert abs(stats[0] - self.mean) <= self.loss_tol.mean() * self.y.size / max(self.count, 1) + 2.0 ** -23 * abs(
+            self.mean)
+
+    def check_grad(self, dH, g, roundings=1):
+        dH = dH.double().cpu().numpy()
+        c = hl.counted(self.y, self.W.shape[0])
+        g = np.where(c, np.asarray(g, dtype=np.float64), 0.0)
+        ref = (self.p * g[:, None]) @ self.W
+        off = (roundings * 2.0 ** -8 * 1.01 * np.abs(self.p) + self.rel[:, None] * self.soft) * np.abs(g)[:, None]
+        tol = off @ np.abs(self.W) + 2.0 ** -8 * np.abs(ref) + 1e-37
+        assert np.all(np.abs(dH - ref) <= tol)
+        assert not dH[~c].any()
+        if self.rel.max() < 1e-3 and self.W.shape[0] > 1:  # and as a whole, well inside
+            assert np.linalg.norm(dH - ref) <= 5e-3 * np.linalg.norm(ref)
+
+
+# tokens, vocabulary, width: one of each, odd ones, tile borders, widths that end inside a stage
+SHAPES = [(1, 1, 8), (1, 1000, 64), (3, 257, 72), (129, 256, 256), (200, 1003, 520), (256, 512, 64), (257, 255, 192),
+          (700, 3001, 1024), (60, 33000, 256)]
+
+
+@pytest.mark.parametrize("T,V,D", SHAPES)
+def test_loss_and_gradient_match_oracle(T, V, D):
+    h, w, y = _case(T, V, D, seed=T)
+    y[-1] = V - 1
+    r = Ref(h, w, y)
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    H, W, Y = h.cuda(), w.cuda(), y.cuda()
+    loss, lse, stats = q.qlora_head_loss_fwd(H, W, Y, status=status)
+    r.check_loss(loss, lse, stats)
+    g = torch.linspace(-1, 2, T)
+    dH = q.qlora_head_loss_bwd(H, W, Y, lse, g.cuda(), status=status)
+    r.check_grad(dH, g.numpy())
+    up = torch.tensor([3.0], device="cuda")
+    r.check_grad(q.qlora_head_loss_bwd(H, W, Y, lse, up, stats=stats), np.full(T, 3.0 / max(r.count, 1)))
+    got = q.qlora_head_loss_step(H, W, Y, scale=2.0, status=status)
+    r.check_loss(*got[:3])
+    r.check_grad(got[3], np.full(T, 2.0 / max(r.count, 1)))
+    got = q.qlora_head_loss_step(H, W, Y, weight=g.cuda(), scale=0.5, status=status)
+    r.check_grad(got[3], 0.5 * g.numpy())
+    assert int(status[0]) == 0
+    again = q.qlora_head_loss_step(H, W, Y, weight=g.cuda(), scale=0.5)
+    for a, b in zip(got, again):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+
+
+@pytest.mark.parametrize("T,V,D", [(16500, 4500, 64), (33000, 2500, 128)])
+def test_several_pieces(T, V, D):
+    """Token counts at which the vocabulary runs in more than one piece: the
+    fp32 sum carried between pieces."""
+    assert q.qlora_head_loss_workspace_size(T, V, D, False, q.HEAD_BWD) < 2 * T * V  # not the whole operand
+    h, w, y = _case(T, V, D, seed=1, lean=10.0)
+    rows = np.unique(np.linspace(0, T - 1, 400).astype(int))
+    r = Ref(h[rows], w, y[rows])
+    H, W, Y = h.cuda(), w.cuda(), y.cuda()
+    g = torch.linspace(-1, 2, T)
+    loss, lse, stats = q.qlora_head_loss_fwd(H, W, Y)
+    assert np.all(np.abs(loss.cpu().numpy()[rows] - r.loss) <= r.loss_tol)
+    sel = torch.from_numpy(rows).cuda()
+    r.check_grad(q.qlora_head_loss_bwd(H, W, Y, lse, g.cuda())[sel], g.numpy()[rows])
+    l2, lse2, st2, dH = q.qlora_head_loss_step(H, W, Y, weight=g.cuda())
+    assert np.all(np.abs(l2.cpu().numpy()[rows] - r.loss) <= r.loss_tol)
+    assert np.all(np.abs(lse2.cpu().numpy()[rows] - r.lse) <= r.lse_tol)
+    assert float(st2[1]) == float(stats[1]) == int((y != -100).sum())
+    assert abs(float(st2[0]) - float(stats[0])) <= 2 * r.loss_tol.max()
+    r.check_grad(dH[sel], g.numpy()[rows])
+
+
+@pytest.mark.parametrize("scale", [30.0, 200.0])
+@pytest.mark.parametrize("T,V,D", [(100, 2000, 256), (16500, 4500, 64)])
+def test_large_logits_take_other_references(T, V, D, scale):
+    """Logits of some hundreds, of either sign and far apart between tiles and
+    pieces: rows whose tiles have different references, a row far below zero."""
+    h, w, y = _case(T, V, D, seed=2, scale=scale)
+    h, w = h.float(), w.float() * 4
+    w[:256, 0] += 1.0
+    w[1000:1256, 0] -= 1.0
+    h[3] = 0
+    w[:, 1] = 1.0
+    h[3, 1] = -300.0        # every logit of the row at -300
+    h[4] = 0
+    h[4, 1] = 300.0
+    h, w = h.to(torch.bfloat16), w.to(torch.bfloat16)
+    y[3], y[4] = 5, V - 1
+    rows = np.unique(np.concatenate([np.arange(60), np.linspace(0, T - 1, 100).astype(int)]))
+    r = Ref(h[rows], w, y[rows])
+    H, W, Y = h.cuda(), w.cuda(), y.cuda()
+    sel = torch.from_numpy(rows).cuda()
+    loss, lse, stats = q.qlora_head_loss_fwd(H, W, Y)
+    assert np.all(np.abs(lse.cpu().numpy()[rows] - r.lse) <= r.lse_tol)
+    g = torch.ones(T, device="cuda")
+    r.check_grad(q.qlora_head_loss_bwd(H, W, Y, lse, g)[sel], np.ones(rows.size))
+    l2, lse2, _, dH = q.qlora_head_loss_step(H, W, Y, weight=g)
+    assert np.all(np.abs(l2.cpu().numpy()[rows] - r.loss) <= r.loss_tol)
+    assert np.all(np.abs(lse2.cpu().numpy()[rows] - r.lse) <= r.lse_tol)
+    r.check_grad(dH[sel], np.ones(rows.size), roundings=2)
+
+
+def test_well_predicted_tokens_keep_their_gradient():
+    """p close to 1 at the label: the gradient is the small difference."""
+    h, w, y = _case(64, 500, 256, seed=4, ignored=0.0)
+    h = (h.float() + 25.0 * w[y].float() / (4e-4 * 256)).to(torch.bfloat16)
+    r = Ref(h, w, y)
+    assert r.loss.min() < 1e-4
+    H, W, Y = h.cuda(), w.cuda(), y.cuda()
+    loss, lse, stats = q.qlora_head_loss_fwd(H, W, Y)
+    dH = q.qlora_head_loss_step(H, W, Y, weight=torch.ones(64, device="cuda"))[3].double().cpu().numpy()
+    ref = r.p @ r.W
+    err = np.linalg.norm(dH - ref, axis=1) / np.linalg.norm(ref, axis=1)
+    # 1 - p is off by the lse's and label logit's fp32 errors over its size
+    small = -np.take_along_axis(r.p, r.y[:, None], 1)[:, 0]
+    assert np.all(err <= 2 * 2.0 ** -8 + r.loss_tol / small)
+
+
+@pytest.mark.parametrize("T,V,D,centred", [(5, 1001, 64, False), (300, 2300, 512, True), (64, 40000, 2048, False),
+                                           (17000, 4500, 128, True)])
+def test_nf4_head(T, V, D, centred):
+    """An NF4 head is the bf16 head of its dequantised weight, bit for bit."""
+    h, w, y = _case(T, V, D, seed=5, lean=5.0)
+    H, Y = h.cuda(), y.cuda()
+    W = (q.quantize_weight_centered if centred else q.quantize_weight)(w.cuda())
+    dense = (q.nf4_dequantize_centered(W.codes, W.c8, W.s2, W.mean, V * D) if centred
+             else q.nf4_dequantize(W.codes, W.c8, W.s2, V * D)).view(V, D)
+    a, b = q.qlora_head_loss_fwd(H, W, Y), q.qlora_head_loss_fwd(H, dense, Y)
+    g = torch.linspace(-1, 1, T, device="cuda")
+    for x, z in zip(a, b):
+        assert torch.equal(x, z)
+    n = min(T, 200)
+    r = Ref(h[:n], dense.cpu(), y[:n])
+    assert np.all(np.abs(a[0].cpu().numpy()[:n] - r.loss) <= r.loss_tol)
+    r.check_grad(q.qlora_head_loss_bwd(H, W, Y, a[1], g)[:n], g.cpu().numpy()[:n])
+    got = q.qlora_head_loss_step(H, W, Y, weight=g)
+    r.check_grad(got[3][:n], g.cpu().numpy()[:n])
+    assert np.all(np.abs(got[0].cpu().numpy()[:n] - r.loss) <= r.loss_tol)
+
+
+def test_ignored_rows_may_hold_anything():
+    h, w, y = _case(300, 700, 128, seed=6, ignored=0.0)
+    y[5], y[6], y[200], y[299] = -100, -100, -100, -100
+    clean = h.clone()
+    h[5], h[6, 3], h[200] = float("nan"), float("inf"), torch.finfo(torch.bfloat16).min
+    H, C, W, Y = h.cuda(), clean.cuda(), w.cuda(), y.cuda()
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    keep = torch.tensor([i for i in range(300) if i not in (5, 6, 200, 299)], device="cuda")
+    a, b = (q.qlora_head_loss_fwd(x, W, Y, status=status) for x in (H, C))
+    g = torch.ones(300, device="cuda")
+    assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2]) and torch.equal(a[1][keep], b[1][keep])
+    da, db = q.qlora_head_loss_bwd(H, W, Y, a[1], g, status=status), q.qlora_head_loss_bwd(C, W, Y, b[1], g)
+    sa, sb = q.qlora_head_loss_step(H, W, Y, status=status), q.qlora_head_loss_step(C, W, Y)
+    for x, z in ((da, db), (sa[3], sb[3]), (sa[0], sb[0]), (sa[2], sb[2])):
+        assert torch.equal(x, z)
+    assert not da[5].any() and not sa[3][200].any()
+    assert int(status[0]) == 0
+    # a counted token's NaN stays with its row and is reported
+    y2 = Y.clone()
+    y2[5] = 1
+    s2 = q.qlora_head_loss_step(H, W, y2, weight=g, status=status)
+    assert int(status[0]) == q.DEV_NONFINITE
+    assert torch.isnan(s2[0][5]) and torch.isnan(s2[3][5]).all()
+    ref = q.qlora_head_loss_step(C, W, Y, weight=g)
+    assert torch.equal(s2[3][keep], ref[3][keep])
+
+
+def test_no_token_counts():
+    h, w, y = _case(40, 300, 64)
+    y[:] = -100
+    H, W, Y = h.cuda(), w.cuda(), y.cuda()
+    loss, lse, stats = q.qlora_head_loss_fwd(H, W, Y)
+    assert not loss.any() and stats.tolist() == [0.0, 0.0] and bool(torch.isfinite(lse).all())
+    assert not q.qlora_head_loss_bwd(H, W, Y, lse, torch.ones(1, device="cuda"), stats=stats).any()
+    got = q.qlora_head_loss_step(H, W, Y)
+    assert not got[3].any() and got[2].tolist() == [0.0, 0.0]
+
+
+def test_no_tokens():
+    H, W = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(9, 64, dtype=torch.bfloat16).cuda()
+    Y = torch.empty(0, dtype=torch.int64, device="cuda")
+    stats = torch.full((2,), 5.0, device="cuda")
+    loss, lse, st = q.qlora_head_loss_fwd(H, W, Y, stats=stats)
+    assert loss.numel() == 0 and st.tolist() == [0.0, 0.0]
+    e = torch.empty(0, device="cuda")
+    assert q.qlora_head_loss_bwd(H, W, Y, e, e).shape == (0, 64)
+    assert q.qlora_head_loss_step(H, W, Y)[3].shape == (0, 64)
+
+
+@pytest.mark.parametrize("bad", [-1, 300, 1 << 40, -(1 << 62)])
+def test_labels_out_of_range_are_reported_and_ignored(bad):
+    h, w, y = _case(40, 300, 64, ignored=0.0)
+    y2 = y.clone()
+    y2[7], y[7] = bad, -100
+    H, W = h.cuda(), w.cuda()
+    g = torch.ones(40, device="cuda")
+    lse = None
+    for f in (lambda Y, st: q.qlora_head_loss_fwd(H, W, Y, status=st),
+              lambda Y, st: q.qlora_head_loss_step(H, W, Y, status=st),
+              lambda Y, st: (q.qlora_head_loss_bwd(H, W, Y, lse, g, status=st),)):
+        status = torch.zeros(4, dtype=torch.int32, device="cuda")
+        a, b = f(y2.cuda(), status), f(y.cuda(), None)
+        assert int(status[0]) == q.DEV_LABEL
+        for x, z in zip(a, b):
+            assert torch.equal(x, z)
+        lse = b[1] if len(b) > 1 else lse
+
+
+def test_other_ignore_index():
+    h, w, y = _case(40, 300, 64)
+    y2 = torch.where(y == -100, torch.full_like(y, 17), torch.where(y == 17, torch.full_like(y, 18), y))
+    y1 = torch.where(y2 == 17, torch.full_like(y, -100), y2)
+    H, W = h.cuda(), w.cuda()
+    a, b = q.qlora_head_loss_step(H, W, y2.cuda(), ignore_index=17), q.qlora_head_loss_step(H, W, y1.cuda())
+    for x, z in zip(a, b):
+        assert torch.equal(x, z)
+
+
+def test_strided_rows_and_shifted_labels():
+    T, V, D = 150, 600, 136
+    h, w, y = _case(T, V, D, seed=8)
+    buf = torch.full((T + 1, 200), float("nan"), dtype=torch.bfloat16, device="cuda")
+    buf[:T, 16:16 + D] = h.cuda()
+    wbuf = torch.full((V, 160), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wbuf[:, 8:8 + D] = w.cuda()
+    lab = torch.cat([torch.zeros(1, dtype=torch.int64), y]).cuda()
+    H, W, Y = buf[:T, 16:16 + D], wbuf[:, 8:8 + D], lab[1:]
+    g = torch.linspace(0, 1, T, device="cuda")
+    dH = torch.full((T + 1, 152), 3.0, dtype=torch.bfloat16, device="cuda")
+    a = q.qlora_head_loss_step(H, W, Y, weight=g, dH=dH[:T, 8:8 + D])
+    b = q.qlora_head_loss_step(h.cuda(), w.cuda(), y.cuda(), weight=g)
+    for x, z in zip(a, b):
+        assert torch.equal(x, z)
+    assert bool((dH[:, :8] == 3).all()) and bool((dH[:, 8 + D:] == 3).all()) and bool((dH[T] == 3).all())
+    c = q.qlora_head_loss_bwd(H, W, Y, a[1], g, dH=dH[:T, 8:8 + D])
+    assert torch.equal(c, q.qlora_head_loss_bwd(h.cuda(), w.cuda(), y.cuda(), b[1], g))
+
+
+def test_gradient_against_differences_of_the_loss():
+    """The gradient along a direction against the loss at two points on it."""
+    h, w, y = _case(128, 700, 256, seed=9, lean=10.0)
+    H, W, Y = h.float().cuda(), w.cuda(), y.cuda()
+    dH = q.qlora_head_loss_step(h.cuda(), W, Y, weight=torch.ones(128, device="cuda"))[3].double()
+    step = torch.sign(dH).float() * 0.0625
+    up, down = (H + step).to(torch.bfloat16), (H - step).to(torch.bfloat16)
+    lu, ld = (q.qlora_head_loss_fwd(x, W, Y)[0].double() for x in (up, down))
+    moved = (up.double() - down.double())
+    pred = (dH * moved).sum(1)
+    # the second-order term cancels in a central difference; third order: |f'''| step^3 / 24 with
+    # |l'| <= |W| |moved| / 2 summed over dim, and bf16 points are off the line by half a step of H
+    reach = (moved.abs() @ W.double().abs().t()).amax(1) / 2
+    skew = ((up.double() + down.double()) / 2 - H.double()).abs() @ W.double().abs().t()
+    tol = reach ** 3 / 3 + 2 * reach * skew.amax(1) + 2.0 ** -7 * pred.abs() + 1e-5
+    assert bool(((lu - ld - pred).abs() <= tol).all())
+
+
+def test_refusals_on_device_tensors():
+    h, w, y = _case(8, 50, 64)
+    H, W, Y = h.cuda(), w.cuda(), y.cuda()
+    g = torch.ones(8, device="cuda")
+    for f in (lambda: q.qlora_head_loss_fwd(H, W[:, :56], Y), lambda: q.qlora_head_loss_fwd(H, W, Y[:7]),
+              lambda: q.qlora_head_loss_fwd(H, W, Y.int()), lambda: q.qlora_head_loss_fwd(H, W, y),
+              lambda: q.qlora_head_loss_fwd(H, W.float(), Y), lambda: q.qlora_head_loss_fwd(H.t(), W, Y),
+              lambda: q.qlora_head_loss_fwd(H[:, :60], W[:, :60], Y),
+              lambda: q.qlora_head_loss_bwd(H, W, Y, g, g[:1]), lambda: q.qlora_head_loss_bwd(H, W, Y, g.double(), g),
+              lambda: q.qlora_head_loss_bwd(H, W, Y, g, g, stats=g[:2]),
+              lambda: q.qlora_head_loss_step(H, W, Y, weight=g[:4]),
+              lambda: q.qlora_head_loss_step(H, W, Y, dH=torch.zeros(8, 32, dtype=torch.bfloat16, device="cuda")),
+              lambda: q.qlora_head_loss_step(H, W, Y, ws=torch.zeros(64, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(q.QloraError):
+            f()
