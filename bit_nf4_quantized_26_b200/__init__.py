@@ -592,61 +592,72 @@ ERR_DTYPE = 9
 Act8 = namedtuple("Act8", "codes exps")
 
 
-class _On:
-    """The device of a call's tensors, and the stream it runs on: ``stream``, or
-    that device's current one.  What a call allocates belongs to that stream."""
-
-    def __init__(self, dev, stream):
-        self._guards = []
-        if dev.index is not None and dev.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(dev))
-        if stream is not None:
-            self._guards.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
+def _run(dev, stream, call):
+    """``call(stream handle)`` with ``dev`` current, on ``stream`` or ``dev``'s
+    current stream; what it allocates belongs to that stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _run(dev, stream, call)
+    if stream is None:
+        return call(torch._C._cuda_getCurrentRawStream(dev.index))
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
-def _need(ok, code, where, what):
-    if not ok:
-        raise QloraError(code, f"{where}: {what}")
+def _refuse(code, where, what):
+    raise QloraError(code, f"{where}: {what}")
 
 
 def _tensor(t, dtype, shape, dev, where, name):
     """A contiguous tensor of this type and shape on this device."""
-    _need(t.dtype == dtype, ERR_DTYPE, where, f"{name} is {t.dtype}, not {dtype}")
-    _need(tuple(t.shape) == tuple(shape), ERR_SHAPE, where, f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
-    _need(t.device == dev, ERR_SHAPE, where, f"{name} is on {t.device}, not {dev}")
-    _need(t.is_contiguous(), ERR_SHAPE, where, f"{name} is not contiguous")
+    if t.dtype != dtype:
+        _refuse(ERR_DTYPE, where, f"{name} is {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        _refuse(ERR_SHAPE, where, f"{name} is {tuple(t.shape)}, not {shape}")
+    if t.device != dev:
+        _refuse(ERR_SHAPE, where, f"{name} is on {t.device}, not {dev}")
+    if not t.is_contiguous():
+        _refuse(ERR_SHAPE, where, f"{name} is not contiguous")
     return t
 
 
-def _vector(t, dtype, n, dev, where, name):
-    return _tensor(t, dtype, (n,), dev, where, name)
+def _out(t, shape, dtype, dev, where, name):
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _tensor(t, dtype, shape, dev, where, name)
 
 
 def _rows(t, where, name, cols=None, rows=None, dev=None):
-    """(rows, columns, row stride) of a bf16 matrix whose rows are contiguous."""
-    _need(t.dtype == torch.bfloat16, ERR_DTYPE, where, f"{name} is {t.dtype}, not torch.bfloat16")
-    _need(t.dim() == 2, ERR_SHAPE, where, f"{name} has {t.dim()} dimensions, not 2")
-    _need(t.is_cuda and (dev is None or t.device == dev), ERR_SHAPE, where, f"{name} is on {t.device}")
+    """(rows, columns, row stride) of a bf16 CUDA matrix whose rows are contiguous."""
+    if t.dtype != torch.bfloat16:
+        _refuse(ERR_DTYPE, where, f"{name} is {t.dtype}, not torch.bfloat16")
+    if t.dim() != 2:
+        _refuse(ERR_SHAPE, where, f"{name} has {t.dim()} dimensions, not 2")
+    if not t.is_cuda or (dev is not None and t.device != dev):
+        _refuse(ERR_SHAPE, where, f"{name} is on {t.device}")
     M, K = t.shape
-    _need((cols is None or K == cols) and (rows is None or M == rows), ERR_SHAPE, where,
-          f"{name} is {tuple(t.shape)}, not {(rows if rows is not None else M, cols if cols is not None else K)}")
-    _need(K <= 1 or M == 0 or t.stride(1) == 1, ERR_SHAPE, where, f"{name}'s rows are not contiguous")
-    return M, K, t.stride(0) if M > 1 else K
+    if (cols is not None and K != cols) or (rows is not None and M != rows):
+        _refuse(ERR_SHAPE, where, f"{name} is {(M, K)}, not {(M if rows is None else rows, cols)}")
+    ld, inner = t.stride()
+    if K > 1 and M > 0 and inner != 1:
+        _refuse(ERR_SHAPE, where, f"{name}'s rows are not contiguous")
+    return M, K, ld if M > 1 else K
 
 
-def _status_word(status, dev, where):
-    if status is not None:
-        _need(status.dtype == torch.int32 and status.numel() >= 1 and status.device == dev, ERR_DTYPE, where,
-              "status is not an int32 word on the call's device")
+def _word(status, dev, where):
+    """Address of the optional device status word."""
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.numel() < 1 or status.device != dev:
+        _refuse(ERR_DTYPE, where, "status is not an int32 word on the call's device")
+    return status.data_ptr()
+
+
+def _workspace(ws, size, dev, where):
+    """(address, bytes, tensor) of the workspace, allocated if not given."""
+    if ws is None:
+        ws = torch.empty(max(size(), 16), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        _refuse(ERR_SHAPE, where, f"ws is on {ws.device}, or not contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def act8_quantize(X, codes=None, exps=None, status=None, stream=None):
@@ -655,31 +666,32 @@ def act8_quantize(X, codes=None, exps=None, status=None, stream=None):
     where = "act8_quantize"
     M, K, ld = _rows(X, where, "X")
     dev = X.device
-    _status_word(status, dev, where)
-    with _On(dev, stream) as st:
-        codes = (torch.empty((M, K), dtype=torch.uint8, device=dev) if codes is None
-                 else _tensor(codes, torch.uint8, (M, K), dev, where, "codes"))
-        exps = (torch.empty((M, K // 64), dtype=torch.uint8, device=dev) if exps is None
-                else _tensor(exps, torch.uint8, (M, K // 64), dev, where, "exps"))
-        _check(_lib.act8_quantize(_ptr(X), M, K, ld, _ptr(codes), _ptr(exps), _ptr(status), st), where)
-    return Act8(codes, exps)
+
+    def call(st):
+        c = _out(codes, (M, K), torch.uint8, dev, where, "codes")
+        e = _out(exps, (M, K // 64), torch.uint8, dev, where, "exps")
+        _check(_lib.act8_quantize(X.data_ptr(), M, K, ld, c.data_ptr(), e.data_ptr(), _word(status, dev, where), st),
+               where)
+        return Act8(c, e)
+    return _run(dev, stream, call)
 
 
 def act8_dequantize(X8, out=None, stream=None):
     """The bf16 values [M, K] an :class:`Act8` stands for (``out`` may have strided rows)."""
     where = "act8_dequantize"
     codes, exps = X8
-    _need(codes.dim() == 2 and codes.is_cuda, ERR_SHAPE, where, "codes is not a CUDA matrix")
+    if codes.dim() != 2 or not codes.is_cuda:
+        _refuse(ERR_SHAPE, where, "codes is not a CUDA matrix")
     M, K = codes.shape
     dev = codes.device
     _act8(X8, M, K, dev, where)
-    with _On(dev, stream) as st:
-        if out is None:
-            out, ld = torch.empty((M, K), dtype=torch.bfloat16, device=dev), K
-        else:
-            ld = _rows(out, where, "out", K, M, dev)[2]
-        _check(_lib.act8_dequantize(_ptr(codes), _ptr(exps), M, K, _ptr(out), ld, st), where)
-    return out
+    ld = K if out is None else _rows(out, where, "out", K, M, dev)[2]
+
+    def call(st):
+        x = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if out is None else out
+        _check(_lib.act8_dequantize(codes.data_ptr(), exps.data_ptr(), M, K, x.data_ptr(), ld, st), where)
+        return x
+    return _run(dev, stream, call)
 
 
 def _act8(X8, M, K, dev, where):
@@ -688,45 +700,47 @@ def _act8(X8, M, K, dev, where):
     _tensor(exps, torch.uint8, (M, K // 64), dev, where, "exps")
 
 
-def _bwd_act8(where, dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, ws_bytes, ws, status, stream, call):
+def _bwd_act8(where, dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, size, ws, status, stream, run):
     """Checks, outputs and workspace shared by the ``*_bwd_act8`` passes."""
     N, K = int(W.n_out), int(W.k_in)
     M = dY.shape[0]
     dev = dY.device
-    _need(A.dim() == 2 and A.shape[0] % G == 0, ERR_SHAPE, where, f"A is {tuple(A.shape)} for {G} members")
+    if dx_dtype not in (DTYPE_BF16, DTYPE_F32):
+        _refuse(ERR_DTYPE, where, f"dx_dtype is {dx_dtype}")
+    if not dY.is_cuda:
+        _refuse(ERR_SHAPE, where, f"dY is on {dev}")
+    if A.dim() != 2 or A.shape[0] % G != 0:
+        _refuse(ERR_SHAPE, where, f"A is {tuple(A.shape)} for {G} members")
     r = A.shape[0] // G
     _tensor(dY, torch.bfloat16, (M, N), dev, where, "dY")
     _act8(X8, M, K, dev, where)
     _tensor(U, torch.float32, (M, G * r), dev, where, "U")
     _tensor(A, torch.bfloat16, (G * r, K), dev, where, "A")
     _tensor(B, torch.bfloat16, (N, r), dev, where, "B")
-    _need(dx_dtype in (DTYPE_BF16, DTYPE_F32), ERR_DTYPE, where, "dx_dtype")
-    _status_word(status, dev, where)
-    with _On(dev, stream) as st:
-        xt = torch.float32 if dx_dtype == DTYPE_F32 else torch.bfloat16
-        dX = torch.empty((M, K), dtype=xt, device=dev) if dX is None else _tensor(dX, xt, (M, K), dev, where, "dX")
-        dA = (torch.empty((G * r, K), dtype=torch.float32, device=dev) if dA is None
-              else _tensor(dA, torch.float32, (G * r, K), dev, where, "dA"))
-        dB = (torch.empty((N, r), dtype=torch.float32, device=dev) if dB is None
-              else _tensor(dB, torch.float32, (N, r), dev, where, "dB"))
-        if ws is None:
-            ws = torch.empty(max(ws_bytes(M, N, K, r), 16), dtype=torch.uint8, device=dev)
+    if W.codes.device != dev:
+        _refuse(ERR_SHAPE, where, f"W is on {W.codes.device}, not {dev}")
+
+    def call(st):
+        x = _out(dX, (M, K), torch.float32 if dx_dtype == DTYPE_F32 else torch.bfloat16, dev, where, "dX")
+        a = _out(dA, (G * r, K), torch.float32, dev, where, "dA")
+        b = _out(dB, (N, r), torch.float32, dev, where, "dB")
         if M == 0:  # nothing to sum; the library's call is a no-op
-            dA.zero_()
-            dB.zero_()
-        else:
-            _check(call(M, r, dX, dA, dB, ws, st), where)
-    return dX, dA, dB
+            a.zero_()
+            b.zero_()
+        at, size_, keep = _workspace(ws, lambda: size(M, N, K, r), dev, where)
+        _check(run(M, r, x.data_ptr(), a.data_ptr(), b.data_ptr(), at, size_, _word(status, dev, where), st), where)
+        return x, a, b
+    return _run(dev, stream, call)
 
 
 def qlora_linear_bwd_act8(dY, X8, U, W, A, B, s, dx_dtype=DTYPE_BF16, dX=None, dA=None, dB=None, ws=None,
                           status=None, stream=None):
     """:func:`qlora_linear_bwd` with the input as its 8-bit checkpoint ``X8``;
     returns ``(dX, dA, dB)``."""
-    def call(M, r, dX, dA, dB, ws, st):
-        return _lib.qlora_linear_bwd_act8(_ptr(dY), _ptr(X8[0]), _ptr(X8[1]), _ptr(U), M, _weight(W), _ptr(A),
-                                          _ptr(B), r, float(s), _ptr(dX), dx_dtype, _ptr(dA), _ptr(dB), _ptr(ws),
-                                          ws.numel(), _ptr(status), st)
+    def call(M, r, dX, dA, dB, ws, size, status, st):
+        return _lib.qlora_linear_bwd_act8(dY.data_ptr(), X8[0].data_ptr(), X8[1].data_ptr(), U.data_ptr(), M,
+                                          _weight(W), A.data_ptr(), B.data_ptr(), r, float(s), dX, dx_dtype, dA, dB,
+                                          ws, size, status, st)
     return _bwd_act8("qlora_linear_bwd_act8", dY, X8, U, W, 1, A, B, dx_dtype, dX, dA, dB,
                      qlora_bwd_workspace_size, ws, status, stream, call)
 
@@ -739,10 +753,10 @@ def qlora_group_bwd_act8(dY, X8, U, W, n_member, A, B, s, dx_dtype=DTYPE_BF16, d
     def size(M, N, K, r):
         return qlora_group_bwd_workspace_size(M, N, K, G, r)
 
-    def call(M, r, dX, dA, dB, ws, st):
-        return _lib.qlora_group_bwd_act8(_ptr(dY), _ptr(X8[0]), _ptr(X8[1]), _ptr(U), M, _weight(W), G,
-                                         ctypes.cast(arr, _P), _ptr(A), _ptr(B), r, float(s), _ptr(dX), dx_dtype,
-                                         _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _ptr(status), st)
+    def call(M, r, dX, dA, dB, ws, size, status, st):
+        return _lib.qlora_group_bwd_act8(dY.data_ptr(), X8[0].data_ptr(), X8[1].data_ptr(), U.data_ptr(), M,
+                                         _weight(W), G, ctypes.cast(arr, _P), A.data_ptr(), B.data_ptr(), r, float(s),
+                                         dX, dx_dtype, dA, dB, ws, size, status, st)
     return _bwd_act8("qlora_group_bwd_act8", dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, size, ws, status, stream,
                      call)
 
@@ -751,11 +765,10 @@ def qlora_linear_bwd_dropout_act8(dY, X8_drop, U, W, A, B, s, p, seed, dx_dtype=
                                   dB=None, ws=None, status=None, stream=None):
     """:func:`qlora_linear_bwd_dropout` with X_drop as its 8-bit checkpoint (same
     ``p`` and ``seed`` as the forward)."""
-    def call(M, r, dX, dA, dB, ws, st):
-        return _lib.qlora_linear_bwd_dropout_act8(_ptr(dY), _ptr(X8_drop[0]), _ptr(X8_drop[1]), _ptr(U), M,
-                                                  _weight(W), _ptr(A), _ptr(B), r, float(s), float(p), int(seed),
-                                                  _ptr(dX), dx_dtype, _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(),
-                                                  _ptr(status), st)
+    def call(M, r, dX, dA, dB, ws, size, status, st):
+        return _lib.qlora_linear_bwd_dropout_act8(dY.data_ptr(), X8_drop[0].data_ptr(), X8_drop[1].data_ptr(),
+                                                  U.data_ptr(), M, _weight(W), A.data_ptr(), B.data_ptr(), r, float(s),
+                                                  float(p), int(seed), dX, dx_dtype, dA, dB, ws, size, status, st)
     return _bwd_act8("qlora_linear_bwd_dropout_act8", dY, X8_drop, U, W, 1, A, B, dx_dtype, dX, dA, dB,
                      qlora_bwd_dropout_workspace_size, ws, status, stream, call)
 
@@ -798,24 +811,28 @@ def _head(head, dev, where):
         return _Head(head.data_ptr(), ld, None, None, None, None, V, D), V, D, False
     V, D = int(head.n_out), int(head.k_in)
     mean = getattr(head, "mean", None)
-    _need(head.codes.device == dev, ERR_SHAPE, where, f"head is on {head.codes.device}, not {dev}")
+    if head.codes.device != dev:
+        _refuse(ERR_SHAPE, where, f"head is on {head.codes.device}, not {dev}")
     return _Head(None, 0, head.codes.data_ptr(), head.c8.data_ptr(), head.s2.data_ptr(),
                  None if mean is None else mean.data_ptr(), V, D), V, D, True
 
 
-def _head_call(where, op, H, head, labels, ws, status):
+def _head_call(where, op, H, head, labels):
+    """The checked problem: tokens, width, H's row stride, device, head, workspace query."""
     T, D, ldh = _rows(H, where, "H")
     dev = H.device
     h, V, dim, nf4 = _head(head, dev, where)
-    _need(dim == D, ERR_SHAPE, where, f"H has {D} columns, the head {dim}")
-    _vector(labels, torch.int64, T, dev, where, "labels")
-    _status_word(status, dev, where)
-    size = qlora_head_loss_workspace_size(T, V, D, nf4, op) if ws is None else 0
-    return T, D, ldh, dev, h, size
+    if dim != D:
+        _refuse(ERR_SHAPE, where, f"H has {D} columns, the head {dim}")
+    _tensor(labels, torch.int64, (T,), dev, where, "labels")
+    return T, D, ldh, dev, h, lambda: qlora_head_loss_workspace_size(T, V, D, nf4, op)
 
 
-def _out(t, shape, dtype, dev, where, name):
-    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _tensor(t, dtype, shape, dev, where, name)
+def _grad_out(dH, T, D, dev, where):
+    """(row stride of dH, maker of dH)."""
+    if dH is None:
+        return D, lambda: torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+    return _rows(dH, where, "dH", D, T, dev)[2], lambda: dH
 
 
 def qlora_head_loss_fwd(H, head, labels, ignore_index=IGNORE_INDEX, loss=None, lse=None, stats=None, ws=None,
@@ -826,16 +843,18 @@ def qlora_head_loss_fwd(H, head, labels, ignore_index=IGNORE_INDEX, loss=None, l
     label is ``ignore_index``), log-sum-exps (keep them for the backward), and
     the mean over the tokens that count with their number."""
     where = "qlora_head_loss_fwd"
-    T, D, ldh, dev, h, size = _head_call(where, HEAD_FWD, H, head, labels, ws, status)
-    with _On(dev, stream) as st:
-        loss = _out(loss, (T,), torch.float32, dev, where, "loss")
-        lse = _out(lse, (T,), torch.float32, dev, where, "lse")
-        stats = _out(stats, (2,), torch.float32, dev, where, "stats")
-        if ws is None:
-            ws = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
-        _check(_lib.qlora_head_loss_fwd(_ptr(H), ldh, T, h, _ptr(labels), int(ignore_index), _ptr(loss), _ptr(lse),
-                                        _ptr(stats), _ptr(ws), ws.numel(), _ptr(status), st), where)
-    return loss, lse, stats
+    T, D, ldh, dev, h, size = _head_call(where, HEAD_FWD, H, head, labels)
+
+    def call(st):
+        lo = _out(loss, (T,), torch.float32, dev, where, "loss")
+        ls = _out(lse, (T,), torch.float32, dev, where, "lse")
+        sm = _out(stats, (2,), torch.float32, dev, where, "stats")
+        at, bytes_, keep = _workspace(ws, size, dev, where)
+        _check(_lib.qlora_head_loss_fwd(H.data_ptr(), ldh, T, h, labels.data_ptr(), int(ignore_index), lo.data_ptr(),
+                                        ls.data_ptr(), sm.data_ptr(), at, bytes_, _word(status, dev, where), st),
+               where)
+        return lo, ls, sm
+    return _run(dev, stream, call)
 
 
 def qlora_head_loss_bwd(H, head, labels, lse, dloss, stats=None, ignore_index=IGNORE_INDEX, dH=None, ws=None,
@@ -844,21 +863,21 @@ def qlora_head_loss_bwd(H, head, labels, lse, dloss, stats=None, ignore_index=IG
     [T, dim]): ``dloss`` [T] holds the gradient of every token's loss, or, with
     the forward's ``stats`` given, ``dloss`` [1] the gradient of the mean."""
     where = "qlora_head_loss_bwd"
-    T, D, ldh, dev, h, size = _head_call(where, HEAD_BWD, H, head, labels, ws, status)
-    _vector(lse, torch.float32, T, dev, where, "lse")
-    _vector(dloss, torch.float32, T if stats is None else 1, dev, where, "dloss")
+    T, D, ldh, dev, h, size = _head_call(where, HEAD_BWD, H, head, labels)
+    _tensor(lse, torch.float32, (T,), dev, where, "lse")
+    _tensor(dloss, torch.float32, (T if stats is None else 1,), dev, where, "dloss")
     if stats is not None:
-        _vector(stats, torch.float32, 2, dev, where, "stats")
-    with _On(dev, stream) as st:
-        if dH is None:
-            dH, ldd = torch.empty((T, D), dtype=torch.bfloat16, device=dev), D
-        else:
-            ldd = _rows(dH, where, "dH", D, T, dev)[2]
-        if ws is None:
-            ws = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
-        _check(_lib.qlora_head_loss_bwd(_ptr(H), ldh, T, h, _ptr(labels), int(ignore_index), _ptr(lse), _ptr(dloss),
-                                        _ptr(stats), _ptr(dH), ldd, _ptr(ws), ws.numel(), _ptr(status), st), where)
-    return dH
+        _tensor(stats, torch.float32, (2,), dev, where, "stats")
+    ldd, grad = _grad_out(dH, T, D, dev, where)
+
+    def call(st):
+        g = grad()
+        at, bytes_, keep = _workspace(ws, size, dev, where)
+        _check(_lib.qlora_head_loss_bwd(H.data_ptr(), ldh, T, h, labels.data_ptr(), int(ignore_index), lse.data_ptr(),
+                                        dloss.data_ptr(), None if stats is None else stats.data_ptr(), g.data_ptr(),
+                                        ldd, at, bytes_, _word(status, dev, where), st), where)
+        return g
+    return _run(dev, stream, call)
 
 
 def qlora_head_loss_step(H, head, labels, weight=None, scale=1.0, ignore_index=IGNORE_INDEX, loss=None, lse=None,
@@ -867,20 +886,20 @@ def qlora_head_loss_step(H, head, labels, weight=None, scale=1.0, ignore_index=I
     dH)``.  ``dH`` is the gradient of ``scale`` times the mean loss, or, with
     ``weight`` (fp32 [T]), of ``scale * sum(weight * loss)``."""
     where = "qlora_head_loss_step"
-    T, D, ldh, dev, h, size = _head_call(where, HEAD_STEP, H, head, labels, ws, status)
+    T, D, ldh, dev, h, size = _head_call(where, HEAD_STEP, H, head, labels)
     if weight is not None:
-        _vector(weight, torch.float32, T, dev, where, "weight")
-    with _On(dev, stream) as st:
-        loss = _out(loss, (T,), torch.float32, dev, where, "loss")
-        lse = _out(lse, (T,), torch.float32, dev, where, "lse")
-        stats = _out(stats, (2,), torch.float32, dev, where, "stats")
-        if dH is None:
-            dH, ldd = torch.empty((T, D), dtype=torch.bfloat16, device=dev), D
-        else:
-            ldd = _rows(dH, where, "dH", D, T, dev)[2]
-        if ws is None:
-            ws = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
-        _check(_lib.qlora_head_loss_step(_ptr(H), ldh, T, h, _ptr(labels), int(ignore_index), _ptr(weight),
-                                         float(scale), _ptr(loss), _ptr(lse), _ptr(stats), _ptr(dH), ldd, _ptr(ws),
-                                         ws.numel(), _ptr(status), st), where)
-    return loss, lse, stats, dH
+        _tensor(weight, torch.float32, (T,), dev, where, "weight")
+    ldd, grad = _grad_out(dH, T, D, dev, where)
+
+    def call(st):
+        lo = _out(loss, (T,), torch.float32, dev, where, "loss")
+        ls = _out(lse, (T,), torch.float32, dev, where, "lse")
+        sm = _out(stats, (2,), torch.float32, dev, where, "stats")
+        g = grad()
+        at, bytes_, keep = _workspace(ws, size, dev, where)
+        _check(_lib.qlora_head_loss_step(H.data_ptr(), ldh, T, h, labels.data_ptr(), int(ignore_index),
+                                         None if weight is None else weight.data_ptr(), float(scale), lo.data_ptr(),
+                                         ls.data_ptr(), sm.data_ptr(), g.data_ptr(), ldd, at, bytes_,
+                                         _word(status, dev, where), st), where)
+        return lo, ls, sm, g
+    return _run(dev, stream, call)

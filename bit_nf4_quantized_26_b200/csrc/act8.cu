@@ -124,6 +124,8 @@ __global__ void __launch_bounds__(kActThreads) act8_dequantize_kernel(const uint
 // copies bring 64 tokens x 128 codes (8 KB), four warps write them as the
 // MN-major 128-byte-swizzled tile the tensor core reads.  Two rings: three
 // stages of copies (24 KB) and two dequantised tiles (16 KB), two CTAs per SM.
+// Summed as DU and DB are (skinny.cu): two accumulators of eight stages each
+// in turn, joined in registers.
 struct ActDaPlan {
   static constexpr uint32_t kA = 16384;    // dU hi/lo: 64 tokens x 128 columns
   static constexpr uint32_t kRaw = 8192;   // codes: 64 tokens x 128 features
@@ -134,6 +136,7 @@ struct ActDaPlan {
   static constexpr uint32_t kTileOff = kCopies * kCopy;
   static constexpr uint32_t kBarOff = kTileOff + kTiles * kB;
   static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
+  static constexpr int kSumStages = 8;
   static constexpr int kLd = 132;  // floats per row of the parked partial tile
   static_assert(2 * kSmem <= 232448u, "two CTAs per SM");
   static_assert(64 * kLd * 4 <= kTileOff, "the partial tile lies in the copy ring");
@@ -149,8 +152,10 @@ __global__ void __launch_bounds__(192, 2)
   uint64_t* empty = full + P::kCopies;                              // copies read (by the MMAs)
   uint64_t* bfull = empty + P::kCopies;                             // tile dequantised
   uint64_t* bempty = bfull + P::kTiles;                             // tile read
-  uint64_t* accf = bempty + P::kTiles;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
+  uint64_t* accf = bempty + P::kTiles;                              // accumulator final
+  uint64_t* acce = accf + 2;                                        // accumulator read
+  uint64_t* done = acce + 2;                                        // the last commit of an aborted CTA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -172,7 +177,11 @@ __global__ void __launch_bounds__(192, 2)
       mbar_init(&bfull[s], 4);
       mbar_init(&bempty[s], 1);
     }
-    mbar_init(accf, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], 4);
+    }
+    mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -181,7 +190,7 @@ __global__ void __launch_bounds__(192, 2)
     tma_prefetch_desc(&tm_x);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 128);
+    tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -215,7 +224,9 @@ __global__ void __launch_bounds__(192, 2)
       bool aborted = false;
       for (int t = 0; t < T; ++t) {
         const uint32_t s = t % P::kCopies, b = t % P::kTiles;
-        if (!mbar_wait(&full[s], (t / P::kCopies) & 1, wc) || !mbar_wait(&bfull[b], (t / P::kTiles) & 1, wc)) {
+        const int ch = t / P::kSumStages, buf = ch & 1;
+        if ((t % P::kSumStages == 0 && ch >= 2 && !mbar_wait(&acce[buf], ((ch >> 1) - 1) & 1, wc)) ||
+            !mbar_wait(&full[s], (t / P::kCopies) & 1, wc) || !mbar_wait(&bfull[b], (t / P::kTiles) & 1, wc)) {
           aborted = true;
           break;
         }
@@ -224,12 +235,16 @@ __global__ void __launch_bounds__(192, 2)
         const uint64_t bd = sdesc_sw128(smem_u32(smem + P::kTileOff + b * P::kB), 8192, 1024);
 #pragma unroll
         for (uint32_t kk = 0; kk < 4; ++kk)  // 16 tokens = 16 rows of 128 bytes
-          umma_bf16(tmem_d, ad + kk * (2048u >> 4), bd + kk * (2048u >> 4), idesc, (t | kk) != 0 ? 1u : 0u);
+          umma_bf16(tmem_d + buf * 128, ad + kk * (2048u >> 4), bd + kk * (2048u >> 4), idesc,
+                    (t % P::kSumStages | kk) != 0 ? 1u : 0u);
         umma_commit(&empty[s]);
         umma_commit(&bempty[b]);
+        if (t % P::kSumStages == P::kSumStages - 1 || t == T - 1) umma_commit(&accf[buf]);
       }
-      umma_commit(accf);
-      if (aborted) mbar_drain(accf, 0, a.status);
+      if (aborted) {
+        umma_commit(done);
+        mbar_drain(done, 0, a.status);
+      }
     }
   } else {
     // ---------------------------------------------------- dequantiser warps
@@ -250,14 +265,46 @@ __global__ void __launch_bounds__(192, 2)
       }
     };
     fetch(0);
+    // TMEM row c = 32 q + lane holds part (lane / 16) of j = 16 q + lane % 16;
+    // of the 128 joined columns lanes 0-15 keep the first half, 16-31 the rest.
+    const int q = warp & 3;
+    float sum[64] = {};
+    auto add_chunk = [&](int ch) {
+      const int buf = ch & 1;
+      if (!mbar_wait_warp(&accf[buf], (ch >> 1) & 1, wc)) return false;
+      tc_fence_after();
+      const uint32_t tq = tmem_d + buf * 128 + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+      for (int cb = 0; cb < 4; ++cb) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tq + cb * 32, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float x = __uint_as_float(v[i]);
+          const float both = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));  // hi + lo
+          if ((lane >= 16) == (cb >= 2)) sum[(cb & 1) * 32 + i] = __fadd_rn(sum[(cb & 1) * 32 + i], both);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acce[buf]);
+      return true;
+    };
+    bool ok = true;
     for (int t = 0; t < T; ++t) {
+      // the chunk before last is final, or nearly: two are in flight
+      if (t % P::kSumStages == 2 && t > P::kSumStages && !(ok = add_chunk(t / P::kSumStages - 1))) break;
       const uint32_t s = t % P::kCopies, b = t % P::kTiles;
       float sc[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[i] = exp_scale(pe[i]);
       fetch(t + 1);
-      if (!mbar_wait_all(&full[s], (t / P::kCopies) & 1, wc)) break;
-      if (t >= static_cast<int>(P::kTiles) && !mbar_wait_all(&bempty[b], ((t / P::kTiles) - 1) & 1, wc)) break;
+      if (!mbar_wait_all(&full[s], (t / P::kCopies) & 1, wc) ||
+          (t >= static_cast<int>(P::kTiles) && !mbar_wait_all(&bempty[b], ((t / P::kTiles) - 1) & 1, wc))) {
+        ok = false;
+        break;
+      }
       const uint8_t* raw = smem + s * P::kCopy + P::kA;
       uint8_t* tile = smem + P::kTileOff + b * P::kB + (cu >> 2) * 8192;  // 64-feature atom
 #pragma unroll
@@ -276,31 +323,20 @@ __global__ void __launch_bounds__(192, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bfull[b]);
     }
-    // ------------------------------------------------ TMEM -> partial tile
-    // TMEM row c = 32 q + lane holds part (lane / 16) of j = 16 q + lane % 16.
-    const int q = warp & 3;
-    float* part = reinterpret_cast<float*>(smem);  // the copy ring is idle once accf completes
-    if (mbar_wait_warp(accf, 0, wc)) {
-      tc_fence_after();
-      const uint32_t tq = tmem_d + (static_cast<uint32_t>(q * 32) << 16);
-      const int j = 16 * q + lane;
-      const bool jok = lane < 16 && j < rw;
-      for (int cb = 0; cb < 4; ++cb) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(tq + cb * 32, v);
-        tmem_ld_wait();
-        if (T <= 0)
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-        float sum[32];
+    // -------------------------------------------------- sums -> partial tile
+    if (ok && T > 0) {  // the chunks the loop did not reach: the last, and the one before a short last
+      const int last = (T - 1) / P::kSumStages;
+      const int first = last - ((last > 0 && (T - 1) % P::kSumStages < 2) ? 1 : 0);
+      for (int ch = first; ok && ch <= last; ++ch) ok = add_chunk(ch);
+    }
+    if (ok) {  // the copy ring is idle: its last stage's MMAs are done
+      float* part = reinterpret_cast<float*>(smem);
+      const int j = 16 * q + (lane & 15);
+      if (j < rw) {
+        float* dst = part + j * P::kLd + (lane >> 4) * 64;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          sum[i] = __uint_as_float(v[i]) + __shfl_down_sync(0xFFFFFFFFu, __uint_as_float(v[i]), 16);
-        if (jok) {
-          float* dst = part + j * P::kLd + cb * 32;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
-        }
+        for (int i = 0; i < 64; i += 4)
+          *reinterpret_cast<float4*>(dst + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
       }
     }
   }
@@ -336,7 +372,7 @@ __global__ void __launch_bounds__(192, 2)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_d, 128);
+    tmem_dealloc(tmem_d, 256);
   }
 }
 

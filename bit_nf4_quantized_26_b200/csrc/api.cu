@@ -966,7 +966,7 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
   {
     ProfScope ps(kKDU, cs);
     if (qlora_status st =
-            from_cuda(launch_skinny(kSkDU, mdy128, mbl, sa, static_cast<int>(cdiv(M, 128)) * Gs, p.s_du, cs)))
+            from_cuda(launch_skinny(kSkDU, mdy128, mbl, sa, static_cast<int>(cdiv(M, 128)) * Gs, p.s_du, cs, !X.x)))
       return st;
   }
 
@@ -1054,7 +1054,7 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
     ProfScope ps(kKDB, side);
     if (qlora_status st =
             from_cuda(launch_skinny(kSkDB, mdy64, msu, sa, static_cast<int>(cdiv(N, 128)) * (chunks ? Gs : 1), p.s_db,
-                                    side)))
+                                    side, !X.x)))
       return st;
   }
 
@@ -1330,9 +1330,29 @@ qlora_status qlora_linear_bwd_dropout_act8(const uint16_t* dY, const uint8_t* co
 struct HeadPlanHost {
   int64_t piece = 0;  // vocabulary rows per piece (a multiple of the tile)
   int64_t pieces = 0;
+  int64_t splits = 1, kper = 0;  // slices of a piece's dH contraction, 64-deep stages each
   size_t off_cnt = 0, off_z = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_sum = 0, off_pl = 0;
   size_t off_g = 0, off_acc = 0, off_w = 0, total = 0;
 };
+
+// Slices of the dH contraction of a piece (kst stages) over `tiles` tiles of
+// 74 CTA pairs: waves x (stages per slice + what a slice's fp32 sums cost to
+// write and join, about 12 stages' time), slices of at least 8 stages, only
+// while all slices together are under four waves (beyond that the sums cost
+// more than the last wave's idle pairs).
+static void head_splits(int64_t tiles, int64_t kst, int64_t& splits, int64_t& per) {
+  constexpr int64_t kPairs = kSms / 2, kCost = 12;
+  int64_t best = 1, cost = cdiv(tiles, kPairs) * kst;
+  for (int64_t s = 2; s <= kst / 8 && tiles * s <= 4 * kPairs; ++s) {
+    const int64_t c = cdiv(tiles * s, kPairs) * (cdiv(kst, s) + kCost);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  per = cdiv(kst, best);
+  splits = cdiv(kst, per);
+}
 
 static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op) {
   HeadPlanHost p;
@@ -1350,6 +1370,7 @@ static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op)
   p.pieces = cdiv(vt * tile, piece);
   p.piece = cdiv(vt, p.pieces) * tile;  // even pieces
   p.pieces = cdiv(vt * tile, p.piece);
+  if (op != QLORA_HEAD_FWD) head_splits(mt * cdiv(D, tile), p.piece / 64, p.splits, p.kper);
   size_t off = 0;
   auto take = [&off](size_t bytes) {
     const size_t at = off;
@@ -1358,10 +1379,10 @@ static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op)
   };
   const size_t t = static_cast<size_t>(T);
   if (op != QLORA_HEAD_BWD) {
-    const int64_t part_tiles = op == QLORA_HEAD_FWD ? vt : p.piece / tile;
+    const int64_t parts = 2 * (op == QLORA_HEAD_FWD ? vt : p.piece / tile);
     p.off_cnt = take(8);
     p.off_z = take(4 * t);
-    p.off_part = take(8 * t * static_cast<size_t>(part_tiles));
+    p.off_part = take(8 * t * static_cast<size_t>(parts));
     p.off_bsum = take(8 * static_cast<size_t>(head_combine_blocks(T)));
   }
   if (op == QLORA_HEAD_STEP) {
@@ -1372,7 +1393,8 @@ static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op)
   }
   if (op != QLORA_HEAD_FWD) {
     p.off_g = take(2 * t * static_cast<size_t>(p.piece));
-    if (p.pieces > 1) p.off_acc = take(4 * static_cast<size_t>(mt * tile) * static_cast<size_t>(cdiv(D, tile) * tile));
+    if (p.pieces > 1 || p.splits > 1)
+      p.off_acc = take(4 * static_cast<size_t>(p.splits * mt * tile) * static_cast<size_t>(cdiv(D, tile) * tile));
   }
   if (nf4) p.off_w = take(2 * static_cast<size_t>(std::min(p.piece, V)) * static_cast<size_t>(D));
   p.total = off;
@@ -1383,7 +1405,7 @@ static qlora_status check_head_shape(int64_t T, int64_t V, int64_t D, bool nf4) 
   const int64_t big = int64_t(1) << 31;
   if (T < 0 || T >= big - kHeadTile || V < 1 || V >= big - kHeadTile) return QLORA_ERR_SHAPE;
   if (D < 8 || D > (int64_t(1) << 20) || D % (nf4 ? 64 : 8) != 0 || V * D >= (int64_t(1) << 40)) return QLORA_ERR_SHAPE;
-  // tiles of every product are counted in 32 bits
+  // tiles of every product (and of its slices) are counted in 32 bits
   if (cdiv(T, kHeadTile) * cdiv(std::max(V, D), kHeadTile) >= big / 64) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
@@ -1506,15 +1528,18 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     a.ncols = static_cast<int>(pv);
     a.ntiles = static_cast<int>(cdiv(pv, kHeadTile));
     a.kst = static_cast<int>(cdiv(D, 64));
+    a.kchunk = 8;
+    a.splits = 1;
+    a.kper = a.kst;
     float2* part = reinterpret_cast<float2*>(at(p.off_part));
-    a.part = op == QLORA_HEAD_FWD ? part + v0 / kHeadTile * T : part;
+    a.part = op == QLORA_HEAD_FWD ? part + v0 / kHeadTile * 2 * T : part;
     {
       const int mode = op == QLORA_HEAD_FWD ? kHeadLoss : op == QLORA_HEAD_BWD ? kHeadProb : kHeadExp;
       ProfScope ps(kKHeadLogits, cs);
       if (qlora_status st = from_cuda(launch_head_gemm(mode, mh, mw, a, cs))) return st;
     }
     if (op == QLORA_HEAD_STEP || (op == QLORA_HEAD_FWD && last)) {
-      cb.ntiles = op == QLORA_HEAD_FWD ? static_cast<int>(cdiv(V, kHeadTile)) : a.ntiles;
+      cb.nparts = 2 * (op == QLORA_HEAD_FWD ? static_cast<int>(cdiv(V, kHeadTile)) : a.ntiles);
       cb.first = op == QLORA_HEAD_FWD || first;
       cb.last = last;
       if (op == QLORA_HEAD_STEP) {
@@ -1533,6 +1558,9 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
       d.ncols = static_cast<int>(D);
       d.ntiles = static_cast<int>(cdiv(D, kHeadTile));
       d.kst = static_cast<int>(cdiv(pv, 64));
+      d.splits = static_cast<int>(p.splits);  // of every piece: their sums run through the pieces
+      d.kper = static_cast<int>(cdiv(d.kst, p.splits));
+      d.kchunk = d.kper;
       d.first = first;
       d.last = last;
       d.acc = reinterpret_cast<float*>(at(p.off_acc));
@@ -1550,6 +1578,8 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
       }
       ProfScope ps(kKHeadGrad, cs);
       if (qlora_status st = from_cuda(launch_head_gemm(kHeadGrad, mg, mwt, d, cs))) return st;
+      if (last && d.splits > 1)
+        if (qlora_status st = from_cuda(launch_head_finish(d, cs))) return st;
     }
   }
   return QLORA_OK;

@@ -10,11 +10,11 @@
 // kernel on CTA pairs makes every product; what its epilogue does with a tile
 // is the mode:
 //
-//   Loss  per row and tile the maximum m and sum exp(l - m): 8 bytes per 256 logits
+//   Loss  per row and 128 columns the maximum m and sum exp(l - m): 8 bytes
 //   Prob  exp(l - lse), less 1 at the label (in fp32), rounded to bf16
 //   Exp   exp(l - ref), 0 at the label, rounded to bf16, and (ref, sum): the
-//         gradient's operand before lse is known.  ref is 0 while the tile's
-//         maximum lies within +-40 (exp then stays far inside bf16's and
+//         gradient's operand before lse is known.  ref is 0 while the maximum
+//         of the row's 128 columns lies within +-40 (exp then stays far inside bf16's and
 //         fp32's range, and the reference costs no precision: both types
 //         float), else that maximum
 //   Grad  (second product) the piece's bf16 [T, piece] operand times W's rows
@@ -48,9 +48,11 @@ struct HeadPlan {
   static_assert(kSmem <= 232448u, "too much shared memory");
 };
 
-// Warp 0: copies; warp 1: MMAs (leader CTA); warps 2..5: epilogue.
-constexpr int kHeadThreads = 192;
-constexpr int kEpiWarps = 4;
+// Warp 0: copies; warp 1: MMAs (leader CTA); warps 2..9: epilogue (two per
+// quarter of the rows, each with half of the columns).
+constexpr int kEpiWarps = 8;
+constexpr int kHeadThreads = 64 + 32 * kEpiWarps;
+constexpr int kHalf = kHeadTile / 2;  // columns an epilogue thread holds
 constexpr int kGroupM = 8;  // token tiles walked together (raster)
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -73,25 +75,45 @@ __device__ __forceinline__ bool counts(int64_t label, int64_t ignore, int64_t vo
   return label != ignore && label >= 0 && label < vocab;
 }
 
-// 32 columns of the accumulator, fp32 bits; columns >= nv become -inf.
-__device__ __forceinline__ void load_logits(uint32_t taddr, int nv, float (&l)[32]) {
-  uint32_t v[32];
-  tmem_ld_32x32b_x32(taddr, v);
-  tmem_ld_wait();
+// 32 lanes x 16 consecutive 32-bit columns of tensor memory.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Adds this thread's 128 columns of a finished accumulator to its registers
+// (16 at a time: 128 sums leave few registers beside them).
+__device__ __forceinline__ void add_chunk(uint32_t taddr, bool first, float (&l)[kHalf]) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) l[j] = __uint_as_float(v[j]);
-  if (nv < 32) {
+  for (int cb = 0; cb < kHalf / 16; ++cb) {
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(taddr + cb * 16, v);
+    tmem_ld_wait();
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j >= nv) l[j] = -INFINITY;
+    for (int j = 0; j < 16; ++j) {
+      const float x = __uint_as_float(v[j]);
+      l[cb * 16 + j] = first ? x : __fadd_rn(l[cb * 16 + j], x);
+    }
   }
 }
 
-__device__ __forceinline__ float max32(const float (&l)[32]) {
+__device__ __forceinline__ float max_all(const float (&l)[kHalf]) {
   float m[4] = {l[0], l[1], l[2], l[3]};
 #pragma unroll
-  for (int j = 4; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], l[j]);
+  for (int j = 4; j < kHalf; ++j) m[j & 3] = fmaxf(m[j & 3], l[j]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Element `at` of l (0 if there is none there).
+__device__ __forceinline__ float pick(const float (&l)[kHalf], int at) {
+  float z = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kHalf; ++j) z = j == at ? l[j] : z;
+  return z;
 }
 
 // 32 bf16 (64 bytes, 16-byte aligned) from fp32; `n` valid (a multiple of 8).
@@ -102,6 +124,33 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32
       reinterpret_cast<uint4*>(dst)[j] =
           make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
                      pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+}
+
+// 128 bf16 (16-byte aligned) from fp32.
+__device__ __forceinline__ void store_bf16(uint16_t* dst, const float (&v)[kHalf]) {
+#pragma unroll
+  for (int j = 0; j < kHalf / 8; ++j)
+    reinterpret_cast<uint4*>(dst)[j] =
+        make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                   pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+}
+
+// fp32 sums between pieces and of split contractions: per (split, tile) and
+// CTA, the epilogue threads' registers as 32 rows of 256 float4, so that every
+// access of a warp is 512 contiguous bytes.
+constexpr int kSumStride = 32 * kEpiWarps;             // float4 per row
+constexpr int kSumBlock = kHalf / 4 * kSumStride;      // float4 per CTA of a tile
+
+// dH_t = ca * (the row's sum over the vocabulary) + cl * W[label].
+__device__ __forceinline__ void grad_row_factors(const HeadArgs& a, int t, float& ca, float& cl) {
+  if (a.row_sum) {
+    const float g = a.weight ? a.scale * __ldcg(a.weight + t) : a.scale / static_cast<float>(__ldcg(a.count));
+    ca = g / __ldcg(a.row_sum + t);
+    cl = g * __ldcg(a.p_label + t);
+  } else {
+    ca = a.stats ? __ldcg(a.dloss) / __ldcg(a.stats + 1) : __ldcg(a.dloss + t);
+    cl = 0.0f;
+  }
 }
 
 // Columns d .. d + 31 of row `row` of the head as fp32 (`n` valid, a multiple of 8).
@@ -133,18 +182,43 @@ __device__ __forceinline__ void load_head_row(const qlora_head& h, const Nf4Tabl
   }
 }
 
+// Columns d .. d + 31 (`n` of them valid) of dH's row t from its sums l.
+__device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t label, bool counted, float ca, float cl,
+                                             int d, int n, float (&l)[32]) {
+  if (!counted) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) l[j] = 0.0f;
+  } else if (a.row_sum) {
+    float w[32];
+    load_head_row(a.head, a.tab, label, d, n, w);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) l[j] = fmaf(cl, w[j], ca * l[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) l[j] *= ca;
+  }
+  store_bf16x32(a.dh + static_cast<int64_t>(t) * a.ldd + d, l, n);
+}
+
 }  // namespace
 
 // A cluster of two CTAs computes 256 tokens x 256 columns per tile: each CTA
 // holds 128 token rows (A) and half of the columns (B) of a 64-deep stage, one
 // thread of the leader issues M = 256, N = 256 MMAs, and each CTA's tensor
-// memory gets its 128 rows.  Two accumulators: the epilogue of a tile runs
-// beside the next tile's MMAs.  Persistent: one pair per TPC.
+// memory gets its 128 rows.  Persistent: one pair per TPC.
+//
+// The tensor core truncates when it adds to its fp32 accumulator: the sum
+// drifts towards zero by about 2^-24 of itself per K = 16 step (measured:
+// -8e-7 relative at dim 1024, -8e-6 at 8192, on random data).  A tile's
+// contraction is therefore cut into chunks (512 deep for logits: 32 steps)
+// that alternate between two accumulators, and the epilogue threads add each
+// finished one to their registers, rounding to nearest, while the next runs.
+// dH, rounded to bf16, takes a whole slice of its contraction as one chunk.
 //
 // Barriers: full[s] (leader: both CTAs' tiles landed), empty[s] (both: the
-// stage's MMAs are done), accf[b] (both: accumulator final), acce[b] (leader:
-// all epilogue warps of both CTAs have read it), done (leader: the last
-// commit).  What an earlier kernel of the same call wrote is read past L1
+// stage's MMAs are done), accf[b] (both: the chunk's accumulator is final),
+// acce[b] (leader: all epilogue warps of both CTAs have read it), done
+// (leader: the last commit).  What an earlier kernel of the same call wrote is read past L1
 // (__ldcg): launches overlap, and nothing is kept there from one to the next.
 template <int MODE>
 __global__ void __launch_bounds__(kHeadThreads, 1)
@@ -164,7 +238,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tiles = a.mtiles * a.ntiles;
+  const int mn = a.mtiles * a.ntiles;
+  const int tiles = mn * (MODE == kHeadGrad ? a.splits : 1);  // (split, tile)
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < P::kStages; ++s) {
@@ -205,10 +280,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       bool ok = true;
       for (int tile = pair; ok && tile < tiles; tile += pairs) {
         int m, n;
-        head_tile(tile, a.mtiles, a.ntiles, m, n);
+        const int split = tile / mn;
+        head_tile(tile - split * mn, a.mtiles, a.ntiles, m, n);
         const int arow = m * kHeadTile + static_cast<int>(rank) * 128;
         const int bcol = n * kHeadTile + static_cast<int>(rank) * 128;
-        for (int kt = 0; kt < a.kst; ++kt, ++it) {
+        const int k1 = min(a.kst, (split + 1) * a.kper);
+        for (int kt = split * a.kper; kt < k1; ++kt, ++it) {
           const uint32_t s = static_cast<uint32_t>(it % P::kStages);
           const uint32_t u = static_cast<uint32_t>(it / P::kStages);
           if (it >= P::kStages && !mbar_wait(&empty[s], (u - 1) & 1, wc)) {
@@ -238,32 +315,40 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       constexpr uint32_t idesc = idesc_bf16_f32(256, 256, 0, MODE == kHeadGrad ? 1 : 0);
       constexpr uint32_t b_step = MODE == kHeadGrad ? (2048u >> 4) : (32u >> 4);
       int64_t it = 0;
-      int acc = 0;
+      int acc = 0;  // chunks begun
       bool ok = true;
-      for (int tile = pair; ok && tile < tiles; tile += pairs, ++acc) {
-        const int buf = acc & 1;
-        if (acc >= 2 && !mbar_wait_all(&acce[buf], ((acc >> 1) - 1) & 1, wc)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_d + buf * 256;
-        for (int kt = 0; kt < a.kst; ++kt, ++it) {
-          const uint32_t s = static_cast<uint32_t>(it % P::kStages);
-          if (!mbar_wait_all(&full[s], static_cast<uint32_t>(it / P::kStages) & 1, wc)) {
+      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+        const int split = tile / mn;
+        const int kn = min(a.kst, (split + 1) * a.kper) - split * a.kper;
+        for (int k0 = 0; ok && k0 < kn; k0 += a.kchunk, ++acc) {
+          const int buf = acc & 1;
+          if (acc >= 2 && !mbar_wait_all(&acce[buf], ((acc >> 1) - 1) & 1, wc)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * P::kStage);
-          const uint64_t ad = sdesc_sw128(sa, 16, 1024);
-          const uint64_t bd = MODE == kHeadGrad ? sdesc_sw128(sa + P::kA, 8192, 1024)
-                                                : sdesc_sw128(sa + P::kA, 16, 1024);
-          if (elect_one()) {
+          const uint32_t d = tmem_d + buf * 256;
+          const int kc = min(a.kchunk, kn - k0);
+          for (int kt = 0; kt < kc; ++kt, ++it) {
+            const uint32_t s = static_cast<uint32_t>(it % P::kStages);
+            if (!mbar_wait_all(&full[s], static_cast<uint32_t>(it / P::kStages) & 1, wc)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + s * P::kStage);
+            const uint64_t ad = sdesc_sw128(sa, 16, 1024);
+            const uint64_t bd = MODE == kHeadGrad ? sdesc_sw128(sa + P::kA, 8192, 1024)
+                                                  : sdesc_sw128(sa + P::kA, 16, 1024);
+            if (elect_one()) {
 #pragma unroll
-            for (uint32_t kk = 0; kk < 4; ++kk)
-              umma_bf16_pair(d, ad + kk * 2, bd + kk * b_step, idesc, (kt | static_cast<int>(kk)) != 0 ? 1u : 0u);
-            umma_commit_pair(&empty[s], 0x3);
-            if (kt == a.kst - 1) umma_commit_pair(&accf[buf], 0x3);
+              for (uint32_t kk = 0; kk < 4; ++kk)
+                umma_bf16_pair(d, ad + kk * 2, bd + kk * b_step, idesc, (kt | static_cast<int>(kk)) != 0 ? 1u : 0u);
+              umma_commit_pair(&empty[s], 0x3);
+              if (kt == kc - 1) umma_commit_pair(&accf[buf], 0x3);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       if (elect_one()) {
@@ -274,174 +359,138 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;  // TMEM lanes 32 q ..
+    const int q = warp & 3;             // TMEM lanes 32 q ..
+    const int half = (warp - 2) >> 2;   // columns 128 half ..
     const int et = threadIdx.x - 64;
-    const uint32_t tq = tmem_d + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t tq = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + half * kHalf;
     int acc = 0;
-    for (int tile = pair; tile < tiles; tile += pairs, ++acc) {
+    for (int tile = pair; tile < tiles; tile += pairs) {
       int m, n;
-      head_tile(tile, a.mtiles, a.ntiles, m, n);
-      const int buf = acc & 1;
+      const int split = tile / mn;
+      head_tile(tile - split * mn, a.mtiles, a.ntiles, m, n);
+      const int kn = min(a.kst, (split + 1) * a.kper) - split * a.kper;
       const int t = m * kHeadTile + static_cast<int>(rank) * 128 + q * 32 + lane;
       const bool rok = t < a.T;
-      const int n0 = n * kHeadTile;
-      const int nv = min(kHeadTile, a.ncols - n0);  // columns of the tile
-      const uint32_t tb = tq + buf * 256;
+      const int n0 = n * kHeadTile + half * kHalf;
+      const int nv = min(kHalf, a.ncols - n0);  // this thread's columns (may be none)
       int64_t label = -1;
       bool counted = false;
-      if (rok && a.labels) {
+      if (rok) {
         label = __ldg(a.labels + t);
         counted = counts(label, a.ignore, a.vocab);
       }
-      // the label's column of this tile, or none
-      const int64_t lc = MODE != kHeadGrad && counted ? label - a.v0 - n0 : -1;
+      // the label's place among this thread's columns, or none
+      int64_t lc = counted ? label - a.v0 - n0 : -1;
+      const int lj = lc >= 0 && lc < nv ? static_cast<int>(lc) : -1;
 
-      if (!mbar_wait_warp(&accf[buf], (acc >> 1) & 1, wc)) break;
-      tc_fence_after();
-
-      if (MODE == kHeadLoss) {
-        float mx = -INFINITY, s = 0.0f, z = 0.0f;
-        for (int cb = 0; cb * 32 < nv; ++cb) {
-          float l[32];
-          load_logits(tb + cb * 32, nv - cb * 32, l);
-          const float cm = max32(l);
-          if (cm > mx) {
-            s *= exp2_fast((mx - cm) * kLog2e);
-            mx = cm;
-          }
-          const float base = mx == -INFINITY ? 0.0f : mx * kLog2e;
-          float p[4] = {};
-#pragma unroll
-          for (int j = 0; j < 32; ++j) p[j & 3] += exp2_fast(fmaf(l[j], kLog2e, -base));
-          s += (p[0] + p[1]) + (p[2] + p[3]);
-          const int lj = (lc >> 5) == cb ? static_cast<int>(lc & 31) : -1;
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j == lj) z = l[j];
+      if (MODE == kHeadGrad) {
+        // one chunk per tile (bf16 results), 32 columns at a time
+        const int buf = acc & 1;
+        if (kn > 0) {  // an empty slice (of a short last piece) adds nothing
+          if (!mbar_wait_warp(&accf[buf], (acc >> 1) & 1, wc)) break;
+          tc_fence_after();
         }
-        if (rok) {
-          a.part[static_cast<int64_t>(n) * a.T + t] = make_float2(mx, s);
-          if (lc >= 0 && lc < nv) a.label_logit[t] = z;
-        }
-      } else if (MODE == kHeadExp) {
-        float mx = -INFINITY;
-        for (int cb = 0; cb * 32 < nv; ++cb) {
-          float l[32];
-          load_logits(tb + cb * 32, nv - cb * 32, l);
-          mx = fmaxf(mx, max32(l));
-        }
-        const float ref = (fabsf(mx) <= kRefRange || mx == -INFINITY) ? 0.0f : mx;
-        const float base = ref * kLog2e;
-        float s = 0.0f, z = 0.0f;
-        uint16_t* grow = a.g + static_cast<int64_t>(t) * a.ldg + n0;
-        for (int cb = 0; cb < kHeadTile / 32; ++cb) {
-          float l[32];
-          load_logits(tb + cb * 32, nv - cb * 32, l);
-          const int lj = (lc >> 5) == cb ? static_cast<int>(lc & 31) : -1;
-          float p[4] = {};
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float x = l[j];
-            l[j] = exp2_fast(fmaf(x, kLog2e, -base));
-            p[j & 3] += l[j];
-            if (j == lj) {
-              z = x;
-              l[j] = 0.0f;
-            }
-          }
-          s += (p[0] + p[1]) + (p[2] + p[3]);
-          if (rok) store_bf16x32(grow + cb * 32, l, 32);
-        }
-        if (rok) {
-          a.part[static_cast<int64_t>(n) * a.T + t] = make_float2(ref, s);
-          if (lc >= 0 && lc < nv) a.label_logit[t] = z;
-        }
-      } else if (MODE == kHeadProb) {
-        const float lse = rok ? __ldcg(a.lse + t) : 0.0f;
-        const float base = lse * kLog2e;
-        uint16_t* grow = a.g + static_cast<int64_t>(t) * a.ldg + n0;
-        for (int cb = 0; cb < kHeadTile / 32; ++cb) {
-          float l[32];
-          load_logits(tb + cb * 32, nv - cb * 32, l);
-          const int lj = (lc >> 5) == cb ? static_cast<int>(lc & 31) : -1;
-          float z = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float x = l[j];
-            if (j == lj) z = x;
-            l[j] = counted ? exp2_fast(fmaf(x, kLog2e, -base)) : 0.0f;
-          }
-          if (lj >= 0) {
-            z = expm1f(z - lse);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j == lj) l[j] = z;
-          }
-          if (rok) store_bf16x32(grow + cb * 32, l, 32);
-        }
-        if (rok && n == 0 && a.v0 == 0 && !counted && label != a.ignore && a.status)
-          atomicOr(a.status, QLORA_DEV_LABEL);
-      } else {
-        // dH = ca * sum + cl * W[label]
-        float ca = 0.0f, cl = 0.0f;
-        if (a.last && counted) {
-          if (a.row_sum) {
-            const float g = a.weight ? a.scale * __ldcg(a.weight + t) : a.scale / static_cast<float>(__ldcg(a.count));
-            ca = g / __ldcg(a.row_sum + t);
-            cl = g * __ldcg(a.p_label + t);
-          } else {
-            ca = a.stats ? __ldcg(a.dloss) / __ldcg(a.stats + 1) : __ldcg(a.dloss + t);
-          }
-        }
+        float4* sum = reinterpret_cast<float4*>(a.acc) + (static_cast<int64_t>(tile) * 2 + rank) * kSumBlock + et;
         const float al = (!a.first && a.alpha && rok) ? __ldcg(a.alpha + t) : 1.0f;
-        float4* sum = reinterpret_cast<float4*>(a.acc) +
-                      ((static_cast<int64_t>(m) * a.ntiles + n) * 2 + rank) * (8 * 8 * 128) + et;
-        for (int cb = 0; cb * 32 < nv; ++cb) {
-          float l[32];
-          {
+        const bool out = a.last && a.splits == 1;
+        float ca = 0.0f, cl = 0.0f;
+        if (out && counted) grad_row_factors(a, t, ca, cl);
+        for (int cb = 0; cb < kHalf / 32; ++cb) {
+          float l[32] = {};
+          if (kn > 0) {
             uint32_t v[32];
-            tmem_ld_32x32b_x32(tb + cb * 32, v);
+            tmem_ld_32x32b_x32(tq + buf * 256 + cb * 32, v);
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; ++j) l[j] = __uint_as_float(v[j]);
           }
-          float4* at = sum + cb * (8 * 128);
+          float4* at = sum + cb * 8 * kSumStride;
           if (!a.first) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float4 o = __ldcg(at + j * 128);
+              const float4 o = __ldcg(at + j * kSumStride);
               l[4 * j] = fmaf(al, o.x, l[4 * j]);
               l[4 * j + 1] = fmaf(al, o.y, l[4 * j + 1]);
               l[4 * j + 2] = fmaf(al, o.z, l[4 * j + 2]);
               l[4 * j + 3] = fmaf(al, o.w, l[4 * j + 3]);
             }
           }
-          if (!a.last) {
+          if (!out) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) __stcg(at + j * 128, make_float4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]));
-          } else if (rok) {
-            const int nc = min(32, nv - cb * 32);
-            if (counted) {
-              if (a.row_sum) {
-                float w[32];
-                load_head_row(a.head, a.tab, label, n0 + cb * 32, nc, w);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) l[j] = fmaf(cl, w[j], ca * l[j]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) l[j] *= ca;
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) l[j] = 0.0f;
-            }
-            store_bf16x32(a.dh + static_cast<int64_t>(t) * a.ldd + n0 + cb * 32, l, nc);
+            for (int j = 0; j < 8; ++j)
+              __stcg(at + j * kSumStride, make_float4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]));
+          } else if (rok && cb * 32 < nv) {
+            store_grad32(a, t, label, counted, ca, cl, n0 + cb * 32, min(32, nv - cb * 32), l);
           }
         }
+        if (kn > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(dsmem_addr(&acce[buf], 0));
+          ++acc;
+        }
+        continue;
       }
-      tc_fence_before();  // this warp's reads of the accumulator are done
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(dsmem_addr(&acce[buf], 0));
+
+      float l[kHalf];
+      bool ok = true;
+      for (int k0 = 0; k0 < kn; k0 += a.kchunk, ++acc) {
+        const int buf = acc & 1;
+        if (!mbar_wait_warp(&accf[buf], (acc >> 1) & 1, wc)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        add_chunk(tq + buf * 256, k0 == 0, l);
+        tc_fence_before();  // this warp's reads of the accumulator are done
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(dsmem_addr(&acce[buf], 0));
+      }
+      if (!ok) break;
+
+      if (nv < kHalf) {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j)
+          if (j >= nv) l[j] = -INFINITY;
+      }
+      if (MODE == kHeadLoss) {
+        const float mx = max_all(l);
+        const float base = mx == -INFINITY ? 0.0f : mx * kLog2e;
+        if (lj >= 0) a.label_logit[t] = pick(l, lj);
+        float p[4] = {};
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) p[j & 3] += exp2_fast(fmaf(l[j], kLog2e, -base));
+        if (rok) a.part[static_cast<int64_t>(2 * n + half) * a.T + t] = make_float2(mx, (p[0] + p[1]) + (p[2] + p[3]));
+      } else if (MODE == kHeadExp) {
+        const float mx = max_all(l);
+        const float ref = (fabsf(mx) <= kRefRange || mx == -INFINITY) ? 0.0f : mx;
+        const float base = ref * kLog2e;
+        if (lj >= 0) a.label_logit[t] = pick(l, lj);
+        float p[4] = {};
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+          l[j] = exp2_fast(fmaf(l[j], kLog2e, -base));
+          p[j & 3] += l[j];
+          if (j == lj) l[j] = 0.0f;
+        }
+        if (rok) {
+          a.part[static_cast<int64_t>(2 * n + half) * a.T + t] = make_float2(ref, (p[0] + p[1]) + (p[2] + p[3]));
+          store_bf16(a.g + static_cast<int64_t>(t) * a.ldg + n0, l);
+        }
+      } else if (MODE == kHeadProb) {
+        const float lse = rok ? __ldcg(a.lse + t) : 0.0f;
+        const float base = lse * kLog2e;
+        const float pl = lj >= 0 ? expm1f(pick(l, lj) - lse) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+          l[j] = counted ? exp2_fast(fmaf(l[j], kLog2e, -base)) : 0.0f;
+          if (j == lj) l[j] = pl;
+        }
+        if (rok) {
+          store_bf16(a.g + static_cast<int64_t>(t) * a.ldg + n0, l);
+          if (n0 == 0 && a.v0 == 0 && !counted && label != a.ignore && a.status) atomicOr(a.status, QLORA_DEV_LABEL);
+        }
+      }
     }
   }
 
@@ -452,6 +501,42 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_d, 512);
   }
+}
+
+// ------------------------------------------------------------------- finish
+//
+// A split contraction's sums joined in split order, and dH's rows from them.
+// blockIdx.x: (tile, CTA of the pair); blockIdx.y: 32 of a thread's 128 columns.
+__global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_constant__ HeadArgs a) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int mn = a.mtiles * a.ntiles;
+  const int tile = blockIdx.x >> 1, rank = blockIdx.x & 1;
+  int m, n;
+  head_tile(tile, a.mtiles, a.ntiles, m, n);
+  const int et = threadIdx.x, w = et >> 5, lane = et & 31;
+  const int t = m * kHeadTile + rank * 128 + ((w + 2) & 3) * 32 + lane;  // as in the product's epilogue
+  const int d = n * kHeadTile + (w >> 2) * kHalf + blockIdx.y * 32;
+  if (t >= a.T || d >= a.ncols) return;
+  const float4* sum = reinterpret_cast<const float4*>(a.acc) + (static_cast<int64_t>(tile) * 2 + rank) * kSumBlock +
+                      static_cast<int>(blockIdx.y) * 8 * kSumStride + et;
+  float l[32] = {};
+  for (int s = 0; s < a.splits; ++s) {
+    const float4* at = sum + static_cast<int64_t>(s) * mn * 2 * kSumBlock;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 o = __ldcg(at + j * kSumStride);
+      l[4 * j] += o.x;
+      l[4 * j + 1] += o.y;
+      l[4 * j + 2] += o.z;
+      l[4 * j + 3] += o.w;
+    }
+  }
+  const int64_t label = __ldg(a.labels + t);
+  const bool counted = counts(label, a.ignore, a.vocab);
+  float ca = 0.0f, cl = 0.0f;
+  if (counted) grad_row_factors(a, t, ca, cl);
+  store_grad32(a, t, label, counted, ca, cl, d, min(32, a.ncols - d), l);
 }
 
 // ------------------------------------------------------------------ combine
@@ -493,7 +578,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
   float R = -INFINITY, S = 0.0f;
   if (rok) {
 #pragma unroll 4
-    for (int j = warp; j < a.ntiles; j += kCombineWarps) {
+    for (int j = warp; j < a.nparts; j += kCombineWarps) {
       const float2 p = a.part[static_cast<int64_t>(j) * a.T + t];
       join(R, S, p.x, p.y);
     }
@@ -546,7 +631,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
   __syncthreads();
   if (a.e) {
     const float ref = ref_s[lane];
-    for (int j = warp; j < a.ntiles; j += kCombineWarps) {
+    for (int j = warp; j < a.nparts; j += kCombineWarps) {
       const float2 p = rok ? a.part[static_cast<int64_t>(j) * a.T + t] : make_float2(0.0f, 0.0f);
       uint32_t todo = __ballot_sync(0xFFFFFFFFu, rok && p.y != 0.0f && p.x != ref);
       const float f = expf(p.x - ref);
@@ -554,14 +639,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
         const float fr = __shfl_sync(0xFFFFFFFFu, f, src);
-        uint4* at = reinterpret_cast<uint4*>(a.e + static_cast<int64_t>(blockIdx.x * 32 + src) * a.lde +
-                                             static_cast<int64_t>(j) * kHeadTile) + lane;
-        const uint4 v = *at;
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = pack_bf16x2(__uint_as_float(w[i] << 16) * fr, __uint_as_float(w[i] & 0xFFFF0000u) * fr);
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        uint2* at = reinterpret_cast<uint2*>(a.e + static_cast<int64_t>(blockIdx.x * 32 + src) * a.lde +
+                                             static_cast<int64_t>(j) * kHalf) + lane;
+        const uint2 v = *at;
+        *at = make_uint2(pack_bf16x2(__uint_as_float(v.x << 16) * fr, __uint_as_float(v.x & 0xFFFF0000u) * fr),
+                         pack_bf16x2(__uint_as_float(v.y << 16) * fr, __uint_as_float(v.y & 0xFFFF0000u) * fr));
       }
     }
   }
@@ -587,7 +669,7 @@ static cudaError_t launch_head_gemm_impl(const CUtensorMap& tm_a, const CUtensor
                                          cudaStream_t stream) {
   static uint64_t done = 0;
   if (cudaError_t e = allow_smem(head_gemm_kernel<MODE>, HeadPlan::kSmem, done)) return e;
-  const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles;
+  const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles * a.splits;
   const int pairs = static_cast<int>(std::min<int64_t>(tiles, 74));  // one pair per TPC
   return launch_kernel(head_gemm_kernel<MODE>, dim3(2 * pairs), dim3(kHeadThreads), HeadPlan::kSmem, stream,
                        dim3(2, 1, 1), tm_a, tm_b, a);
@@ -602,6 +684,11 @@ cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMa
     case kHeadGrad: return launch_head_gemm_impl<kHeadGrad>(tm_a, tm_b, a, stream);
     default: return cudaErrorInvalidValue;
   }
+}
+
+cudaError_t launch_head_finish(const HeadArgs& a, cudaStream_t stream) {
+  return launch_kernel(head_finish_kernel, dim3(2 * a.mtiles * a.ntiles, kHalf / 32), dim3(kSumStride), 0, stream,
+                       dim3(1, 1, 1), a);
 }
 
 int head_combine_blocks(int64_t T) { return static_cast<int>((T + 31) / 32); }

@@ -198,9 +198,10 @@ cudaError_t launch_fused_pair_fwd(const CUtensorMap& tm_b, const CUtensorMap& tm
                                   cudaStream_t stream);
 
 // Skinny LoRA products; the contraction is split over a cluster of `splits`
-// (1..8) CTAs along y and reduced in-cluster.  See skinny.cu for the maps.
+// (1..8) CTAs along y and reduced in-cluster.  See skinny.cu for the maps, and
+// for the summed forms (DU, DB).
 cudaError_t launch_skinny(int mode, const CUtensorMap& tmA, const CUtensorMap& tmB, const SkinnyArgs& a,
-                          int grid_rows, int splits, cudaStream_t stream);
+                          int grid_rows, int splits, cudaStream_t stream, bool summed = false);
 
 // Few-token forward (M <= 32): register-operand MMAs on in-register
 // dequantised tiles, persistent CTAs over (128-row tile, 256-wide K chunk)

@@ -57,7 +57,9 @@ __device__ __forceinline__ void store_hilo(uint16_t* cat, int m, int ld, int col
   row[hilo_col(j) + 16] = lo;
 }
 
-template <int MODE>
+constexpr int kSumStages = 8;  // stages per accumulator of a summed form
+
+template <int MODE, bool SUMMED>
 __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
     skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const SkinnyArgs a) {
@@ -67,8 +69,10 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBarOff);
   uint64_t* empty = full + P::kStages;
   uint64_t* accf = empty + P::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
+  uint64_t* acce = accf + 2;  // summed forms: accf and acce of two accumulators
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + (SUMMED ? 5 : 1));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  constexpr uint32_t kTmemCols = (SUMMED ? 2 : 1) * P::kTmemCols;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Tile origin: DOWN/DU rows are tokens, DB rows are output features, DA's
@@ -98,6 +102,12 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
       mbar_init(&empty[s], 1);
     }
     mbar_init(accf, 1);
+    if (SUMMED) {
+      mbar_init(accf + 1, 1);
+      mbar_init(acce, 4);
+      mbar_init(acce + 1, 4);
+      mbar_init(acce + 2, 1);  // abort path only
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -106,7 +116,7 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, P::kTmemCols);
+    tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -167,6 +177,11 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
       bool aborted = false;
       for (int t = 0; t < T; ++t) {
         const uint32_t s = t % P::kStages, u = t / P::kStages;
+        const int ch = t / kSumStages, buf = SUMMED ? ch & 1 : 0;
+        if (SUMMED && t % kSumStages == 0 && ch >= 2 && !mbar_wait(&acce[buf], ((ch >> 1) - 1) & 1, wc)) {
+          aborted = true;
+          break;
+        }
         if (!mbar_wait(&full[s], u & 1, wc)) { aborted = true; break; }
         tc_fence_after();
         const uint32_t sa = smem_u32(smem + s * P::kStage), sb = sa + P::kA;
@@ -174,18 +189,66 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
         const uint64_t bdesc = b_mn ? sdesc_sw128(sb, 8192, 1024) : sdesc_sw128(sb, 16, 1024);
 #pragma unroll
         for (uint32_t kk = 0; kk < 4; ++kk)
-          umma_bf16(tmem_d, adesc + kk * a_step, bdesc + kk * b_step, idesc, (t | kk) != 0 ? 1u : 0u);
+          umma_bf16(tmem_d + buf * P::kTmemCols, adesc + kk * a_step, bdesc + kk * b_step, idesc,
+                    ((SUMMED ? t % kSumStages : t) | kk) != 0 ? 1u : 0u);
         umma_commit(&empty[s]);
+        if (SUMMED && (t % kSumStages == kSumStages - 1 || t == T - 1)) umma_commit(&accf[buf]);
       }
-      umma_commit(accf);
-      if (aborted) mbar_drain(accf, 0, a.status);
+      if (!SUMMED) {
+        umma_commit(accf);
+        if (aborted) mbar_drain(accf, 0, a.status);
+      } else if (aborted) {  // the MMAs in flight end with the stages' own commits; wait for the last
+        uint64_t* last = acce + 2;
+        umma_commit(last);
+        mbar_drain(last, 0, a.status);
+      }
     }
   } else {
     // ------------------------------------------------ TMEM -> own partial tile
     const int q = warp & 3;
     const int rl = q * 32 + lane;
     float* part = reinterpret_cast<float*>(smem);  // ring is idle once accf completes
-    if (mbar_wait_warp(accf, 0, wc)) {
+    if (SUMMED) {
+      // rows = tokens (DU) or output features (DB, hi/lo columns joined)
+      float sum[64] = {};
+      bool ok = true;
+      for (int ch = 0; ok && ch * kSumStages < T; ++ch) {
+        const int buf = ch & 1;
+        ok = mbar_wait_warp(&accf[buf], (ch >> 1) & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tq = tmem_d + buf * P::kTmemCols + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+        for (int cb = 0; cb < (MODE == kSkDB ? 4 : 2); ++cb) {
+          if (cb * (MODE == kSkDB ? 16 : 32) < rw) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tq + cb * 32, v);
+            tmem_ld_wait();
+            if (MODE == kSkDB) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                sum[cb * 16 + j] =
+                    __fadd_rn(sum[cb * 16 + j], __fadd_rn(__uint_as_float(v[j]), __uint_as_float(v[j + 16])));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                sum[(cb & 1) * 32 + j] = __fadd_rn(sum[(cb & 1) * 32 + j], __uint_as_float(v[j]));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acce[buf]);
+      }
+      // Another warp's last accumulator is final too (the same commit), so
+      // the ring is idle for every warp that gets here.
+      if (ok) {
+        float* dst = part + rl * P::kLdRows;
+#pragma unroll
+        for (int j = 0; j < 64; j += 4)
+          if (j < rw) *reinterpret_cast<float4*>(dst + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
+      }
+    } else if (mbar_wait_warp(accf, 0, wc)) {
       tc_fence_after();
       const uint32_t tq = tmem_d + (static_cast<uint32_t>(q * 32) << 16);
       if (MODE == kSkDown || MODE == kSkDU) {
@@ -313,17 +376,17 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_d, P::kTmemCols);
+    tmem_dealloc(tmem_d, kTmemCols);
   }
 }
 
-template <int MODE>
+template <int MODE, bool SUMMED = false>
 static cudaError_t launch_skinny_impl(const CUtensorMap& tmA, const CUtensorMap& tmB, const SkinnyArgs& a,
                                       int grid_rows, int splits, cudaStream_t stream) {
   using P = SkPlan<MODE>;
   static bool attr_set = false;
   if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(skinny_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(skinny_kernel<MODE, SUMMED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(P::kSmem));
     if (e != cudaSuccess) return e;
     attr_set = true;
@@ -333,12 +396,19 @@ static cudaError_t launch_skinny_impl(const CUtensorMap& tmA, const CUtensorMap&
   // row tiles they sit on both SMs of a TPC, rather than on one SM of many
   // TPCs, each of which could then hold no GEMM pair.
   const dim3 cluster = (splits == 1 && grid_rows % 2 == 0) ? dim3(2, 1, 1) : dim3(1, static_cast<unsigned>(splits), 1);
-  return launch_kernel(skinny_kernel<MODE>, dim3(grid_rows, splits, 1), dim3(192), P::kSmem, stream, cluster, tmA,
+  return launch_kernel(skinny_kernel<MODE, SUMMED>, dim3(grid_rows, splits, 1), dim3(192), P::kSmem, stream, cluster, tmA,
                        tmB, a);
 }
 
 cudaError_t launch_skinny(int mode, const CUtensorMap& tmA, const CUtensorMap& tmB, const SkinnyArgs& a,
-                          int grid_rows, int splits, cudaStream_t stream) {
+                          int grid_rows, int splits, cudaStream_t stream, bool summed) {
+  if (summed) {
+    switch (mode) {
+      case kSkDU: return launch_skinny_impl<kSkDU, true>(tmA, tmB, a, grid_rows, splits, stream);
+      case kSkDB: return launch_skinny_impl<kSkDB, true>(tmA, tmB, a, grid_rows, splits, stream);
+      default: return cudaErrorInvalidValue;
+    }
+  }
   switch (mode) {
     case kSkDown: return launch_skinny_impl<kSkDown>(tmA, tmB, a, grid_rows, splits, stream);
     case kSkDU: return launch_skinny_impl<kSkDU>(tmA, tmB, a, grid_rows, splits, stream);

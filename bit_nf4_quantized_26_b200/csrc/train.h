@@ -50,6 +50,8 @@ struct HeadArgs {
   int T;                  // tokens
   int ncols;              // columns of this product: the piece's vocabulary rows, or dim (Grad)
   int kst;                // 64-deep contraction stages
+  int kchunk;             // stages summed in one accumulator
+  int splits, kper;       // Grad: slices of the contraction and their stages (else 1, kst)
   int b_row0;             // the piece's first row in W's tensor map
   int64_t v0;             // the piece's first vocabulary index
   int64_t vocab;
@@ -57,7 +59,7 @@ struct HeadArgs {
   const int64_t* labels;
   int64_t ignore;
   float* label_logit;     // Loss, Exp: [T]
-  float2* part;           // Loss, Exp: (reference, sum of exponentials) [tile][T], from the piece's first tile
+  float2* part;           // Loss, Exp: (reference, sum of exponentials) [128 columns][T], from the piece's first column
   const float* lse;       // Prob: [T]
   uint16_t* g;            // Prob, Exp: [T, ldg]
   int64_t ldg;
@@ -65,7 +67,7 @@ struct HeadArgs {
   int zero_count;
   // Grad
   int first, last;        // of the pieces
-  float* acc;             // fp32 sum over the pieces so far, tile-blocked
+  float* acc;             // fp32 sums of the pieces so far, and of each split (blocked by tile)
   const float* alpha;     // [T] factor of the sum so far (null: 1)
   uint16_t* dh;           // [T, ldd]
   int64_t ldd;
@@ -86,10 +88,13 @@ struct HeadArgs {
 cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
                              cudaStream_t stream);
 
+// Grad with splits > 1: joins the splits' sums after the last piece.
+cudaError_t launch_head_finish(const HeadArgs& a, cudaStream_t stream);
+
 // Joins the per-tile statistics of every row; see head_loss.cu.
 struct HeadCombineArgs {
-  int T, ntiles;
-  const float2* part;      // [ntiles][T]
+  int T, nparts;
+  const float2* part;      // [nparts][T]
   const float* label_logit;
   const int64_t* labels;
   int64_t ignore;

@@ -62,9 +62,11 @@ QLORA_API qlora_status act8_dequantize(const uint8_t* codes, const uint8_t* exps
 /*
  * The backward passes of qlora_nf4.h with the adapter's input given as its
  * 8-bit checkpoint (of X; for the dropout form, of X_drop, whose zeros stay
- * zeros): dA = dU^T X', everything else unchanged and bitwise the same.
- * Arguments, constraints, workspaces and errors as for qlora_linear_bwd,
- * qlora_group_bwd and qlora_linear_bwd_dropout.
+ * zeros): dA = dU^T X', everything else by the same formulas.  The rank-r
+ * products (dU, dB, dA) join their accumulator's sums every 512 terms in fp32
+ * with rounding to nearest: dA and dB within 1e-5 relative Frobenius error,
+ * whatever the number of tokens.  Arguments, constraints, workspaces and errors
+ * as for qlora_linear_bwd, qlora_group_bwd and qlora_linear_bwd_dropout.
  */
 QLORA_API qlora_status qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* codes, const uint8_t* exps,
                                              const float* U, int64_t M, nf4_weight W, const uint16_t* A,
@@ -138,10 +140,11 @@ typedef struct {
  * their type's alignment only (a shifted view of the labels is fine).
  * Workspaces: qlora_head_loss_workspace_size(T, vocab, dim, nf4, op) bytes with
  * nf4 nonzero for an NF4 head and op one of QLORA_HEAD_FWD / _BWD / _STEP.
- * Beside per-token words it holds 8 bytes per 256 logits (forward, step), a
+ * Beside per-token words it holds 8 bytes per 128 logits (forward, step), a
  * piece of the probabilities (backward, step: about 128 MB in bf16, at least
- * 2048 columns), with several pieces an fp32 [T, dim], and a dequantised piece
- * of an NF4 head (at most 128 MB, at least 2048 rows).
+ * 2048 columns), fp32 sums [T, dim] (with several pieces, and for few tokens
+ * one per slice of the contraction), and a dequantised piece of an NF4 head (at
+ * most 128 MB, at least 2048 rows).
  * Accuracy: exact bf16 inputs, fp32 accumulation and softmax; the probabilities
  * enter the second product as bf16 (label term subtracted in fp32 first); dH
  * within 5e-3 relative Frobenius error of the fp64 gradient.

@@ -131,12 +131,12 @@ def test_head_loss_workspace_sizes():
     f = q.qlora_head_loss_workspace_size
     assert f(0, 1000, 512, False, q.HEAD_FWD) == 0 and f(10, 1000, 512, False, 3) == 0
     assert f(10, 1000, 520, True, q.HEAD_FWD) == 0            # a shape the calls refuse
-    # forward: 8 bytes per 256 logits and per-token words, no logits
+    # forward: 8 bytes per 128 logits and per-token words, no logits
     T, V = 8192, 128000
-    assert 8 * T * V // 256 <= f(T, V, 4096, False, q.HEAD_FWD) <= 8 * T * V // 256 + 16 * T + 4096
+    assert 8 * T * V // 128 <= f(T, V, 4096, False, q.HEAD_FWD) <= 8 * T * V // 128 + 16 * T + 4096
     # backward and step: bounded in the vocabulary
     for op in (q.HEAD_BWD, q.HEAD_STEP):
-        assert f(T, V, 4096, False, op) <= (1 << 27) + 4 * T * 4096 + (1 << 22)
+        assert f(T, V, 4096, False, op) <= (1 << 27) + 4 * T * 4096 + (1 << 23)  # piece, sum, statistics
         assert f(T, 4 * V, 4096, False, op) <= f(T, V, 4096, False, op) + (1 << 20)
     assert f(T, V, 4096, True, q.HEAD_BWD) - f(T, V, 4096, False, q.HEAD_BWD) <= 1 << 27
 

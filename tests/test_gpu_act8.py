@@ -1,8 +1,12 @@
 """GPU parity of the 8-bit activation checkpoints: codes and exponents bit for
-bit, decoded values exactly, and the backward passes that read them: dX and dB
-bitwise those of the plain passes, dA bitwise that of the plain pass on the
-decoded input (the same operand values in the same order) and within 1e-4 of
-the fp64 oracle, as every fp32 output of the linears."""
+bit, decoded values exactly, and the backward passes that read them, against
+the fp64 oracle on the decoded input.
+
+dX keeps the linears' 2e-3.  dA and dB are held to 1e-5 (relative Frobenius
+error): sums of exact products join every 32 accumulator steps, each step at
+most 2^-24 of the sum off towards zero, 32 2^-24 = 1.9e-6; dU and s U enter
+as a bf16 pair, off by at most 2^-17 of a value and randomly; dA has the drift
+of dU as well: 2 * 1.9e-6 + 2^-18 + fp32 joins < 1e-5."""
 
 import numpy as np
 import pytest
@@ -11,8 +15,6 @@ import torch
 import bit_nf4_quantized_26_b200 as q
 import synth
 from oracle import act8
-from oracle import linear as ol
-from oracle import nf4
 from tests._util import bits
 
 pytestmark = pytest.mark.gpu
@@ -87,7 +89,8 @@ def test_no_rows():
 
 # tokens, outputs, inputs, rank: every GEMM path, ragged stages and tiles, rank chunks
 SHAPES = [(1, 64, 64, 16), (64, 512, 512, 16), (65, 192, 320, 48), (200, 512, 640, 32), (600, 512, 768, 64),
-          (1000, 384, 448, 64), (150, 384, 448, 144), (700, 512, 768, 256), (4096, 4096, 4096, 64)]
+          (1000, 384, 448, 64), (150, 384, 448, 144), (700, 512, 768, 256), (4096, 4096, 4096, 64),
+          (577, 256, 256, 64), (16384, 128, 4096, 16), (1153, 8192, 128, 64)]
 
 
 @pytest.mark.parametrize("M,N,K,r", SHAPES)
@@ -100,15 +103,29 @@ def test_linear_bwd_act8(M, N, K, r, dt):
     x8 = q.act8_quantize(g["X"])
     status = torch.zeros(4, dtype=torch.int32, device="cuda")
     dX, dA, dB = q.qlora_linear_bwd_act8(g["dY"], x8, U, W, g["A"], g["B"], s, dx_dtype=dt, status=status)
-    pX, _, pB = q.qlora_linear_bwd(g["dY"], g["X"], U, W, g["A"], g["B"], s, dx_dtype=dt)
-    _, pA, _ = q.qlora_linear_bwd(g["dY"], q.act8_dequantize(x8), U, W, g["A"], g["B"], s, dx_dtype=dt)
     assert int(status[0]) == 0
-    assert _same(dX, pX) and _same(dB, pB) and _same(dA, pA)
-    dU = s * (ol._f64(bits(d["dY"])) @ ol._f64(bits(d["B"])))
-    ref = dU.T @ act8.dequantize(*act8.quantize(bits(d["X"])))
-    assert ol.rel_frobenius(dA.cpu().numpy(), ref) <= 1e-4
+    _check(d["dY"], x8, U, q.nf4_dequantize(W.codes, W.c8, W.s2, N * K).view(N, K), [N], d["A"], d["B"], s,
+           (dX, dA, dB))
     again = q.qlora_linear_bwd_act8(g["dY"], x8, U, W, g["A"], g["B"], s, dx_dtype=dt)
-    assert _same(again[1], dA)
+    for a, b in zip(again, (dX, dA, dB)):
+        assert _same(a, b)
+
+
+def _check(dY, x8, U, Wd, members, A, B, s, got):
+    """Against the formulas in fp64 on the GPU (the oracle's values as inputs)."""
+    x = torch.from_numpy(act8.dequantize(x8.codes.cpu().numpy(), x8.exps.cpu().numpy())).cuda()
+    dY, A, B, U, Wd = (v.double().cuda() for v in (dY, A, B, U, Wd))
+    r = A.shape[0] // len(members)
+    dX, dA, dB, n0 = 0, [], [], 0
+    for i, n in enumerate(members):
+        dYg, Bg, j = dY[:, n0:n0 + n], B[n0:n0 + n], slice(i * r, (i + 1) * r)
+        dU = s * (dYg @ Bg)
+        dX = dX + dYg @ Wd[n0:n0 + n] + dU @ A[j]
+        dA.append(dU.t() @ x)
+        dB.append(s * (dYg.t() @ U[:, j]))
+        n0 += n
+    for a, ref, tol in zip(got, (dX, torch.cat(dA), torch.cat(dB)), (2e-3, 1e-5, 1e-5)):
+        assert float((a.double() - ref).norm() / ref.norm()) <= tol
 
 
 @pytest.mark.parametrize("M,members,K,r", [(333, (256, 128), 512, 16), (1030, (512, 512, 256), 768, 64),
@@ -123,9 +140,7 @@ def test_group_bwd_act8(M, members, K, r):
     U = X.float() @ A.float().t()
     x8 = q.act8_quantize(X)
     got = q.qlora_group_bwd_act8(dY, x8, U, W, members, A, B, 0.5)
-    want = q.qlora_group_bwd(dY, q.act8_dequantize(x8), U, W, members, A, B, 0.5)
-    for a, b in zip(got, want):
-        assert _same(a, b)
+    _check(dY, x8, U, q.nf4_dequantize(W.codes, W.c8, W.s2, N * K).view(N, K), members, A, B, 0.5, got)
 
 
 @pytest.mark.parametrize("M,N,K,r,p", [(200, 512, 640, 32, 0.05), (600, 512, 768, 64, 0.5), (150, 384, 448, 144, 0.1)])
@@ -139,8 +154,8 @@ def test_dropout_bwd_act8(M, N, K, r, p):
     assert bool((back[Xd == 0] == 0).all())
     got = q.qlora_linear_bwd_dropout_act8(g["dY"], x8, U, W, g["A"], g["B"], 0.25, p, 11)
     want = q.qlora_linear_bwd_dropout(g["dY"], back, U, W, g["A"], g["B"], 0.25, p, 11)
-    for a, b in zip(got, want):
-        assert _same(a, b)
+    for a, b, tol in zip(got, want, (2e-3, 1e-4, 1e-4)):  # the plain pass on the decoded input
+        assert float((a.double() - b.double()).norm() / b.double().norm()) <= tol
 
 
 def test_no_tokens_give_zero_gradients():
