@@ -120,29 +120,36 @@ __global__ void __launch_bounds__(kActThreads) act8_dequantize_kernel(const uint
 // dA[j, k] = sum_m dU[m, j] X'[m, k]: the GEMM of skinny.cu's mode DA (128 rows
 // of dU's bf16 hi/lo columns, tiles of 128 input features, the tokens split
 // over a cluster and summed in rank order through distributed shared memory),
-// with the token-side operand turned from codes into bf16 on the way:
-// copies bring 64 tokens x 128 codes (8 KB), four warps write them as the
-// MN-major 128-byte-swizzled tile the tensor core reads.  Two rings: three
-// stages of copies (24 KB) and two dequantised tiles (16 KB), two CTAs per SM.
+// with the token-side operand turned from codes into bf16 on the way: copies
+// bring 64 tokens x 128 codes (8 KB) beside dU's 16 KB, and two groups of four
+// warps taking alternate stages write them as the MN-major 128-byte-swizzled
+// tile the tensor core reads.  A stage is a chain (copy, convert, multiply)
+// and runs beside the dX GEMM on few SMs, so what counts is how many are in
+// flight: six copies and four converted tiles, one CTA per SM.  (Three and
+// two with one group, two CTAs per SM, took 193 us for 16384 tokens of 4096
+// features on 64 CTAs.)  The rings are even, so a slot's earlier stages are
+// the same group's and its parity waits cannot run a phase ahead.
 // Summed as DU and DB are (skinny.cu): two accumulators of eight stages each
 // in turn, joined in registers.
 struct ActDaPlan {
   static constexpr uint32_t kA = 16384;    // dU hi/lo: 64 tokens x 128 columns
   static constexpr uint32_t kRaw = 8192;   // codes: 64 tokens x 128 features
   static constexpr uint32_t kCopy = kA + kRaw;
-  static constexpr uint32_t kCopies = 3;
-  static constexpr uint32_t kB = 16384;    // dequantised: 64 tokens x 128 features
-  static constexpr uint32_t kTiles = 2;
+  static constexpr uint32_t kCopies = 6;
+  static constexpr uint32_t kB = 16384;    // converted: 64 tokens x 128 features
+  static constexpr uint32_t kTiles = 4;
   static constexpr uint32_t kTileOff = kCopies * kCopy;
   static constexpr uint32_t kBarOff = kTileOff + kTiles * kB;
   static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
   static constexpr int kSumStages = 8;
   static constexpr int kLd = 132;  // floats per row of the parked partial tile
-  static_assert(2 * kSmem <= 232448u, "two CTAs per SM");
+  static_assert(kSmem <= 232448u, "too much shared memory");
+  static_assert(kCopies % 2 == 0 && kTiles % 2 == 0, "two alternating groups need even rings");
   static_assert(64 * kLd * 4 <= kTileOff, "the partial tile lies in the copy ring");
 };
+constexpr int kActDaThreads = 320;  // copy warp, MMA warp, 2 x 4 converting warps
 
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(kActDaThreads, 1)
     act8_da_kernel(const __grid_constant__ CUtensorMap tm_du, const __grid_constant__ CUtensorMap tm_x,
                    const uint8_t* __restrict__ exps, const SkinnyArgs a) {
   using P = ActDaPlan;
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(192, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBarOff);  // copies landed
   uint64_t* empty = full + P::kCopies;                              // copies read (by the MMAs)
-  uint64_t* bfull = empty + P::kCopies;                             // tile dequantised
+  uint64_t* bfull = empty + P::kCopies;                             // tile converted
   uint64_t* bempty = bfull + P::kTiles;                             // tile read
   uint64_t* accf = bempty + P::kTiles;                              // accumulator final
   uint64_t* acce = accf + 2;                                        // accumulator read
@@ -179,7 +186,7 @@ __global__ void __launch_bounds__(192, 2)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
-      mbar_init(&acce[b], 4);
+      mbar_init(&acce[b], 8);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -210,29 +217,29 @@ __global__ void __launch_bounds__(192, 2)
         uint8_t* st = smem + s * P::kCopy;
         const int m0 = (st0 + t) * 64;
         mbar_arrive_expect_tx(&full[s], (wide ? 16384u : 8192u) + P::kRaw);
+        tma_load_2d(st + P::kA, &tm_x, &full[s], row0, m0);
         tma_load_2d(st, &tm_du, &full[s], ucol, m0);
         if (wide) tma_load_2d(st + 8192, &tm_du, &full[s], ucol + 64, m0);
-        tma_load_2d(st + P::kA, &tm_x, &full[s], row0, m0);
         issued = t + 1;
       }
       for (int t = max(0, issued - static_cast<int>(P::kCopies)); t < issued; ++t)
         mbar_drain(&full[t % P::kCopies], (t / P::kCopies) & 1, a.status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, 128, 1, 1);
-      bool aborted = false;
-      for (int t = 0; t < T; ++t) {
-        const uint32_t s = t % P::kCopies, b = t % P::kTiles;
-        const int ch = t / P::kSumStages, buf = ch & 1;
-        if ((t % P::kSumStages == 0 && ch >= 2 && !mbar_wait(&acce[buf], ((ch >> 1) - 1) & 1, wc)) ||
-            !mbar_wait(&full[s], (t / P::kCopies) & 1, wc) || !mbar_wait(&bfull[b], (t / P::kTiles) & 1, wc)) {
-          aborted = true;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t ad = sdesc_sw128(smem_u32(smem + s * P::kCopy), 8192, 1024);
-        const uint64_t bd = sdesc_sw128(smem_u32(smem + P::kTileOff + b * P::kB), 8192, 1024);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 1, 1);
+    bool aborted = false;
+    for (int t = 0; t < T; ++t) {
+      const uint32_t s = t % P::kCopies, b = t % P::kTiles;
+      const int ch = t / P::kSumStages, buf = ch & 1;
+      if ((t % P::kSumStages == 0 && ch >= 2 && !mbar_wait_all(&acce[buf], ((ch >> 1) - 1) & 1, wc)) ||
+          !mbar_wait_all(&full[s], (t / P::kCopies) & 1, wc) || !mbar_wait_all(&bfull[b], (t / P::kTiles) & 1, wc)) {
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t ad = sdesc_sw128(smem_u32(smem + s * P::kCopy), 8192, 1024);
+      const uint64_t bd = sdesc_sw128(smem_u32(smem + P::kTileOff + b * P::kB), 8192, 1024);
+      if (elect_one()) {
 #pragma unroll
         for (uint32_t kk = 0; kk < 4; ++kk)  // 16 tokens = 16 rows of 128 bytes
           umma_bf16(tmem_d + buf * 128, ad + kk * (2048u >> 4), bd + kk * (2048u >> 4), idesc,
@@ -241,18 +248,21 @@ __global__ void __launch_bounds__(192, 2)
         umma_commit(&bempty[b]);
         if (t % P::kSumStages == P::kSumStages - 1 || t == T - 1) umma_commit(&accf[buf]);
       }
-      if (aborted) {
-        umma_commit(done);
-        mbar_drain(done, 0, a.status);
-      }
+      __syncwarp();
     }
+    if (aborted && elect_one()) {
+      umma_commit(done);
+      mbar_drain(done, 0, a.status);
+    }
+    __syncwarp();
   } else {
-    // ---------------------------------------------------- dequantiser warps
+    // ------------------------------------------------------ converting warps
     // Unit i of a stage: 16 codes of row i / 8, columns 16 (i % 8); a thread
     // takes rows dt/8, dt/8 + 16, .. of one column unit, all in one block.
-    const int dt = threadIdx.x - 64;
+    const int grp = (warp - 2) >> 2;  // stages t with t % 2 == grp
+    const int dt = (threadIdx.x - 64) & 127;
     const int cu = dt & 7, r0 = dt >> 3;
-    const int kb = (row0 >> 6) + (cu >> 2);      // block along K
+    const int kb = (row0 >> 6) + (cu >> 2);  // block along K
     const int64_t kbpr = a.K / 64;
     const bool kok = kb < kbpr;
     const uint32_t c0 = (cu & 3) * 2, flip = cu >> 2;  // first of two 16-byte chunks; the order alternates
@@ -264,18 +274,18 @@ __global__ void __launch_bounds__(192, 2)
         pe[i] = (t < T && kok && m < a.M) ? __ldg(exps + m * kbpr + kb) : 0u;  // outside: codes are zero-filled
       }
     };
-    fetch(0);
-    // TMEM row c = 32 q + lane holds part (lane / 16) of j = 16 q + lane % 16;
-    // of the 128 joined columns lanes 0-15 keep the first half, 16-31 the rest.
+    // TMEM row c = 32 q + lane holds part (lane / 16) of j = 16 q + lane % 16.
+    // The groups join 64 columns each; lanes 0-15 keep the first 32 of them,
+    // lanes 16-31 the rest.
     const int q = warp & 3;
-    float sum[64] = {};
+    float sum[32] = {};
     auto add_chunk = [&](int ch) {
       const int buf = ch & 1;
       if (!mbar_wait_warp(&accf[buf], (ch >> 1) & 1, wc)) return false;
       tc_fence_after();
-      const uint32_t tq = tmem_d + buf * 128 + (static_cast<uint32_t>(q * 32) << 16);
+      const uint32_t tq = tmem_d + buf * 128 + (static_cast<uint32_t>(q * 32) << 16) + grp * 64;
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) {
+      for (int cb = 0; cb < 2; ++cb) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(tq + cb * 32, v);
         tmem_ld_wait();
@@ -283,7 +293,7 @@ __global__ void __launch_bounds__(192, 2)
         for (int i = 0; i < 32; ++i) {
           const float x = __uint_as_float(v[i]);
           const float both = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));  // hi + lo
-          if ((lane >= 16) == (cb >= 2)) sum[(cb & 1) * 32 + i] = __fadd_rn(sum[(cb & 1) * 32 + i], both);
+          if ((lane >= 16) == (cb == 1)) sum[i] = __fadd_rn(sum[i], both);
         }
       }
       tc_fence_before();
@@ -292,14 +302,15 @@ __global__ void __launch_bounds__(192, 2)
       return true;
     };
     bool ok = true;
-    for (int t = 0; t < T; ++t) {
-      // the chunk before last is final, or nearly: two are in flight
-      if (t % P::kSumStages == 2 && t > P::kSumStages && !(ok = add_chunk(t / P::kSumStages - 1))) break;
+    fetch(grp);
+    for (int t = grp; t < T; t += 2) {
+      // one chunk in flight, one final or nearly: join it while the MMAs go on
+      if (t % P::kSumStages == 2 + grp && t > P::kSumStages && !(ok = add_chunk(t / P::kSumStages - 1))) break;
       const uint32_t s = t % P::kCopies, b = t % P::kTiles;
       float sc[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[i] = exp_scale(pe[i]);
-      fetch(t + 1);
+      fetch(t + 2);
       if (!mbar_wait_all(&full[s], (t / P::kCopies) & 1, wc) ||
           (t >= static_cast<int>(P::kTiles) && !mbar_wait_all(&bempty[b], ((t / P::kTiles) - 1) & 1, wc))) {
         ok = false;
@@ -311,9 +322,9 @@ __global__ void __launch_bounds__(192, 2)
       for (int i = 0; i < 4; ++i) {
         const int row = r0 + 16 * i;
         const uint4 c = *reinterpret_cast<const uint4*>(raw + row * 128 + cu * 16);
-        const uint2 p = codes4_to_bf16(c.x, sc[i]), q = codes4_to_bf16(c.y, sc[i]), v = codes4_to_bf16(c.z, sc[i]),
+        const uint2 p = codes4_to_bf16(c.x, sc[i]), q2 = codes4_to_bf16(c.y, sc[i]), v = codes4_to_bf16(c.z, sc[i]),
                     w = codes4_to_bf16(c.w, sc[i]);
-        const uint4 lo = make_uint4(p.x, p.y, q.x, q.y), hi = make_uint4(v.x, v.y, w.x, w.y);
+        const uint4 lo = make_uint4(p.x, p.y, q2.x, q2.y), hi = make_uint4(v.x, v.y, w.x, w.y);
         uint8_t* dst = tile + row * 128;
         const uint32_t sw = row & 7;
         *reinterpret_cast<uint4*>(dst + (((c0 + flip) ^ sw) << 4)) = flip ? hi : lo;
@@ -326,16 +337,16 @@ __global__ void __launch_bounds__(192, 2)
     // -------------------------------------------------- sums -> partial tile
     if (ok && T > 0) {  // the chunks the loop did not reach: the last, and the one before a short last
       const int last = (T - 1) / P::kSumStages;
-      const int first = last - ((last > 0 && (T - 1) % P::kSumStages < 2) ? 1 : 0);
+      const int first = last - ((last > 0 && (T - 1) % P::kSumStages < 2 + grp) ? 1 : 0);
       for (int ch = first; ok && ch <= last; ++ch) ok = add_chunk(ch);
     }
     if (ok) {  // the copy ring is idle: its last stage's MMAs are done
       float* part = reinterpret_cast<float*>(smem);
       const int j = 16 * q + (lane & 15);
       if (j < rw) {
-        float* dst = part + j * P::kLd + (lane >> 4) * 64;
+        float* dst = part + j * P::kLd + grp * 64 + (lane >> 4) * 32;
 #pragma unroll
-        for (int i = 0; i < 64; i += 4)
+        for (int i = 0; i < 32; i += 4)
           *reinterpret_cast<float4*>(dst + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
       }
     }
@@ -402,7 +413,7 @@ cudaError_t launch_act8_da(const CUtensorMap& tm_du, const CUtensorMap& tm_x, co
   // unsplit products as clusters of two tiles, as in skinny.cu: they run
   // beside a CTA-pair GEMM and then sit on both SMs of a TPC
   const dim3 cluster = (splits == 1 && grid_rows % 2 == 0) ? dim3(2, 1, 1) : dim3(1, static_cast<unsigned>(splits), 1);
-  return launch_kernel(act8_da_kernel, dim3(grid_rows, splits, 1), dim3(192), ActDaPlan::kSmem, stream, cluster, tm_du,
+  return launch_kernel(act8_da_kernel, dim3(grid_rows, splits, 1), dim3(kActDaThreads), ActDaPlan::kSmem, stream, cluster, tm_du,
                        tm_x, exps, a);
 }
 
