@@ -1330,6 +1330,8 @@ qlora_status qlora_linear_bwd_dropout_act8(const uint16_t* dY, const uint8_t* co
 struct HeadPlanHost {
   int64_t piece = 0;  // vocabulary rows per piece (a multiple of the tile)
   int64_t pieces = 0;
+  int64_t tw = 0;                // columns of a logit tile
+  int64_t ldg = 0, parts = 0;    // per piece: columns its tiles cover, and their halves
   int64_t splits = 1, kper = 0;  // slices of a piece's dH contraction, 64-deep stages each
   size_t off_cnt = 0, off_z = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_sum = 0, off_pl = 0;
   size_t off_g = 0, off_acc = 0, off_w = 0, total = 0;
@@ -1354,6 +1356,23 @@ static void head_splits(int64_t tiles, int64_t kst, int64_t& splits, int64_t& pe
   splits = cdiv(kst, per);
 }
 
+// Columns of a logit tile: the width that makes the fewest column-times of
+// waves of 74 CTA pairs, a tile costing its width and about 16 columns' time
+// more (its token side, filling and draining).  256 when the waves are many;
+// 32000 rows of one token tile: 143 tiles of 224 instead of 125 of 256, whose
+// second wave is two thirds empty.
+static int64_t head_tile_width(int64_t mt, int64_t cols) {
+  int64_t best = kHeadTile, cost = -1;
+  for (int64_t w = kHeadTile; w >= 64; w -= 32) {
+    const int64_t c = cdiv(mt * cdiv(cols, w), kSms / 2) * (w + 16);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = w;
+    }
+  }
+  return best;
+}
+
 static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op) {
   HeadPlanHost p;
   const int64_t tile = kHeadTile;
@@ -1370,6 +1389,9 @@ static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op)
   p.pieces = cdiv(vt * tile, piece);
   p.piece = cdiv(vt, p.pieces) * tile;  // even pieces
   p.pieces = cdiv(vt * tile, p.piece);
+  p.tw = head_tile_width(mt, std::min(p.piece, V));
+  p.ldg = cdiv(p.piece, p.tw) * p.tw;
+  p.parts = 2 * cdiv(p.piece, p.tw);
   if (op != QLORA_HEAD_FWD) head_splits(mt * cdiv(D, tile), p.piece / 64, p.splits, p.kper);
   size_t off = 0;
   auto take = [&off](size_t bytes) {
@@ -1379,7 +1401,7 @@ static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op)
   };
   const size_t t = static_cast<size_t>(T);
   if (op != QLORA_HEAD_BWD) {
-    const int64_t parts = 2 * (op == QLORA_HEAD_FWD ? vt : p.piece / tile);
+    const int64_t parts = (op == QLORA_HEAD_FWD ? p.pieces : 1) * p.parts;
     p.off_cnt = take(8);
     p.off_z = take(4 * t);
     p.off_part = take(8 * t * static_cast<size_t>(parts));
@@ -1392,7 +1414,7 @@ static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op)
     p.off_pl = take(4 * t);
   }
   if (op != QLORA_HEAD_FWD) {
-    p.off_g = take(2 * t * static_cast<size_t>(p.piece));
+    p.off_g = take(2 * t * static_cast<size_t>(p.ldg));
     if (p.pieces > 1 || p.splits > 1)
       p.off_acc = take(4 * static_cast<size_t>(p.splits * mt * tile) * static_cast<size_t>(cdiv(D, tile) * tile));
   }
@@ -1406,7 +1428,7 @@ static qlora_status check_head_shape(int64_t T, int64_t V, int64_t D, bool nf4) 
   if (T < 0 || T >= big - kHeadTile || V < 1 || V >= big - kHeadTile) return QLORA_ERR_SHAPE;
   if (D < 8 || D > (int64_t(1) << 20) || D % (nf4 ? 64 : 8) != 0 || V * D >= (int64_t(1) << 40)) return QLORA_ERR_SHAPE;
   // tiles of every product (and of its slices) are counted in 32 bits
-  if (cdiv(T, kHeadTile) * cdiv(std::max(V, D), kHeadTile) >= big / 64) return QLORA_ERR_SHAPE;
+  if (cdiv(T, kHeadTile) * cdiv(std::max(V, D), kHeadTile) >= big / 256) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
 
@@ -1479,7 +1501,8 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
   a.labels = c.labels;
   a.ignore = c.ignore;
   a.g = g;
-  a.ldg = p.piece;
+  a.ldg = p.ldg;
+  a.tw = static_cast<int>(p.tw);
   a.lse = c.lse_in;
   a.status = d_status;
   a.tab = tables();
@@ -1505,8 +1528,8 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
 
   CUtensorMap mh, mg, mw, mwt;
   if (!map_bf16_ld(&mh, c.H, T, D, c.ldh, 64, 128)) return QLORA_ERR_CUDA;
-  if (op != QLORA_HEAD_FWD && !map_bf16_ld(&mg, g, T, p.piece, p.piece, 64, 128)) return QLORA_ERR_CUDA;
-  if (!nf4 && (!map_bf16_ld(&mw, hd.w, V, D, hd.ld, 64, 128) || !map_bf16_ld(&mwt, hd.w, V, D, hd.ld, 64, 64)))
+  const uint32_t wbox = static_cast<uint32_t>(p.tw / 2);
+  if (!nf4 && (!map_bf16_ld(&mw, hd.w, V, D, hd.ld, 64, wbox) || !map_bf16_ld(&mwt, hd.w, V, D, hd.ld, 64, 64)))
     return QLORA_ERR_CUDA;
 
   for (int64_t i = 0; i < p.pieces; ++i) {
@@ -1515,7 +1538,7 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     if (nf4) {  // v0 * D is a whole number of double-quantisation groups: v0 % 256 == 0, D % 64 == 0
       const int64_t e0 = v0 * D;
       CUtensorMap out;
-      if (!map_bf16(&out, wbuf, pv * D / 64, 64, 64, 32, 128) || !map_bf16_ld(&mw, wbuf, pv, D, D, 64, 128) ||
+      if (!map_bf16(&out, wbuf, pv * D / 64, 64, 64, 32, 128) || !map_bf16_ld(&mw, wbuf, pv, D, D, 64, wbox) ||
           !map_bf16_ld(&mwt, wbuf, pv, D, D, 64, 64))
         return QLORA_ERR_CUDA;
       ProfScope ps(kKDequantize, cs);
@@ -1526,20 +1549,21 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     a.b_row0 = nf4 ? 0 : static_cast<int>(v0);
     a.v0 = v0;
     a.ncols = static_cast<int>(pv);
-    a.ntiles = static_cast<int>(cdiv(pv, kHeadTile));
+    a.ntiles = static_cast<int>(cdiv(pv, p.tw));
     a.kst = static_cast<int>(cdiv(D, 64));
     a.kchunk = 8;
     a.splits = 1;
     a.kper = a.kst;
     float2* part = reinterpret_cast<float2*>(at(p.off_part));
-    a.part = op == QLORA_HEAD_FWD ? part + v0 / kHeadTile * 2 * T : part;
+    a.part = op == QLORA_HEAD_FWD ? part + i * p.parts * T : part;
     {
       const int mode = op == QLORA_HEAD_FWD ? kHeadLoss : op == QLORA_HEAD_BWD ? kHeadProb : kHeadExp;
       ProfScope ps(kKHeadLogits, cs);
       if (qlora_status st = from_cuda(launch_head_gemm(mode, mh, mw, a, cs))) return st;
     }
     if (op == QLORA_HEAD_STEP || (op == QLORA_HEAD_FWD && last)) {
-      cb.nparts = 2 * (op == QLORA_HEAD_FWD ? static_cast<int>(cdiv(V, kHeadTile)) : a.ntiles);
+      cb.nparts = 2 * a.ntiles + (op == QLORA_HEAD_FWD ? static_cast<int>(i * p.parts) : 0);
+      cb.part_cols = static_cast<int>(p.tw / 2);
       cb.first = op == QLORA_HEAD_FWD || first;
       cb.last = last;
       if (op == QLORA_HEAD_STEP) {
@@ -1548,13 +1572,15 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
         cb.row_sum = reinterpret_cast<float*>(at(p.off_sum));
         cb.p_label = reinterpret_cast<float*>(at(p.off_pl));
         cb.e = g;
-        cb.lde = p.piece;
+        cb.lde = p.ldg;
       }
       ProfScope ps(kKHeadCombine, cs);
       if (qlora_status st = from_cuda(launch_head_combine(cb, cs))) return st;
     }
     if (op != QLORA_HEAD_FWD) {
       HeadArgs d = a;
+      // columns no tile covers read as zero
+      if (!map_bf16_ld(&mg, g, T, a.ntiles * p.tw, p.ldg, 64, 128)) return QLORA_ERR_CUDA;
       d.ncols = static_cast<int>(D);
       d.ntiles = static_cast<int>(cdiv(D, kHeadTile));
       d.kst = static_cast<int>(cdiv(pv, 64));

@@ -10,11 +10,11 @@
 // kernel on CTA pairs makes every product; what its epilogue does with a tile
 // is the mode:
 //
-//   Loss  per row and 128 columns the maximum m and sum exp(l - m): 8 bytes
+//   Loss  per row and half tile the maximum m and sum exp(l - m): 8 bytes
 //   Prob  exp(l - lse), less 1 at the label (in fp32), rounded to bf16
 //   Exp   exp(l - ref), 0 at the label, rounded to bf16, and (ref, sum): the
 //         gradient's operand before lse is known.  ref is 0 while the maximum
-//         of the row's 128 columns lies within +-40 (exp then stays far inside bf16's and
+//         of the row's half tile lies within +-40 (exp then stays far inside bf16's and
 //         fp32's range, and the reference costs no precision: both types
 //         float), else that maximum
 //   Grad  (second product) the piece's bf16 [T, piece] operand times W's rows
@@ -40,7 +40,7 @@ constexpr float kRefRange = 40.0f;  // tile maxima within +-kRefRange share the 
 
 struct HeadPlan {
   static constexpr uint32_t kA = 16384;  // 128 tokens x 64
-  static constexpr uint32_t kB = 16384;  // 128 columns x 64
+  static constexpr uint32_t kB = 16384;  // up to 128 columns x 64
   static constexpr uint32_t kStage = kA + kB;
   static constexpr uint32_t kStages = 6;
   static constexpr uint32_t kBarOff = kStages * kStage;
@@ -85,11 +85,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-// Adds this thread's 128 columns of a finished accumulator to its registers
-// (16 at a time: 128 sums leave few registers beside them).
-__device__ __forceinline__ void add_chunk(uint32_t taddr, bool first, float (&l)[kHalf]) {
+// Adds this thread's columns (a multiple of 16, up to 128) of a finished
+// accumulator to its registers (16 at a time: 128 sums leave few registers beside them).
+__device__ __forceinline__ void add_chunk(uint32_t taddr, bool first, int cols, float (&l)[kHalf]) {
 #pragma unroll
   for (int cb = 0; cb < kHalf / 16; ++cb) {
+    if (cb * 16 >= cols) break;
     uint32_t v[16];
     tmem_ld_32x32b_x16(taddr + cb * 16, v);
     tmem_ld_wait();
@@ -126,13 +127,18 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32
                      pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
 }
 
-// 128 bf16 (16-byte aligned) from fp32.
-__device__ __forceinline__ void store_bf16(uint16_t* dst, const float (&v)[kHalf]) {
+// `cols` bf16 (a multiple of 16; 32-byte aligned) from fp32, whole sectors a store.
+__device__ __forceinline__ void store_bf16(uint16_t* dst, int cols, const float (&v)[kHalf]) {
 #pragma unroll
-  for (int j = 0; j < kHalf / 8; ++j)
-    reinterpret_cast<uint4*>(dst)[j] =
-        make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                   pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+  for (int j = 0; j < kHalf; j += 16) {
+    if (j >= cols) break;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[j + 2 * i], v[j + 2 * i + 1]);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + j), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  }
 }
 
 // fp32 sums between pieces and of split contractions: per (split, tile) and
@@ -202,9 +208,10 @@ __device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t l
 
 }  // namespace
 
-// A cluster of two CTAs computes 256 tokens x 256 columns per tile: each CTA
+// A cluster of two CTAs computes 256 tokens x tw columns per tile (256, or for
+// products of few tiles the width that fills its last wave): each CTA
 // holds 128 token rows (A) and half of the columns (B) of a 64-deep stage, one
-// thread of the leader issues M = 256, N = 256 MMAs, and each CTA's tensor
+// thread of the leader issues M = 256, N = tw MMAs, and each CTA's tensor
 // memory gets its 128 rows.  Persistent: one pair per TPC.
 //
 // The tensor core truncates when it adds to its fp32 accumulator: the sum
@@ -239,6 +246,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int mn = a.mtiles * a.ntiles;
+  const int tw = MODE == kHeadGrad ? kHeadTile : a.tw;  // columns of a tile
   const int tiles = mn * (MODE == kHeadGrad ? a.splits : 1);  // (split, tile)
 
   if (threadIdx.x == 0) {
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         const int split = tile / mn;
         head_tile(tile - split * mn, a.mtiles, a.ntiles, m, n);
         const int arow = m * kHeadTile + static_cast<int>(rank) * 128;
-        const int bcol = n * kHeadTile + static_cast<int>(rank) * 128;
+        const int bcol = n * tw + static_cast<int>(rank) * (tw / 2);
         const int k1 = min(a.kst, (split + 1) * a.kper);
         for (int kt = split * a.kper; kt < k1; ++kt, ++it) {
           const uint32_t s = static_cast<uint32_t>(it % P::kStages);
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
           }
           uint8_t* st = smem + s * P::kStage;
           const uint32_t full0 = dsmem_addr(&full[s], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * P::kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * P::kA + tw * 128u);
           tma_load_2d_pair(st, &tm_a, full0, kt * 64, arow);
           if (MODE == kHeadGrad) {  // W's rows are the contraction: two 64-column atoms
             tma_load_2d_pair(st + P::kA, &tm_b, full0, bcol, a.b_row0 + kt * 64);
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA (leader)
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, 0, MODE == kHeadGrad ? 1 : 0);
+      const uint32_t idesc = idesc_bf16_f32(256, tw, 0, MODE == kHeadGrad ? 1 : 0);
       constexpr uint32_t b_step = MODE == kHeadGrad ? (2048u >> 4) : (32u >> 4);
       int64_t it = 0;
       int acc = 0;  // chunks begun
@@ -360,9 +368,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;             // TMEM lanes 32 q ..
-    const int half = (warp - 2) >> 2;   // columns 128 half ..
+    const int half = (warp - 2) >> 2;   // columns hw half ..
+    const int hw = tw / 2;
     const int et = threadIdx.x - 64;
-    const uint32_t tq = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + half * kHalf;
+    const uint32_t tq = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + half * hw;
     int acc = 0;
     for (int tile = pair; tile < tiles; tile += pairs) {
       int m, n;
@@ -371,8 +380,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       const int kn = min(a.kst, (split + 1) * a.kper) - split * a.kper;
       const int t = m * kHeadTile + static_cast<int>(rank) * 128 + q * 32 + lane;
       const bool rok = t < a.T;
-      const int n0 = n * kHeadTile + half * kHalf;
-      const int nv = min(kHalf, a.ncols - n0);  // this thread's columns (may be none)
+      const int n0 = n * tw + half * hw;
+      const int nv = min(hw, a.ncols - n0);  // this thread's columns (may be none)
       int64_t label = -1;
       bool counted = false;
       if (rok) {
@@ -441,7 +450,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
           break;
         }
         tc_fence_after();
-        add_chunk(tq + buf * 256, k0 == 0, l);
+        add_chunk(tq + buf * 256, k0 == 0, hw, l);
         tc_fence_before();  // this warp's reads of the accumulator are done
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(dsmem_addr(&acce[buf], 0));
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         }
         if (rok) {
           a.part[static_cast<int64_t>(2 * n + half) * a.T + t] = make_float2(ref, (p[0] + p[1]) + (p[2] + p[3]));
-          store_bf16(a.g + static_cast<int64_t>(t) * a.ldg + n0, l);
+          store_bf16(a.g + static_cast<int64_t>(t) * a.ldg + n0, hw, l);
         }
       } else if (MODE == kHeadProb) {
         const float lse = rok ? __ldcg(a.lse + t) : 0.0f;
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
           if (j == lj) l[j] = pl;
         }
         if (rok) {
-          store_bf16(a.g + static_cast<int64_t>(t) * a.ldg + n0, l);
+          store_bf16(a.g + static_cast<int64_t>(t) * a.ldg + n0, hw, l);
           if (n0 == 0 && a.v0 == 0 && !counted && label != a.ignore && a.status) atomicOr(a.status, QLORA_DEV_LABEL);
         }
       }
@@ -639,8 +648,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
         const float fr = __shfl_sync(0xFFFFFFFFu, f, src);
+        if (4 * lane >= a.part_cols) continue;
         uint2* at = reinterpret_cast<uint2*>(a.e + static_cast<int64_t>(blockIdx.x * 32 + src) * a.lde +
-                                             static_cast<int64_t>(j) * kHalf) + lane;
+                                             static_cast<int64_t>(j) * a.part_cols) + lane;
         const uint2 v = *at;
         *at = make_uint2(pack_bf16x2(__uint_as_float(v.x << 16) * fr, __uint_as_float(v.x & 0xFFFF0000u) * fr),
                          pack_bf16x2(__uint_as_float(v.y << 16) * fr, __uint_as_float(v.y & 0xFFFF0000u) * fr));

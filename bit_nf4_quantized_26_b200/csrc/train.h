@@ -56,10 +56,11 @@ struct HeadArgs {
   int64_t v0;             // the piece's first vocabulary index
   int64_t vocab;
   int mtiles, ntiles;
+  int tw;                 // columns of a tile: a multiple of 32 up to 256 (Grad: 256)
   const int64_t* labels;
   int64_t ignore;
   float* label_logit;     // Loss, Exp: [T]
-  float2* part;           // Loss, Exp: (reference, sum of exponentials) [128 columns][T], from the piece's first column
+  float2* part;           // Loss, Exp: (reference, sum of exponentials) [half tile][T], from the piece's first
   const float* lse;       // Prob: [T]
   uint16_t* g;            // Prob, Exp: [T, ldg]
   int64_t ldg;
@@ -83,8 +84,8 @@ struct HeadArgs {
   int32_t* status;
 };
 
-//   tm_a: H [T, dim] (Grad: the piece's [T, ldg]) box {64, 128} SW128;
-//   tm_b: W rows, box {64, 128} SW128 (Grad: {64, 64}).
+//   tm_a: H [T, dim] (Grad: the piece's [T, ntiles tw]) box {64, 128} SW128;
+//   tm_b: W rows, box {64, tw / 2} SW128 (Grad: {64, 64}).
 cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
                              cudaStream_t stream);
 
@@ -94,6 +95,7 @@ cudaError_t launch_head_finish(const HeadArgs& a, cudaStream_t stream);
 // Joins the per-tile statistics of every row; see head_loss.cu.
 struct HeadCombineArgs {
   int T, nparts;
+  int part_cols;           // columns a part covers
   const float2* part;      // [nparts][T]
   const float* label_logit;
   const int64_t* labels;

@@ -140,7 +140,8 @@ typedef struct {
  * their type's alignment only (a shifted view of the labels is fine).
  * Workspaces: qlora_head_loss_workspace_size(T, vocab, dim, nf4, op) bytes with
  * nf4 nonzero for an NF4 head and op one of QLORA_HEAD_FWD / _BWD / _STEP.
- * Beside per-token words it holds 8 bytes per 128 logits (forward, step), a
+ * Beside per-token words it holds 8 bytes per 128 logits (fewer for few tokens;
+ * forward, step), a
  * piece of the probabilities (backward, step: about 128 MB in bf16, at least
  * 2048 columns), fp32 sums [T, dim] (with several pieces, and for few tokens
  * one per slice of the contraction), and a dequantised piece of an NF4 head (at
