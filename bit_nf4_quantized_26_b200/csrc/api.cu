@@ -119,6 +119,7 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t
   const cuuint32_t estr[2] = {1, 1};
   const CUtensorMapSwizzle sw = swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                               : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                      : CU_TENSOR_MAP_SWIZZLE_NONE;
   return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1321,6 +1322,11 @@ qlora_status qlora_linear_bwd_dropout_act8(const uint16_t* dY, const uint8_t* co
 
 // ------------------------------------------------------------------ loss head
 
+// An NF4 head is read from its codes for up to this many tokens: every token
+// tile dequantises every weight again, while the dequantised pieces cost one
+// more pass over the head.
+constexpr int64_t kHeadCodesT = 512;
+
 // How a call walks the vocabulary, and its workspace.  The backward and the
 // step hold a piece's bf16 [T, piece] operand: about 2^26 elements (128 MB,
 // near the L2's size, and deep enough a contraction that reading and writing
@@ -1328,6 +1334,8 @@ qlora_status qlora_linear_bwd_dropout_act8(const uint16_t* dY, const uint8_t* co
 // at least 2048 columns.  An NF4 head is dequantised a piece at a time: at
 // most 2^26 elements.  A forward over a bf16 head has one piece.
 struct HeadPlanHost {
+  bool pair = true;   // tiles of 256 tokens on CTA pairs, or of 128 on single CTAs
+  bool codes = false; // the products read an NF4 head's codes, or its dequantised pieces
   int64_t piece = 0;  // vocabulary rows per piece (a multiple of the tile)
   int64_t pieces = 0;
   int64_t tw = 0;                // columns of a logit tile
@@ -1337,16 +1345,16 @@ struct HeadPlanHost {
   size_t off_g = 0, off_acc = 0, off_w = 0, total = 0;
 };
 
-// Slices of the dH contraction of a piece (kst stages) over `tiles` tiles of
-// 74 CTA pairs: waves x (stages per slice + what a slice's fp32 sums cost to
+// Slices of the dH contraction of a piece (kst stages) over `tiles` tiles and
+// `workers` CTA pairs or CTAs: waves x (stages per slice + what a slice's fp32 sums cost to
 // write and join, about 12 stages' time), slices of at least 8 stages, only
 // while all slices together are under four waves (beyond that the sums cost
 // more than the last wave's idle pairs).
-static void head_splits(int64_t tiles, int64_t kst, int64_t& splits, int64_t& per) {
-  constexpr int64_t kPairs = kSms / 2, kCost = 12;
-  int64_t best = 1, cost = cdiv(tiles, kPairs) * kst;
-  for (int64_t s = 2; s <= kst / 8 && tiles * s <= 4 * kPairs; ++s) {
-    const int64_t c = cdiv(tiles * s, kPairs) * (cdiv(kst, s) + kCost);
+static void head_splits(int64_t tiles, int64_t kst, int64_t workers, int64_t& splits, int64_t& per) {
+  constexpr int64_t kCost = 12;
+  int64_t best = 1, cost = cdiv(tiles, workers) * kst;
+  for (int64_t s = 2; s <= kst / 8 && tiles * s <= 4 * workers; ++s) {
+    const int64_t c = cdiv(tiles * s, workers) * (cdiv(kst, s) + kCost);
     if (c < cost) {
       cost = c;
       best = s;
@@ -1357,14 +1365,14 @@ static void head_splits(int64_t tiles, int64_t kst, int64_t& splits, int64_t& pe
 }
 
 // Columns of a logit tile: the width that makes the fewest column-times of
-// waves of 74 CTA pairs, a tile costing its width and about 16 columns' time
+// waves of the CTA pairs or CTAs, a tile costing its width and about 16 columns' time
 // more (its token side, filling and draining).  256 when the waves are many;
 // 32000 rows of one token tile: 143 tiles of 224 instead of 125 of 256, whose
 // second wave is two thirds empty.
-static int64_t head_tile_width(int64_t mt, int64_t cols) {
-  int64_t best = kHeadTile, cost = -1;
-  for (int64_t w = kHeadTile; w >= 64; w -= 32) {
-    const int64_t c = cdiv(mt * cdiv(cols, w), kSms / 2) * (w + 16);
+static int64_t head_tile_width(int64_t mt, int64_t cols, int64_t widest, int64_t workers) {
+  int64_t best = widest, cost = -1;
+  for (int64_t w = widest; w >= 64; w -= 32) {
+    const int64_t c = cdiv(mt * cdiv(cols, w), workers) * (w + 16);
     if (cost < 0 || c < cost) {
       cost = c;
       best = w;
@@ -1376,23 +1384,27 @@ static int64_t head_tile_width(int64_t mt, int64_t cols) {
 static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op) {
   HeadPlanHost p;
   const int64_t tile = kHeadTile;
-  const int64_t vt = cdiv(V, tile), mt = cdiv(T, tile);
+  p.pair = T > 128;
+  p.codes = nf4 && T <= kHeadCodesT;
+  const int64_t workers = head_workers(p.pair);
+  const int64_t vt = cdiv(V, tile), mt = cdiv(T, p.pair ? 256 : 128);
+  const int64_t trows = mt * (p.pair ? 256 : 128);
   int64_t piece = vt * tile;
   if (op != QLORA_HEAD_FWD) {
-    const int64_t fit = (int64_t(1) << 26) / (mt * tile) / tile * tile;
+    const int64_t fit = (int64_t(1) << 26) / trows / tile * tile;
     piece = std::min(piece, std::max<int64_t>(fit, 2048));
   }
-  if (nf4) {
+  if (nf4 && !p.codes) {
     const int64_t fit = (int64_t(1) << 26) / D / tile * tile;
     piece = std::min(piece, std::max<int64_t>(fit, 2048));
   }
   p.pieces = cdiv(vt * tile, piece);
   p.piece = cdiv(vt, p.pieces) * tile;  // even pieces
   p.pieces = cdiv(vt * tile, p.piece);
-  p.tw = head_tile_width(mt, std::min(p.piece, V));
+  p.tw = head_tile_width(mt, std::min(p.piece, V), p.codes ? 128 : 256, workers);
   p.ldg = cdiv(p.piece, p.tw) * p.tw;
   p.parts = 2 * cdiv(p.piece, p.tw);
-  if (op != QLORA_HEAD_FWD) head_splits(mt * cdiv(D, tile), p.piece / 64, p.splits, p.kper);
+  if (op != QLORA_HEAD_FWD) head_splits(mt * cdiv(D, tile), p.piece / 64, workers, p.splits, p.kper);
   size_t off = 0;
   auto take = [&off](size_t bytes) {
     const size_t at = off;
@@ -1416,9 +1428,9 @@ static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op)
   if (op != QLORA_HEAD_FWD) {
     p.off_g = take(2 * t * static_cast<size_t>(p.ldg));
     if (p.pieces > 1 || p.splits > 1)
-      p.off_acc = take(4 * static_cast<size_t>(p.splits * mt * tile) * static_cast<size_t>(cdiv(D, tile) * tile));
+      p.off_acc = take(4 * static_cast<size_t>(p.splits * trows) * static_cast<size_t>(cdiv(D, tile) * tile));
   }
-  if (nf4) p.off_w = take(2 * static_cast<size_t>(std::min(p.piece, V)) * static_cast<size_t>(D));
+  if (nf4 && !p.codes) p.off_w = take(2 * static_cast<size_t>(std::min(p.piece, V)) * static_cast<size_t>(D));
   p.total = off;
   return p;
 }
@@ -1497,7 +1509,9 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
   HeadArgs a{};
   a.T = static_cast<int>(T);
   a.vocab = V;
-  a.mtiles = static_cast<int>(cdiv(T, kHeadTile));
+  a.pair = p.pair;
+  a.nf4 = p.codes;
+  a.mtiles = static_cast<int>(cdiv(T, p.pair ? 256 : 128));
   a.labels = c.labels;
   a.ignore = c.ignore;
   a.g = g;
@@ -1527,15 +1541,20 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
   }
 
   CUtensorMap mh, mg, mw, mwt;
-  if (!map_bf16_ld(&mh, c.H, T, D, c.ldh, 64, 128)) return QLORA_ERR_CUDA;
-  const uint32_t wbox = static_cast<uint32_t>(p.tw / 2);
+  const uint32_t abox = static_cast<uint32_t>(std::min<int64_t>(128, cdiv(T, 8) * 8));
+  a.arows = static_cast<int>(abox);
+  if (!map_bf16_ld(&mh, c.H, T, D, c.ldh, 64, abox)) return QLORA_ERR_CUDA;
+  const uint32_t wbox = static_cast<uint32_t>(p.pair ? p.tw / 2 : p.tw);
+if (p.codes && (!map_u8(&mw, hd.codes, V, D / 2, 32, wbox, 32) ||
+                  !map_u8(&mwt, hd.codes, V, D / 2, p.pair ? 64 : 128, 64, p.pair ? 64 : 128)))
+    return QLORA_ERR_CUDA;
   if (!nf4 && (!map_bf16_ld(&mw, hd.w, V, D, hd.ld, 64, wbox) || !map_bf16_ld(&mwt, hd.w, V, D, hd.ld, 64, 64)))
     return QLORA_ERR_CUDA;
 
   for (int64_t i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.piece, pv = std::min(p.piece, V - v0);
     const bool first = i == 0, last = i == p.pieces - 1;
-    if (nf4) {  // v0 * D is a whole number of double-quantisation groups: v0 % 256 == 0, D % 64 == 0
+    if (nf4 && !p.codes) {  // v0 * D is a whole number of double-quantisation groups: v0 % 256 == 0, D % 64 == 0
       const int64_t e0 = v0 * D;
       CUtensorMap out;
       if (!map_bf16(&out, wbuf, pv * D / 64, 64, 64, 32, 128) || !map_bf16_ld(&mw, wbuf, pv, D, D, 64, wbox) ||
@@ -1546,8 +1565,9 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
                                                             hd.mean, pv * D, wbuf, &out, tables(), cs)))
         return st;
     }
-    a.b_row0 = nf4 ? 0 : static_cast<int>(v0);
+    a.b_row0 = nf4 && !p.codes ? 0 : static_cast<int>(v0);
     a.v0 = v0;
+    a.wrows = static_cast<int>(pv);
     a.ncols = static_cast<int>(pv);
     a.ntiles = static_cast<int>(cdiv(pv, p.tw));
     a.kst = static_cast<int>(cdiv(D, 64));
@@ -1580,7 +1600,7 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     if (op != QLORA_HEAD_FWD) {
       HeadArgs d = a;
       // columns no tile covers read as zero
-      if (!map_bf16_ld(&mg, g, T, a.ntiles * p.tw, p.ldg, 64, 128)) return QLORA_ERR_CUDA;
+      if (!map_bf16_ld(&mg, g, T, a.ntiles * p.tw, p.ldg, 64, abox)) return QLORA_ERR_CUDA;
       d.ncols = static_cast<int>(D);
       d.ntiles = static_cast<int>(cdiv(D, kHeadTile));
       d.kst = static_cast<int>(cdiv(pv, 64));

@@ -6,8 +6,8 @@
 //   l = H W^T    lse = log sum exp l    loss = lse - l[label]
 //   dH = g (exp(l - lse) - onehot) W
 //
-// The logits exist only as 256 x 256 fp32 tiles in tensor memory.  One GEMM
-// kernel on CTA pairs makes every product; what its epilogue does with a tile
+// The logits exist only as fp32 tiles in tensor memory.  One GEMM kernel
+// makes every product; what its epilogue does with a tile
 // is the mode:
 //
 //   Loss  per row and half tile the maximum m and sum exp(l - m): 8 bytes
@@ -38,21 +38,36 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRefRange = 40.0f;  // tile maxima within +-kRefRange share the reference 0
 
+// PAIR: tiles of 256 tokens on CTA pairs; otherwise, for at most 128 tokens,
+// of 128 on single CTAs (twice the workers, none of the tile without tokens).
+// NF4: W's tile is dequantised into the ring from its codes.
+template <int MODE, bool PAIR, bool NF4>
 struct HeadPlan {
-  static constexpr uint32_t kA = 16384;  // 128 tokens x 64
-  static constexpr uint32_t kB = 16384;  // up to 128 columns x 64
-  static constexpr uint32_t kStage = kA + kB;
-  static constexpr uint32_t kStages = 6;
+  static constexpr bool kGrad = MODE == kHeadGrad;
+  // columns of a tile at most: an NF4 kernel's extra warps leave the epilogue
+  // registers for 64 sums a thread
+  static constexpr int kMaxTw = NF4 && !kGrad ? 128 : 256;
+  static constexpr int kCols = kMaxTw / 2;                       // an epilogue thread's
+  static constexpr int kBRows = PAIR ? kMaxTw / 2 : kMaxTw;      // columns of the tile in this CTA's ring
+  static constexpr uint32_t kA = 16384;                          // 128 tokens x 64
+  static constexpr uint32_t kB = kBRows * 128;
+  static constexpr uint32_t kC = NF4 ? kBRows * 32 : 0;          // packed codes of the same
+  static constexpr uint32_t kStage = kA + kB + kC;
+  // Warp 0: copies; warp 1: MMAs; then eight epilogue warps (two per quarter of
+  // the rows, each with half of the columns); NF4: eight that dequantise.
+  static constexpr int kThreads = 64 + 256 + (NF4 ? 256 : 0);
+  // The dequantisers as groups that take the stages in turn, a 64-weight block
+  // a thread; the ring is a multiple of the groups, so a slot's earlier stages
+  // are the same group's and its parity waits cannot run a phase ahead.
+  static constexpr int kGroups = NF4 ? 256 / kBRows : 1;
+  static constexpr int kArrive = (PAIR ? 2 : 1) * 8 / kGroups;   // their arrivals on a stage
+  static constexpr uint32_t kStages = (232448 - 2048) / kStage / (NF4 ? kGroups : 2) * (NF4 ? kGroups : 2);
   static constexpr uint32_t kBarOff = kStages * kStage;
-  static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
-  static_assert(kSmem <= 232448u, "too much shared memory");
+  static constexpr uint32_t kSmem = 1024 + kBarOff + 512;
+  static_assert(kSmem <= 232448u && kStages >= 4, "the ring does not fit");
 };
 
-// Warp 0: copies; warp 1: MMAs (leader CTA); warps 2..9: epilogue (two per
-// quarter of the rows, each with half of the columns).
 constexpr int kEpiWarps = 8;
-constexpr int kHeadThreads = 64 + 32 * kEpiWarps;
-constexpr int kHalf = kHeadTile / 2;  // columns an epilogue thread holds
 constexpr int kGroupM = 8;  // token tiles walked together (raster)
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -85,11 +100,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-// Adds this thread's columns (a multiple of 16, up to 128) of a finished
-// accumulator to its registers (16 at a time: 128 sums leave few registers beside them).
-__device__ __forceinline__ void add_chunk(uint32_t taddr, bool first, int cols, float (&l)[kHalf]) {
+// Adds this thread's columns (a multiple of 16) of a finished accumulator to
+// its registers (16 at a time: 128 sums leave few registers beside them).
+template <int N>
+__device__ __forceinline__ void add_chunk(uint32_t taddr, bool first, int cols, float (&l)[N]) {
 #pragma unroll
-  for (int cb = 0; cb < kHalf / 16; ++cb) {
+  for (int cb = 0; cb < N / 16; ++cb) {
     if (cb * 16 >= cols) break;
     uint32_t v[16];
     tmem_ld_32x32b_x16(taddr + cb * 16, v);
@@ -102,18 +118,20 @@ __device__ __forceinline__ void add_chunk(uint32_t taddr, bool first, int cols, 
   }
 }
 
-__device__ __forceinline__ float max_all(const float (&l)[kHalf]) {
+template <int N>
+__device__ __forceinline__ float max_all(const float (&l)[N]) {
   float m[4] = {l[0], l[1], l[2], l[3]};
 #pragma unroll
-  for (int j = 4; j < kHalf; ++j) m[j & 3] = fmaxf(m[j & 3], l[j]);
+  for (int j = 4; j < N; ++j) m[j & 3] = fmaxf(m[j & 3], l[j]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 // Element `at` of l (0 if there is none there).
-__device__ __forceinline__ float pick(const float (&l)[kHalf], int at) {
+template <int N>
+__device__ __forceinline__ float pick(const float (&l)[N], int at) {
   float z = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kHalf; ++j) z = j == at ? l[j] : z;
+  for (int j = 0; j < N; ++j) z = j == at ? l[j] : z;
   return z;
 }
 
@@ -128,9 +146,10 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32
 }
 
 // `cols` bf16 (a multiple of 16; 32-byte aligned) from fp32, whole sectors a store.
-__device__ __forceinline__ void store_bf16(uint16_t* dst, int cols, const float (&v)[kHalf]) {
+template <int N>
+__device__ __forceinline__ void store_bf16(uint16_t* dst, int cols, const float (&v)[N]) {
 #pragma unroll
-  for (int j = 0; j < kHalf; j += 16) {
+  for (int j = 0; j < N; j += 16) {
     if (j >= cols) break;
     uint32_t w[8];
 #pragma unroll
@@ -144,8 +163,9 @@ __device__ __forceinline__ void store_bf16(uint16_t* dst, int cols, const float 
 // fp32 sums between pieces and of split contractions: per (split, tile) and
 // CTA, the epilogue threads' registers as 32 rows of 256 float4, so that every
 // access of a warp is 512 contiguous bytes.
-constexpr int kSumStride = 32 * kEpiWarps;             // float4 per row
-constexpr int kSumBlock = kHalf / 4 * kSumStride;      // float4 per CTA of a tile
+constexpr int kSumCols = kHeadTile / 2;                 // a thread's columns
+constexpr int kSumStride = 32 * kEpiWarps;              // float4 per row
+constexpr int kSumBlock = kSumCols / 4 * kSumStride;    // float4 per CTA of a tile
 
 // dH_t = ca * (the row's sum over the vocabulary) + cl * W[label].
 __device__ __forceinline__ void grad_row_factors(const HeadArgs& a, int t, float& ca, float& cl) {
@@ -208,11 +228,13 @@ __device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t l
 
 }  // namespace
 
-// A cluster of two CTAs computes 256 tokens x tw columns per tile (256, or for
-// products of few tiles the width that fills its last wave): each CTA
-// holds 128 token rows (A) and half of the columns (B) of a 64-deep stage, one
-// thread of the leader issues M = 256, N = tw MMAs, and each CTA's tensor
-// memory gets its 128 rows.  Persistent: one pair per TPC.
+// A tile is 256 tokens (a CTA pair's; 128 of a single CTA) x tw columns: 256,
+// or for products of few tiles the width that fills the last wave.  Per 64-deep
+// stage each CTA holds its 128 token rows (A; rows without a token hold
+// whatever the ring held: rows do not mix) and its columns (B: half of the
+// tile's in a pair), one thread issues the MMAs (in a pair the leader's, M =
+// 256), and each CTA's tensor memory gets its 128 rows.  Persistent: one pair
+// per TPC, or one CTA per SM.
 //
 // The tensor core truncates when it adds to its fp32 accumulator: the sum
 // drifts towards zero by about 2^-24 of itself per K = 16 step (measured:
@@ -222,16 +244,21 @@ __device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t l
 // finished one to their registers, rounding to nearest, while the next runs.
 // dH, rounded to bf16, takes a whole slice of its contraction as one chunk.
 //
-// Barriers: full[s] (leader: both CTAs' tiles landed), empty[s] (both: the
-// stage's MMAs are done), accf[b] (both: the chunk's accumulator is final),
-// acce[b] (leader: all epilogue warps of both CTAs have read it), done
-// (leader: the last commit).  What an earlier kernel of the same call wrote is read past L1
+// Barriers (leader: the pair's first CTA, or the single one): full[s] (leader:
+// the stage's copies landed, and its dequantised tiles are written), empty[s]
+// (all: the stage's MMAs are done), cfull[s] (each: an NF4 stage's codes
+// landed), accf[b] (all: the chunk's accumulator is
+// final), acce[b] (leader: all epilogue warps have read it), done (leader: the
+// last commit).  What an earlier kernel of the same call wrote is read past L1
 // (__ldcg): launches overlap, and nothing is kept there from one to the next.
-template <int MODE>
-__global__ void __launch_bounds__(kHeadThreads, 1)
+template <int MODE, bool PAIR, bool NF4>
+__global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ HeadArgs a) {
-  using P = HeadPlan;
+  using P = HeadPlan<MODE, PAIR, NF4>;
+  constexpr bool kGrad = P::kGrad;
+  constexpr uint32_t kCtas = PAIR ? 2 : 1;
+  constexpr int kTokens = 128 * kCtas;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBarOff);
@@ -239,24 +266,26 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   uint64_t* accf = empty + P::kStages;
   uint64_t* acce = accf + 2;
   uint64_t* done = acce + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* cfull = done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cfull + P::kStages);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+  const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
   const int mn = a.mtiles * a.ntiles;
-  const int tw = MODE == kHeadGrad ? kHeadTile : a.tw;  // columns of a tile
-  const int tiles = mn * (MODE == kHeadGrad ? a.splits : 1);  // (split, tile)
+  const int tw = kGrad ? kHeadTile : a.tw;           // columns of a tile
+  const int tiles = mn * (kGrad ? a.splits : 1);     // (split, tile)
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < P::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + (NF4 ? P::kArrive : 0));
       mbar_init(&empty[s], 1);
+      mbar_init(&cfull[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
-      mbar_init(&acce[b], 2 * kEpiWarps);
+      mbar_init(&acce[b], kCtas * kEpiWarps);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -267,12 +296,18 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     tma_prefetch_desc(&tm_b);
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, 512);
-    tmem_relinquish_pair();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncwarp();
-  cluster_sync_all();
+  if constexpr (PAIR) cluster_sync_all();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_d = *tmem_slot;
   const WaitCtx wc{abort_flag, a.status};
@@ -286,13 +321,15 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     if (lane == 0) {
       int64_t it = 0;  // stages issued
       bool ok = true;
-      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+      for (int tile = worker; ok && tile < tiles; tile += workers) {
         int m, n;
         const int split = tile / mn;
         head_tile(tile - split * mn, a.mtiles, a.ntiles, m, n);
-        const int arow = m * kHeadTile + static_cast<int>(rank) * 128;
+        const int arow = m * kTokens + static_cast<int>(rank) * 128;
         const int bcol = n * tw + static_cast<int>(rank) * (tw / 2);
         const int k1 = min(a.kst, (split + 1) * a.kper);
+        const bool mine = arow < a.T;  // else the CTA's rows hold no token: nothing to copy
+        const uint32_t bytes = (PAIR && arow + 128 < a.T ? 2 : 1) * a.arows * 128u + (NF4 ? 0 : tw * 128u);
         for (int kt = split * a.kper; kt < k1; ++kt, ++it) {
           const uint32_t s = static_cast<uint32_t>(it % P::kStages);
           const uint32_t u = static_cast<uint32_t>(it / P::kStages);
@@ -301,31 +338,53 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
             break;
           }
           uint8_t* st = smem + s * P::kStage;
-          const uint32_t full0 = dsmem_addr(&full[s], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * P::kA + tw * 128u);
-          tma_load_2d_pair(st, &tm_a, full0, kt * 64, arow);
-          if (MODE == kHeadGrad) {  // W's rows are the contraction: two 64-column atoms
-            tma_load_2d_pair(st + P::kA, &tm_b, full0, bcol, a.b_row0 + kt * 64);
-            tma_load_2d_pair(st + P::kA + 8192, &tm_b, full0, bcol + 64, a.b_row0 + kt * 64);
+          const uint32_t full0 = PAIR ? dsmem_addr(&full[s], 0) : 0;
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+            if constexpr (PAIR) tma_load_2d_pair(dst, map, full0, x, y);
+            else tma_load_2d(dst, map, &full[s], x, y);
+          };
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          if (mine) load(st, &tm_a, kt * 64, arow);
+          if constexpr (NF4) {
+            mbar_arrive_expect_tx(&cfull[s], kGrad ? P::kC : (PAIR ? tw / 2 : tw) * 32u);
+            uint8_t* codes = st + P::kA + P::kB;
+            if constexpr (kGrad) tma_load_2d(codes, &tm_b, &cfull[s], bcol / 2, a.b_row0 + kt * 64);
+            else tma_load_2d(codes, &tm_b, &cfull[s], kt * 32, a.b_row0 + bcol);
           } else {
-            tma_load_2d_pair(st + P::kA, &tm_b, full0, kt * 64, a.b_row0 + bcol);
+            if constexpr (kGrad) {  // W's rows are the contraction: 64-column atoms
+#pragma unroll
+              for (int i = 0; i < P::kBRows / 64; ++i)
+                load(st + P::kA + i * 8192, &tm_b, bcol + i * 64, a.b_row0 + kt * 64);
+            } else {
+              load(st + P::kA, &tm_b, kt * 64, a.b_row0 + bcol);
+            }
           }
         }
       }
-      if (rank == 0)
-        for (int64_t t = it > P::kStages ? it - P::kStages : 0; t < it; ++t)
-          mbar_drain(&full[t % P::kStages], static_cast<uint32_t>(t / P::kStages) & 1, a.status);
+      // The full barriers of an NF4 ring also count the dequantisers'
+      // arrivals, which may never come after an abort: a short limit then (the
+      // copies land in microseconds).
+      const uint64_t lim = *abort_flag ? 1000000ull : kWaitTimeoutNs;
+      for (int64_t t = it > P::kStages ? it - P::kStages : 0; t < it; ++t) {
+        const uint32_t parity = static_cast<uint32_t>(t / P::kStages) & 1;
+        if (NF4) mbar_drain(&cfull[t % P::kStages], parity, a.status, lim);
+        if (rank == 0) mbar_drain(&full[t % P::kStages], parity, a.status, lim);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA (leader)
     if (rank == 0) {
-      const uint32_t idesc = idesc_bf16_f32(256, tw, 0, MODE == kHeadGrad ? 1 : 0);
-      constexpr uint32_t b_step = MODE == kHeadGrad ? (2048u >> 4) : (32u >> 4);
+      const uint32_t idesc = idesc_bf16_f32(kTokens, tw, 0, kGrad ? 1 : 0);
+      constexpr uint32_t b_step = kGrad ? (2048u >> 4) : (32u >> 4);
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (PAIR) umma_commit_pair(bar, 0x3);
+        else umma_commit(bar);
+      };
       int64_t it = 0;
       int acc = 0;  // chunks begun
       bool ok = true;
-      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+      for (int tile = worker; ok && tile < tiles; tile += workers) {
         const int split = tile / mn;
         const int kn = min(a.kst, (split + 1) * a.kper) - split * a.kper;
         for (int k0 = 0; ok && k0 < kn; k0 += a.kchunk, ++acc) {
@@ -346,24 +405,136 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
             tc_fence_after();
             const uint32_t sa = smem_u32(smem + s * P::kStage);
             const uint64_t ad = sdesc_sw128(sa, 16, 1024);
-            const uint64_t bd = MODE == kHeadGrad ? sdesc_sw128(sa + P::kA, 8192, 1024)
-                                                  : sdesc_sw128(sa + P::kA, 16, 1024);
+            const uint64_t bd = kGrad ? sdesc_sw128(sa + P::kA, 8192, 1024) : sdesc_sw128(sa + P::kA, 16, 1024);
             if (elect_one()) {
 #pragma unroll
-              for (uint32_t kk = 0; kk < 4; ++kk)
-                umma_bf16_pair(d, ad + kk * 2, bd + kk * b_step, idesc, (kt | static_cast<int>(kk)) != 0 ? 1u : 0u);
-              umma_commit_pair(&empty[s], 0x3);
-              if (kt == kc - 1) umma_commit_pair(&accf[buf], 0x3);
+              for (uint32_t kk = 0; kk < 4; ++kk) {
+                const uint32_t more = (kt | static_cast<int>(kk)) != 0 ? 1u : 0u;
+                if constexpr (PAIR) umma_bf16_pair(d, ad + kk * 2, bd + kk * b_step, idesc, more);
+                else umma_bf16(d, ad + kk * 2, bd + kk * b_step, idesc, more);
+              }
+              commit(&empty[s]);
+              if (kt == kc - 1) commit(&accf[buf]);
             }
             __syncwarp();
           }
         }
       }
-      if (elect_one()) {
-        umma_commit_pair(done, 0x1);
-        mbar_drain(done, 0, a.status);  // nothing of the pair is in flight when the tensor memory is freed
+      if (elect_one()) {  // nothing is in flight when the tensor memory is freed
+        if constexpr (PAIR) umma_commit_pair(done, 0x1);
+        else umma_commit(done);
+        mbar_drain(done, 0, a.status);
       }
       __syncwarp();
+    }
+  } else if (NF4 && warp >= 2 + kEpiWarps) {
+    // ----------------------------------------------------------- dequantisers
+    // A thread turns one 64-weight block a stage into a 128-byte row of the
+    // tile.  Logits: the block of column bcol + i at depth 64 kt (a K-major
+    // row).  Grad: columns 64 (i / 64) .. of W's row 64 kt + i % 64 (a row of an
+    // MN-major atom).  The codes come with the stage (swizzled, so that the
+    // lanes' 16-byte reads spread over the banks), the block constants from
+    // global memory, kAhead of the thread's stages ahead.
+    const int di = threadIdx.x - 64 - 32 * kEpiWarps;
+    constexpr int kSize = 256 / P::kGroups;  // threads of a group
+    const int grp = di / kSize, i = di % kSize;
+    const int blocks = kGrad ? P::kBRows : (PAIR ? tw / 2 : tw);  // of a stage in this CTA
+    const int64_t kbpr = a.head.dim / 64;
+    const Nf4Mean wmean = nf4_load_mean(a.head.mean);
+    // this thread's codes in the stage, as 16-byte chunks
+    uint32_t c_at, c_x;  // byte offset of the row; chunk pair (2 h) ^ swizzle
+    if constexpr (!kGrad) {
+      c_at = i * 32;
+      c_x = (i >> 2) & 1;
+    } else if constexpr (PAIR) {
+      c_at = (i & 63) * 64;
+      c_x = ((i >> 6) * 2) ^ ((i >> 1) & 3);
+    } else {
+      c_at = (i & 63) * 128;
+      c_x = ((i >> 6) * 2) ^ (i & 7);
+    }
+    constexpr int kAhead = 4;
+    struct At {  // a stage of this worker's tiles
+      int tile, kt, k1, bcol;
+    };
+    auto enter = [&](At& p) {  // first stage of p.tile, or of a later one that has any
+      for (; p.tile < tiles; p.tile += workers) {
+        const int split = p.tile / mn;
+        int m, n;
+        head_tile(p.tile - split * mn, a.mtiles, a.ntiles, m, n);
+        p.bcol = n * tw + static_cast<int>(rank) * (tw / 2);
+        p.kt = split * a.kper;
+        p.k1 = min(a.kst, p.kt + a.kper);
+        if (p.kt < p.k1) return;
+      }
+    };
+    auto advance = [&](At& p, int by) {
+      for (int k = 0; k < by && p.tile < tiles; ++k) {
+        if (++p.kt >= p.k1) {
+          p.tile += workers;
+          enter(p);
+        }
+      }
+    };
+    uint32_t pk[kAhead];
+    float ps[kAhead];
+    auto fetch = [&](const At& p, uint32_t& k8, float& s2) {
+      k8 = 0x100;  // outside: zeros, whatever the codes
+      s2 = 0.0f;
+      if (p.tile >= tiles || i >= blocks) return;
+      const int row = kGrad ? p.kt * 64 + (i & 63) : p.bcol + i;  // of the piece
+      const int64_t kb = kGrad ? p.bcol / 64 + (i >> 6) : p.kt;
+      if (row >= a.wrows || kb >= kbpr) return;
+      const int64_t b = (a.v0 + row) * kbpr + kb;
+      k8 = __ldg(a.head.c8 + b);
+      s2 = __ldg(a.head.s2 + (b >> 8));
+    };
+    At now{worker, 0, 0, 0};
+    enter(now);
+    advance(now, grp);
+    At fut = now;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      fetch(fut, pk[j], ps[j]);
+      advance(fut, P::kGroups);
+    }
+    // (Unrolled over the slots, so that each is refilled in place: moving a
+    // register that a load is still filling waits for the load.)
+    bool ok = true;
+    for (int64_t it = grp; ok && now.tile < tiles;) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (now.tile >= tiles) break;
+        const uint32_t s = static_cast<uint32_t>(it % P::kStages);
+        const uint32_t u = static_cast<uint32_t>(it / P::kStages);
+        const float chat = pk[j] == 0x100u ? 0.0f : nf4_block_scale(pk[j], ps[j], wmean);
+        const Nf4Lut lut = nf4_make_lut(a.tab, chat);
+        fetch(fut, pk[j], ps[j]);
+        if (!mbar_wait_all(&cfull[s], u & 1, wc)) {
+          ok = false;
+          break;
+        }
+        if (i < blocks) {
+          uint8_t* st = smem + s * P::kStage + P::kA;
+          const uint8_t* codes = st + P::kB + c_at;
+          const uint4 c0 = *reinterpret_cast<const uint4*>(codes + (c_x << 4));
+          const uint4 c1 = *reinterpret_cast<const uint4*>(codes + ((c_x ^ 1) << 4));
+          const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+          uint8_t* dst = st + i * 128;  // (Grad: atom i / 64, row i % 64)
+#pragma unroll
+          for (uint32_t c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(dst + ((c ^ (i & 7)) << 4)) = nf4_lookup8(cw[c], lut);
+        }
+        fence_proxy_async_smem();  // this lane's row -> async proxy
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR) mbar_arrive_remote(dsmem_addr(&full[s], 0));
+          else mbar_arrive(&full[s]);
+        }
+        it += P::kGroups;
+        advance(fut, P::kGroups);
+        advance(now, P::kGroups);
+      }
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -373,12 +544,20 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     const int et = threadIdx.x - 64;
     const uint32_t tq = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + half * hw;
     int acc = 0;
-    for (int tile = pair; tile < tiles; tile += pairs) {
+    auto release = [&](int buf) {  // this warp's reads of the accumulator are done
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_remote(dsmem_addr(&acce[buf], 0));
+        else mbar_arrive(&acce[buf]);
+      }
+    };
+    for (int tile = worker; tile < tiles; tile += workers) {
       int m, n;
       const int split = tile / mn;
       head_tile(tile - split * mn, a.mtiles, a.ntiles, m, n);
       const int kn = min(a.kst, (split + 1) * a.kper) - split * a.kper;
-      const int t = m * kHeadTile + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const int t = m * kTokens + static_cast<int>(rank) * 128 + q * 32 + lane;
       const bool rok = t < a.T;
       const int n0 = n * tw + half * hw;
       const int nv = min(hw, a.ncols - n0);  // this thread's columns (may be none)
@@ -399,12 +578,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
           if (!mbar_wait_warp(&accf[buf], (acc >> 1) & 1, wc)) break;
           tc_fence_after();
         }
-        float4* sum = reinterpret_cast<float4*>(a.acc) + (static_cast<int64_t>(tile) * 2 + rank) * kSumBlock + et;
+        float4* sum = reinterpret_cast<float4*>(a.acc) + (static_cast<int64_t>(tile) * kCtas + rank) * kSumBlock + et;
         const float al = (!a.first && a.alpha && rok) ? __ldcg(a.alpha + t) : 1.0f;
         const bool out = a.last && a.splits == 1;
         float ca = 0.0f, cl = 0.0f;
         if (out && counted) grad_row_factors(a, t, ca, cl);
-        for (int cb = 0; cb < kHalf / 32; ++cb) {
+        for (int cb = 0; cb < kSumCols / 32; ++cb) {
           float l[32] = {};
           if (kn > 0) {
             uint32_t v[32];
@@ -433,15 +612,14 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
           }
         }
         if (kn > 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(dsmem_addr(&acce[buf], 0));
+          release(buf);
           ++acc;
         }
         continue;
       }
 
-      float l[kHalf];
+      constexpr int kCols = P::kCols;
+      float l[kCols];
       bool ok = true;
       for (int k0 = 0; k0 < kn; k0 += a.kchunk, ++acc) {
         const int buf = acc & 1;
@@ -451,15 +629,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         }
         tc_fence_after();
         add_chunk(tq + buf * 256, k0 == 0, hw, l);
-        tc_fence_before();  // this warp's reads of the accumulator are done
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(dsmem_addr(&acce[buf], 0));
+        release(buf);
       }
       if (!ok) break;
 
-      if (nv < kHalf) {
+      if (nv < kCols) {
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j)
+        for (int j = 0; j < kCols; ++j)
           if (j >= nv) l[j] = -INFINITY;
       }
       if (MODE == kHeadLoss) {
@@ -468,7 +644,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         if (lj >= 0) a.label_logit[t] = pick(l, lj);
         float p[4] = {};
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) p[j & 3] += exp2_fast(fmaf(l[j], kLog2e, -base));
+        for (int j = 0; j < kCols; ++j) p[j & 3] += exp2_fast(fmaf(l[j], kLog2e, -base));
         if (rok) a.part[static_cast<int64_t>(2 * n + half) * a.T + t] = make_float2(mx, (p[0] + p[1]) + (p[2] + p[3]));
       } else if (MODE == kHeadExp) {
         const float mx = max_all(l);
@@ -477,7 +653,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         if (lj >= 0) a.label_logit[t] = pick(l, lj);
         float p[4] = {};
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
+        for (int j = 0; j < kCols; ++j) {
           l[j] = exp2_fast(fmaf(l[j], kLog2e, -base));
           p[j & 3] += l[j];
           if (j == lj) l[j] = 0.0f;
@@ -491,7 +667,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         const float base = lse * kLog2e;
         const float pl = lj >= 0 ? expm1f(pick(l, lj) - lse) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
+        for (int j = 0; j < kCols; ++j) {
           l[j] = counted ? exp2_fast(fmaf(l[j], kLog2e, -base)) : 0.0f;
           if (j == lj) l[j] = pl;
         }
@@ -505,33 +681,36 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
 
   tc_fence_before();
   __syncwarp();
-  cluster_sync_all();
+  if constexpr (PAIR) cluster_sync_all();
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_d, 512);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_d, 512);
+    else tmem_dealloc(tmem_d, 512);
   }
 }
 
 // ------------------------------------------------------------------- finish
 //
 // A split contraction's sums joined in split order, and dH's rows from them.
-// blockIdx.x: (tile, CTA of the pair); blockIdx.y: 32 of a thread's 128 columns.
+// blockIdx.x: (tile, CTA of it); blockIdx.y: 32 of a thread's 128 columns.
 __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_constant__ HeadArgs a) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int mn = a.mtiles * a.ntiles;
-  const int tile = blockIdx.x >> 1, rank = blockIdx.x & 1;
+  const int ctas = a.pair ? 2 : 1;
+  const int tile = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   int m, n;
   head_tile(tile, a.mtiles, a.ntiles, m, n);
   const int et = threadIdx.x, w = et >> 5, lane = et & 31;
-  const int t = m * kHeadTile + rank * 128 + ((w + 2) & 3) * 32 + lane;  // as in the product's epilogue
-  const int d = n * kHeadTile + (w >> 2) * kHalf + blockIdx.y * 32;
+  const int t = (m * ctas + rank) * 128 + ((w + 2) & 3) * 32 + lane;  // as in the product's epilogue
+  const int d = n * kHeadTile + (w >> 2) * kSumCols + blockIdx.y * 32;
   if (t >= a.T || d >= a.ncols) return;
-  const float4* sum = reinterpret_cast<const float4*>(a.acc) + (static_cast<int64_t>(tile) * 2 + rank) * kSumBlock +
+  const float4* sum = reinterpret_cast<const float4*>(a.acc) + static_cast<int64_t>(blockIdx.x) * kSumBlock +
                       static_cast<int>(blockIdx.y) * 8 * kSumStride + et;
   float l[32] = {};
   for (int s = 0; s < a.splits; ++s) {
-    const float4* at = sum + static_cast<int64_t>(s) * mn * 2 * kSumBlock;
+    const float4* at = sum + static_cast<int64_t>(s) * mn * ctas * kSumBlock;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float4 o = __ldcg(at + j * kSumStride);
@@ -674,31 +853,42 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
   }
 }
 
-template <int MODE>
+template <int MODE, bool PAIR, bool NF4>
 static cudaError_t launch_head_gemm_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
                                          cudaStream_t stream) {
+  using P = HeadPlan<MODE, PAIR, NF4>;
   static uint64_t done = 0;
-  if (cudaError_t e = allow_smem(head_gemm_kernel<MODE>, HeadPlan::kSmem, done)) return e;
+  if (cudaError_t e = allow_smem(head_gemm_kernel<MODE, PAIR, NF4>, P::kSmem, done)) return e;
   const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles * a.splits;
-  const int pairs = static_cast<int>(std::min<int64_t>(tiles, 74));  // one pair per TPC
-  return launch_kernel(head_gemm_kernel<MODE>, dim3(2 * pairs), dim3(kHeadThreads), HeadPlan::kSmem, stream,
-                       dim3(2, 1, 1), tm_a, tm_b, a);
+  const int workers = static_cast<int>(std::min<int64_t>(tiles, head_workers(PAIR)));
+  return launch_kernel(head_gemm_kernel<MODE, PAIR, NF4>, dim3((PAIR ? 2 : 1) * workers), dim3(P::kThreads), P::kSmem,
+                       stream, dim3(PAIR ? 2 : 1, 1, 1), tm_a, tm_b, a);
+}
+
+template <int MODE>
+static cudaError_t launch_head_gemm_mode(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
+                                         cudaStream_t stream) {
+  if (a.pair)
+    return a.nf4 ? launch_head_gemm_impl<MODE, true, true>(tm_a, tm_b, a, stream)
+                 : launch_head_gemm_impl<MODE, true, false>(tm_a, tm_b, a, stream);
+  return a.nf4 ? launch_head_gemm_impl<MODE, false, true>(tm_a, tm_b, a, stream)
+               : launch_head_gemm_impl<MODE, false, false>(tm_a, tm_b, a, stream);
 }
 
 cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
                              cudaStream_t stream) {
   switch (mode) {
-    case kHeadLoss: return launch_head_gemm_impl<kHeadLoss>(tm_a, tm_b, a, stream);
-    case kHeadProb: return launch_head_gemm_impl<kHeadProb>(tm_a, tm_b, a, stream);
-    case kHeadExp: return launch_head_gemm_impl<kHeadExp>(tm_a, tm_b, a, stream);
-    case kHeadGrad: return launch_head_gemm_impl<kHeadGrad>(tm_a, tm_b, a, stream);
+    case kHeadLoss: return launch_head_gemm_mode<kHeadLoss>(tm_a, tm_b, a, stream);
+    case kHeadProb: return launch_head_gemm_mode<kHeadProb>(tm_a, tm_b, a, stream);
+    case kHeadExp: return launch_head_gemm_mode<kHeadExp>(tm_a, tm_b, a, stream);
+    case kHeadGrad: return launch_head_gemm_mode<kHeadGrad>(tm_a, tm_b, a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 cudaError_t launch_head_finish(const HeadArgs& a, cudaStream_t stream) {
-  return launch_kernel(head_finish_kernel, dim3(2 * a.mtiles * a.ntiles, kHalf / 32), dim3(kSumStride), 0, stream,
-                       dim3(1, 1, 1), a);
+  return launch_kernel(head_finish_kernel, dim3((a.pair ? 2 : 1) * a.mtiles * a.ntiles, kSumCols / 32),
+                       dim3(kSumStride), 0, stream, dim3(1, 1, 1), a);
 }
 
 int head_combine_blocks(int64_t T) { return static_cast<int>((T + 31) / 32); }

@@ -46,17 +46,23 @@ enum HeadMode {
   kHeadGrad = 3   // those times the piece's weight -> dH (or its fp32 sum so far)
 };
 
+// CTA pairs, or CTAs, of a persistent launch: one per TPC, one per SM.
+constexpr int head_workers(bool pair) { return pair ? 74 : 148; }
+
 struct HeadArgs {
+  int pair, nf4;          // which kernel: tiles of 256 tokens on CTA pairs, W from its codes
   int T;                  // tokens
+  int arows;              // token rows of a copy: 128, or for fewer tokens those, to a multiple of 8
   int ncols;              // columns of this product: the piece's vocabulary rows, or dim (Grad)
   int kst;                // 64-deep contraction stages
   int kchunk;             // stages summed in one accumulator
   int splits, kper;       // Grad: slices of the contraction and their stages (else 1, kst)
   int b_row0;             // the piece's first row in W's tensor map
   int64_t v0;             // the piece's first vocabulary index
+  int wrows;              // the piece's vocabulary rows
   int64_t vocab;
   int mtiles, ntiles;
-  int tw;                 // columns of a tile: a multiple of 32 up to 256 (Grad: 256)
+  int tw;                 // columns of a tile: a multiple of 32 up to 256, NF4 128 (Grad: 256)
   const int64_t* labels;
   int64_t ignore;
   float* label_logit;     // Loss, Exp: [T]
@@ -79,13 +85,15 @@ struct HeadArgs {
   const float* weight;    // [T] or null (step)
   float scale;
   const int32_t* count;   // tokens that count (step, weight null)
-  qlora_head head;        // step: the label's row of W
+  qlora_head head;        // step: the label's row of W; NF4: its codes
   Nf4Tables tab;
   int32_t* status;
 };
 
-//   tm_a: H [T, dim] (Grad: the piece's [T, ntiles tw]) box {64, 128} SW128;
-//   tm_b: W rows, box {64, tw / 2} SW128 (Grad: {64, 64}).
+//   tm_a: H [T, dim] (Grad: the piece's [T, ntiles tw]) box {64, arows} SW128;
+//   tm_b: W rows, box {64, tw / 2 (pair) or tw} SW128 (Grad: {64, 64}); with
+//   nf4 W's codes [vocab, dim / 2], box {32, tw / 2 (pair) or tw} SW32 (Grad:
+//   {64, 64} SW64 (pair) or {128, 64} SW128).
 cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
                              cudaStream_t stream);
 

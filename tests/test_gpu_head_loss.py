@@ -82,7 +82,7 @@ class Ref:
 
 # tokens, vocabulary, width: one of each, odd ones, tile borders, widths that end inside a stage
 SHAPES = [(1, 1, 8), (1, 1000, 64), (3, 257, 72), (129, 256, 256), (200, 1003, 520), (256, 512, 64), (257, 255, 192),
-          (700, 3001, 1024), (60, 33000, 256)]
+          (700, 3001, 1024), (60, 33000, 256), (128, 4000, 328), (16, 40001, 640)]
 
 
 @pytest.mark.parametrize("T,V,D", SHAPES)
@@ -181,7 +181,8 @@ def test_well_predicted_tokens_keep_their_gradient():
 
 
 @pytest.mark.parametrize("T,V,D,centred", [(5, 1001, 64, False), (300, 2300, 512, True), (64, 40000, 2048, False),
-                                           (17000, 4500, 128, True)])
+                                           (17000, 4500, 128, True), (128, 300, 64, False), (129, 5000, 192, True),
+                                           (512, 1000, 448, False), (513, 700, 128, False), (1, 30000, 1024, False)])
 def test_nf4_head(T, V, D, centred):
     """An NF4 head is the bf16 head of its dequantised weight.  The logits are the
     same bits; the pieces, and so the order in which a row's exponentials are
@@ -203,6 +204,20 @@ def test_nf4_head(T, V, D, centred):
     got = q.qlora_head_loss_step(H, W, Y, weight=g)
     r.check_grad(got[3][:n], g.cpu().numpy()[:n])
     assert np.all(np.abs(got[0].cpu().numpy()[:n] - r.loss) <= r.loss_tol)
+
+
+def test_nf4_head_of_equal_constants():
+    """Mean-centred constants that are all equal have scale 0: their value is the mean."""
+    T, V, D = 20, 500, 128
+    h, _, y = _case(T, V, D, seed=7)
+    g = torch.Generator().manual_seed(3)
+    w = torch.where(torch.rand(V, D, generator=g) < 0.5, 0.25, -0.25).to(torch.bfloat16)
+    W = q.quantize_weight_centered(w.cuda())
+    assert not W.s2.any() and float(W.mean) == 0.25
+    r = Ref(h, w, y)
+    got = q.qlora_head_loss_step(h.cuda(), W, y.cuda(), weight=torch.ones(T, device="cuda"))
+    r.check_loss(*got[:3])
+    r.check_grad(got[3], np.ones(T))
 
 
 def test_ignored_rows_may_hold_anything():
