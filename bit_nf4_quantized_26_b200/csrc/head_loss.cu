@@ -40,9 +40,10 @@ constexpr float kRefRange = 40.0f;  // tile maxima within +-kRefRange share the 
 
 // PAIR: tiles of 256 tokens on CTA pairs; otherwise, for at most 128 tokens,
 // of 128 on single CTAs (twice the workers, none of the tile without tokens).
-// NF4: W's tile is dequantised into the ring from its codes.
+// NF4 (single CTAs only): W's tile is dequantised into the ring from its codes.
 template <int MODE, bool PAIR, bool NF4>
 struct HeadPlan {
+  static_assert(!(PAIR && NF4), "no such kernel");
   static constexpr bool kGrad = MODE == kHeadGrad;
   // columns of a tile at most: an NF4 kernel's extra warps leave the epilogue
   // registers for 64 sums a thread
@@ -60,7 +61,7 @@ struct HeadPlan {
   // a thread; the ring is a multiple of the groups, so a slot's earlier stages
   // are the same group's and its parity waits cannot run a phase ahead.
   static constexpr int kGroups = NF4 ? 256 / kBRows : 1;
-  static constexpr int kArrive = (PAIR ? 2 : 1) * 8 / kGroups;   // their arrivals on a stage
+  static constexpr int kArrive = 8 / kGroups;                    // their arrivals on a stage
   static constexpr uint32_t kStages = (232448 - 2048) / kStage / (NF4 ? kGroups : 2) * (NF4 ? kGroups : 2);
   static constexpr uint32_t kBarOff = kStages * kStage;
   static constexpr uint32_t kSmem = 1024 + kBarOff + 512;
@@ -68,7 +69,6 @@ struct HeadPlan {
 };
 
 constexpr int kEpiWarps = 8;
-constexpr int kGroupM = 8;  // token tiles walked together (raster)
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -76,14 +76,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Tile order: groups of kGroupM token tiles, tokens first within a group, so
-// the pairs at work share a few panels of each operand in L2.
+// Tile order: groups of token tiles, tokens first within a group, so the pairs
+// at work share a few panels of each operand in L2.  Groups of 16 for logits
+// (8192 x 32000 x 4096, forward: 1584-1621 us, of 8 1635-1650, of 32 1800), of
+// 8 for dH, whose token panels are a piece wide.
+template <bool GRAD>
 __device__ __forceinline__ void head_tile(int tile, int mtiles, int ntiles, int& m, int& n) {
-  const int per = kGroupM * ntiles;
+  constexpr int kGroup = GRAD ? 8 : 16;
+  const int per = kGroup * ntiles;
   const int grp = tile / per, rem = tile - grp * per;
-  const int gsz = min(kGroupM, mtiles - grp * kGroupM);
+  const int gsz = min(kGroup, mtiles - grp * kGroup);
   n = rem / gsz;
-  m = grp * kGroupM + rem - n * gsz;
+  m = grp * kGroup + rem - n * gsz;
 }
 
 __device__ __forceinline__ bool counts(int64_t label, int64_t ignore, int64_t vocab) {
@@ -226,6 +230,20 @@ __device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t l
   store_bf16x32(a.dh + static_cast<int64_t>(t) * a.ldd + d, l, n);
 }
 
+// Place in a ring of N slots: the slot, and the parity of its round.  (Counted
+// on: a division per stage would take the MMA warp a fifth of a stage's time.)
+template <uint32_t N>
+struct Ring {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void advance(uint32_t by = 1) {
+    slot += by;
+    if (slot >= N) {
+      slot -= N;
+      parity ^= 1;
+    }
+  }
+};
+
 }  // namespace
 
 // A tile is 256 tokens (a CTA pair's; 128 of a single CTA) x tw columns: 256,
@@ -239,10 +257,12 @@ __device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t l
 // The tensor core truncates when it adds to its fp32 accumulator: the sum
 // drifts towards zero by about 2^-24 of itself per K = 16 step (measured:
 // -8e-7 relative at dim 1024, -8e-6 at 8192, on random data).  A tile's
-// contraction is therefore cut into chunks (512 deep for logits: 32 steps)
-// that alternate between two accumulators, and the epilogue threads add each
-// finished one to their registers, rounding to nearest, while the next runs.
-// dH, rounded to bf16, takes a whole slice of its contraction as one chunk.
+// contraction of a loss is therefore cut into chunks (768 deep: 48 steps, a
+// drift of 6e-7) that alternate between two accumulators, and the epilogue
+// threads add each finished one to their registers, rounding to nearest, while
+// the next runs.  (512 deep costs the products 2-3%, 1024 nothing.)  Results
+// rounded to bf16 take longer ones: the backward's probabilities 4096, dH a
+// whole slice of its contraction.
 //
 // Barriers (leader: the pair's first CTA, or the single one): full[s] (leader:
 // the stage's copies landed, and its dequantised tiles are written), empty[s]
@@ -319,24 +339,25 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int64_t it = 0;  // stages issued
+      Ring<P::kStages> at;
+      uint32_t issued = 0;  // stages, up to a full ring
       bool ok = true;
       for (int tile = worker; ok && tile < tiles; tile += workers) {
         int m, n;
         const int split = tile / mn;
-        head_tile(tile - split * mn, a.mtiles, a.ntiles, m, n);
+        head_tile<kGrad>(tile - split * mn, a.mtiles, a.ntiles, m, n);
         const int arow = m * kTokens + static_cast<int>(rank) * 128;
         const int bcol = n * tw + static_cast<int>(rank) * (tw / 2);
         const int k1 = min(a.kst, (split + 1) * a.kper);
         const bool mine = arow < a.T;  // else the CTA's rows hold no token: nothing to copy
         const uint32_t bytes = (PAIR && arow + 128 < a.T ? 2 : 1) * a.arows * 128u + (NF4 ? 0 : tw * 128u);
-        for (int kt = split * a.kper; kt < k1; ++kt, ++it) {
-          const uint32_t s = static_cast<uint32_t>(it % P::kStages);
-          const uint32_t u = static_cast<uint32_t>(it / P::kStages);
-          if (it >= P::kStages && !mbar_wait(&empty[s], (u - 1) & 1, wc)) {
+        for (int kt = split * a.kper; kt < k1; ++kt, at.advance()) {
+          const uint32_t s = at.slot;
+          if (issued == P::kStages && !mbar_wait(&empty[s], at.parity ^ 1, wc)) {
             ok = false;
             break;
           }
+          issued = min(issued + 1, P::kStages);
           uint8_t* st = smem + s * P::kStage;
           const uint32_t full0 = PAIR ? dsmem_addr(&full[s], 0) : 0;
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
@@ -346,7 +367,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           if (mine) load(st, &tm_a, kt * 64, arow);
           if constexpr (NF4) {
-            mbar_arrive_expect_tx(&cfull[s], kGrad ? P::kC : (PAIR ? tw / 2 : tw) * 32u);
+            mbar_arrive_expect_tx(&cfull[s], kGrad ? P::kC : tw * 32u);
             uint8_t* codes = st + P::kA + P::kB;
             if constexpr (kGrad) tma_load_2d(codes, &tm_b, &cfull[s], bcol / 2, a.b_row0 + kt * 64);
             else tma_load_2d(codes, &tm_b, &cfull[s], kt * 32, a.b_row0 + bcol);
@@ -365,10 +386,10 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
       // arrivals, which may never come after an abort: a short limit then (the
       // copies land in microseconds).
       const uint64_t lim = *abort_flag ? 1000000ull : kWaitTimeoutNs;
-      for (int64_t t = it > P::kStages ? it - P::kStages : 0; t < it; ++t) {
-        const uint32_t parity = static_cast<uint32_t>(t / P::kStages) & 1;
-        if (NF4) mbar_drain(&cfull[t % P::kStages], parity, a.status, lim);
-        if (rank == 0) mbar_drain(&full[t % P::kStages], parity, a.status, lim);
+      for (uint32_t s = 0; s < issued; ++s) {  // each slot's last copy
+        const uint32_t parity = s < at.slot ? at.parity : at.parity ^ 1;
+        if (NF4) mbar_drain(&cfull[s], parity, a.status, lim);
+        if (rank == 0) mbar_drain(&full[s], parity, a.status, lim);
       }
     }
     __syncwarp();
@@ -381,7 +402,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         if constexpr (PAIR) umma_commit_pair(bar, 0x3);
         else umma_commit(bar);
       };
-      int64_t it = 0;
+      Ring<P::kStages> at;
       int acc = 0;  // chunks begun
       bool ok = true;
       for (int tile = worker; ok && tile < tiles; tile += workers) {
@@ -396,9 +417,9 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
           tc_fence_after();
           const uint32_t d = tmem_d + buf * 256;
           const int kc = min(a.kchunk, kn - k0);
-          for (int kt = 0; kt < kc; ++kt, ++it) {
-            const uint32_t s = static_cast<uint32_t>(it % P::kStages);
-            if (!mbar_wait_all(&full[s], static_cast<uint32_t>(it / P::kStages) & 1, wc)) {
+          for (int kt = 0; kt < kc; ++kt, at.advance()) {
+            const uint32_t s = at.slot;
+            if (!mbar_wait_all(&full[s], at.parity, wc)) {
               ok = false;
               break;
             }
@@ -438,20 +459,17 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     const int di = threadIdx.x - 64 - 32 * kEpiWarps;
     constexpr int kSize = 256 / P::kGroups;  // threads of a group
     const int grp = di / kSize, i = di % kSize;
-    const int blocks = kGrad ? P::kBRows : (PAIR ? tw / 2 : tw);  // of a stage in this CTA
+    const int blocks = kGrad ? P::kBRows : tw;  // of a stage
     const int64_t kbpr = a.head.dim / 64;
     const Nf4Mean wmean = nf4_load_mean(a.head.mean);
     // this thread's codes in the stage, as 16-byte chunks
     uint32_t c_at, c_x;  // byte offset of the row; chunk pair (2 h) ^ swizzle
-    if constexpr (!kGrad) {
-      c_at = i * 32;
-      c_x = (i >> 2) & 1;
-    } else if constexpr (PAIR) {
-      c_at = (i & 63) * 64;
-      c_x = ((i >> 6) * 2) ^ ((i >> 1) & 3);
-    } else {
+    if constexpr (kGrad) {
       c_at = (i & 63) * 128;
       c_x = ((i >> 6) * 2) ^ (i & 7);
+    } else {
+      c_at = i * 32;
+      c_x = (i >> 2) & 1;
     }
     constexpr int kAhead = 4;
     struct At {  // a stage of this worker's tiles
@@ -461,8 +479,8 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
       for (; p.tile < tiles; p.tile += workers) {
         const int split = p.tile / mn;
         int m, n;
-        head_tile(p.tile - split * mn, a.mtiles, a.ntiles, m, n);
-        p.bcol = n * tw + static_cast<int>(rank) * (tw / 2);
+        head_tile<kGrad>(p.tile - split * mn, a.mtiles, a.ntiles, m, n);
+        p.bcol = n * tw;
         p.kt = split * a.kper;
         p.k1 = min(a.kst, p.kt + a.kper);
         if (p.kt < p.k1) return;
@@ -501,16 +519,17 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     // (Unrolled over the slots, so that each is refilled in place: moving a
     // register that a load is still filling waits for the load.)
     bool ok = true;
-    for (int64_t it = grp; ok && now.tile < tiles;) {
+    Ring<P::kStages> at;
+    at.advance(grp);
+    while (ok && now.tile < tiles) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         if (now.tile >= tiles) break;
-        const uint32_t s = static_cast<uint32_t>(it % P::kStages);
-        const uint32_t u = static_cast<uint32_t>(it / P::kStages);
+        const uint32_t s = at.slot;
         const float chat = pk[j] == 0x100u ? 0.0f : nf4_block_scale(pk[j], ps[j], wmean);
         const Nf4Lut lut = nf4_make_lut(a.tab, chat);
         fetch(fut, pk[j], ps[j]);
-        if (!mbar_wait_all(&cfull[s], u & 1, wc)) {
+        if (!mbar_wait_all(&cfull[s], at.parity, wc)) {
           ok = false;
           break;
         }
@@ -527,11 +546,8 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         }
         fence_proxy_async_smem();  // this lane's row -> async proxy
         __syncwarp();
-        if (lane == 0) {
-          if constexpr (PAIR) mbar_arrive_remote(dsmem_addr(&full[s], 0));
-          else mbar_arrive(&full[s]);
-        }
-        it += P::kGroups;
+        if (lane == 0) mbar_arrive(&full[s]);
+        at.advance(P::kGroups);
         advance(fut, P::kGroups);
         advance(now, P::kGroups);
       }
@@ -555,7 +571,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     for (int tile = worker; tile < tiles; tile += workers) {
       int m, n;
       const int split = tile / mn;
-      head_tile(tile - split * mn, a.mtiles, a.ntiles, m, n);
+      head_tile<kGrad>(tile - split * mn, a.mtiles, a.ntiles, m, n);
       const int kn = min(a.kst, (split + 1) * a.kper) - split * a.kper;
       const int t = m * kTokens + static_cast<int>(rank) * 128 + q * 32 + lane;
       const bool rok = t < a.T;
@@ -701,7 +717,7 @@ __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_co
   const int ctas = a.pair ? 2 : 1;
   const int tile = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   int m, n;
-  head_tile(tile, a.mtiles, a.ntiles, m, n);
+  head_tile<true>(tile, a.mtiles, a.ntiles, m, n);
   const int et = threadIdx.x, w = et >> 5, lane = et & 31;
   const int t = (m * ctas + rank) * 128 + ((w + 2) & 3) * 32 + lane;  // as in the product's epilogue
   const int d = n * kHeadTile + (w >> 2) * kSumCols + blockIdx.y * 32;
@@ -729,12 +745,14 @@ __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_co
 
 // ------------------------------------------------------------------ combine
 //
-// Joins the (reference, sum) pairs of a row's tiles: R = max ref, S = sum of
-// s exp(ref - R).  A block takes 32 tokens (a lane each) and splits the tiles
-// over 16 warps.  Step: R and S run over the pieces, exponentials of tiles
-// whose reference is not R are rescaled in place, and alpha = exp(R_old - R).
-// With the last piece: lse, loss, and the mean in fp64 (per-block sums, added
-// in block order by the block that finishes last).
+// Joins the (reference, sum) pairs of a row's parts (half tiles): R = max ref,
+// S = sum of s exp(ref - R).  Step: R and S run over the pieces, exponentials of
+// parts whose reference is not R are rescaled in place (rows with logits beyond
+// +-40 only), and alpha = exp(R_old - R).  With the last piece: lse, loss, and
+// the mean in fp64 (per-block sums, added in block order by the block that
+// finishes last).  A block takes TB tokens; its threads split their parts.  TB
+// is 32 (whole sectors of a part's row) or, for few tokens, where the chain of
+// loads is what takes the time, fewer, so that a thread has a few parts only.
 
 namespace {
 
@@ -742,56 +760,75 @@ constexpr int kCombineWarps = 16;
 
 __device__ __forceinline__ void join(float& R, float& S, float ref, float s) {
   if (s == 0.0f) return;  // (a NaN is not equal and joins)
-  if (ref > R) {
-    S = S * expf(R - ref) + s;  // R = -inf: the factor is 0
-    R = ref;
-  } else {
-    S += s * (ref == R ? 1.0f : expf(ref - R));
-  }
+  const float top = fmaxf(R, ref);
+  // R = -inf (nothing yet): the factor is 0
+  S = S * (R == top ? 1.0f : expf(R - top)) + s * (ref == top ? 1.0f : expf(ref - top));
+  R = top;
 }
 
 }  // namespace
 
+template <int TB>
 __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const HeadCombineArgs a) {
-  __shared__ float2 sm[kCombineWarps][32];
-  __shared__ float ref_s[32];
+  __shared__ float2 sm[kCombineWarps][TB];
+  __shared__ float ref_s[TB];
   __shared__ bool last_block;
   __shared__ double sums[kCombineWarps];
+  constexpr int kSlices = kCombineWarps * 32 / TB;
   grid_dependency_wait();
   grid_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 32 + lane;
+  const int tok = threadIdx.x % TB, slice = threadIdx.x / TB;
+  const int t0 = blockIdx.x * TB, t = t0 + tok;
   const bool rok = t < a.T;
 
   float R = -INFINITY, S = 0.0f;
+  float lo = INFINITY;  // smallest reference of a part with a sum
   if (rok) {
-#pragma unroll 4
-    for (int j = warp; j < a.nparts; j += kCombineWarps) {
-      const float2 p = a.part[static_cast<int64_t>(j) * a.T + t];
-      join(R, S, p.x, p.y);
+    for (int j0 = slice; j0 < a.nparts; j0 += 8 * kSlices) {
+      float2 p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = j0 + i * kSlices;
+        p[i] = j < a.nparts ? __ldcg(a.part + static_cast<int64_t>(j) * a.T + t) : make_float2(0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        join(R, S, p[i].x, p[i].y);
+        if (p[i].y != 0.0f) lo = fminf(lo, p[i].x);
+      }
     }
   }
-  sm[warp][lane] = make_float2(R, S);
+#pragma unroll
+  for (int o = 16; o >= TB; o >>= 1) {  // lanes of the same token
+    const float r = __shfl_xor_sync(0xFFFFFFFFu, R, o), s = __shfl_xor_sync(0xFFFFFFFFu, S, o);
+    // the lower lane's value first, so that both get the same bits
+    float r2 = (lane & o) ? r : R, s2 = (lane & o) ? s : S;
+    join(r2, s2, (lane & o) ? R : r, (lane & o) ? S : s);
+    R = r2;
+    S = s2;
+  }
+  if (lane < TB) sm[warp][lane] = make_float2(R, S);
   __syncthreads();
   if (warp == 0) {
-    for (int w = 1; w < kCombineWarps; ++w) join(R, S, sm[w][lane].x, sm[w][lane].y);
-    if (a.run && rok) {
-      if (!a.first) {
-        const float2 old = a.run[t];
-        join(R, S, old.x, old.y);
-        a.alpha[t] = (old.y == 0.0f || old.x == R) ? 1.0f : expf(old.x - R);
+    bool counted = false;
+    double sum = 0.0;
+    if (lane < TB) {
+      for (int w = 1; w < kCombineWarps; ++w) join(R, S, sm[w][lane].x, sm[w][lane].y);
+      if (a.run && rok) {
+        if (!a.first) {
+          const float2 old = __ldcg(a.run + t);
+          join(R, S, old.x, old.y);
+          a.alpha[t] = (old.y == 0.0f || old.x == R) ? 1.0f : expf(old.x - R);
+        }
+        a.run[t] = make_float2(R, S);
       }
-      a.run[t] = make_float2(R, S);
-    }
-    ref_s[lane] = R;
-    if (a.last) {
-      double sum = 0.0;
-      bool counted = false;
-      if (rok) {
+      ref_s[lane] = R;
+      if (a.last && rok) {
         const int64_t label = a.labels[t];
-        counted = label != a.ignore && label >= 0 && label < a.vocab;
+        counted = counts(label, a.ignore, a.vocab);
         const float lse = R + logf(S);
-        const float z = counted ? a.label_logit[t] : lse;
+        const float z = counted ? __ldcg(a.label_logit + t) : lse;
         const float loss = counted ? lse - z : 0.0f;
         a.lse[t] = lse;
         a.loss[t] = loss;
@@ -805,6 +842,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
           if (!counted && label != a.ignore) atomicOr(a.status, QLORA_DEV_LABEL);
         }
       }
+    }
+    if (a.last) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
       const uint32_t votes = __ballot_sync(0xFFFFFFFFu, counted);
@@ -818,21 +857,26 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
   }
   __syncthreads();
   if (a.e) {
-    const float ref = ref_s[lane];
-    for (int j = warp; j < a.nparts; j += kCombineWarps) {
-      const float2 p = rok ? a.part[static_cast<int64_t>(j) * a.T + t] : make_float2(0.0f, 0.0f);
-      uint32_t todo = __ballot_sync(0xFFFFFFFFu, rok && p.y != 0.0f && p.x != ref);
-      const float f = expf(p.x - ref);
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const float fr = __shfl_sync(0xFFFFFFFFu, f, src);
-        if (4 * lane >= a.part_cols) continue;
-        uint2* at = reinterpret_cast<uint2*>(a.e + static_cast<int64_t>(blockIdx.x * 32 + src) * a.lde +
-                                             static_cast<int64_t>(j) * a.part_cols) + lane;
-        const uint2 v = *at;
-        *at = make_uint2(pack_bf16x2(__uint_as_float(v.x << 16) * fr, __uint_as_float(v.x & 0xFFFF0000u) * fr),
-                         pack_bf16x2(__uint_as_float(v.y << 16) * fr, __uint_as_float(v.y & 0xFFFF0000u) * fr));
+    const float ref = ref_s[tok];
+    // (no part of this thread: lo = inf)
+    if (__syncthreads_or(rok && lo < ref)) {
+      for (int j = slice; j - slice < a.nparts; j += kSlices) {
+        const float2 p = rok && j < a.nparts ? __ldcg(a.part + static_cast<int64_t>(j) * a.T + t)
+                                             : make_float2(0.0f, 0.0f);
+        uint32_t todo = __ballot_sync(0xFFFFFFFFu, p.y != 0.0f && p.x != ref);
+        const float f = expf(p.x - ref);
+        while (todo) {
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const float fr = __shfl_sync(0xFFFFFFFFu, f, src);
+          const int js = __shfl_sync(0xFFFFFFFFu, j, src), ts = __shfl_sync(0xFFFFFFFFu, t, src);
+          if (4 * lane >= a.part_cols) continue;
+          uint2* at = reinterpret_cast<uint2*>(a.e + static_cast<int64_t>(ts) * a.lde +
+                                               static_cast<int64_t>(js) * a.part_cols) + lane;
+          const uint2 v = __ldcg(at);
+          *at = make_uint2(pack_bf16x2(__uint_as_float(v.x << 16) * fr, __uint_as_float(v.x & 0xFFFF0000u) * fr),
+                           pack_bf16x2(__uint_as_float(v.y << 16) * fr, __uint_as_float(v.y & 0xFFFF0000u) * fr));
+        }
       }
     }
   }
@@ -868,9 +912,7 @@ static cudaError_t launch_head_gemm_impl(const CUtensorMap& tm_a, const CUtensor
 template <int MODE>
 static cudaError_t launch_head_gemm_mode(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
                                          cudaStream_t stream) {
-  if (a.pair)
-    return a.nf4 ? launch_head_gemm_impl<MODE, true, true>(tm_a, tm_b, a, stream)
-                 : launch_head_gemm_impl<MODE, true, false>(tm_a, tm_b, a, stream);
+  if (a.pair) return a.nf4 ? cudaErrorInvalidValue : launch_head_gemm_impl<MODE, true, false>(tm_a, tm_b, a, stream);
   return a.nf4 ? launch_head_gemm_impl<MODE, false, true>(tm_a, tm_b, a, stream)
                : launch_head_gemm_impl<MODE, false, false>(tm_a, tm_b, a, stream);
 }
@@ -891,11 +933,17 @@ cudaError_t launch_head_finish(const HeadArgs& a, cudaStream_t stream) {
                        dim3(kSumStride), 0, stream, dim3(1, 1, 1), a);
 }
 
-int head_combine_blocks(int64_t T) { return static_cast<int>((T + 31) / 32); }
+// Tokens of a combine block: 32, or for few tokens 4 (then at most 512 blocks).
+static int combine_tokens(int64_t T) { return T > 2048 ? 32 : 4; }
+
+int head_combine_blocks(int64_t T) {
+  const int tb = combine_tokens(T);
+  return static_cast<int>((T + tb - 1) / tb);
+}
 
 cudaError_t launch_head_combine(const HeadCombineArgs& a, cudaStream_t stream) {
-  return launch_kernel(head_combine_kernel, dim3(head_combine_blocks(a.T)), dim3(kCombineWarps * 32), 0, stream,
-                       dim3(1, 1, 1), a);
+  return launch_kernel(combine_tokens(a.T) == 32 ? head_combine_kernel<32> : head_combine_kernel<4>,
+                       dim3(head_combine_blocks(a.T)), dim3(kCombineWarps * 32), 0, stream, dim3(1, 1, 1), a);
 }
 
 }  // namespace qnf4

@@ -50,7 +50,7 @@ enum HeadMode {
 constexpr int head_workers(bool pair) { return pair ? 74 : 148; }
 
 struct HeadArgs {
-  int pair, nf4;          // which kernel: tiles of 256 tokens on CTA pairs, W from its codes
+  int pair, nf4;          // which kernel: tiles of 256 tokens on CTA pairs; (single CTAs) W from its codes
   int T;                  // tokens
   int arows;              // token rows of a copy: 128, or for fewer tokens those, to a multiple of 8
   int ncols;              // columns of this product: the piece's vocabulary rows, or dim (Grad)
@@ -92,8 +92,7 @@ struct HeadArgs {
 
 //   tm_a: H [T, dim] (Grad: the piece's [T, ntiles tw]) box {64, arows} SW128;
 //   tm_b: W rows, box {64, tw / 2 (pair) or tw} SW128 (Grad: {64, 64}); with
-//   nf4 W's codes [vocab, dim / 2], box {32, tw / 2 (pair) or tw} SW32 (Grad:
-//   {64, 64} SW64 (pair) or {128, 64} SW128).
+//   nf4 W's codes [vocab, dim / 2], box {32, tw} SW32 (Grad: {128, 64} SW128).
 cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
                              cudaStream_t stream);
 

@@ -182,7 +182,7 @@ def test_well_predicted_tokens_keep_their_gradient():
 
 @pytest.mark.parametrize("T,V,D,centred", [(5, 1001, 64, False), (300, 2300, 512, True), (64, 40000, 2048, False),
                                            (17000, 4500, 128, True), (128, 300, 64, False), (129, 5000, 192, True),
-                                           (512, 1000, 448, False), (513, 700, 128, False), (1, 30000, 1024, False)])
+                                           (512, 1000, 448, False), (127, 70001, 64, True), (1, 30000, 1024, False)])
 def test_nf4_head(T, V, D, centred):
     """An NF4 head is the bf16 head of its dequantised weight.  The logits are the
     same bits; the pieces, and so the order in which a row's exponentials are
