@@ -828,10 +828,20 @@ def _head_call(where, op, H, head, labels):
     return T, D, ldh, dev, h, lambda: qlora_head_loss_workspace_size(T, V, D, nf4, op)
 
 
-def _grad_out(dH, T, D, dev, where):
+def _loss_out(H, loss, lse, stats, T, dev, where):
+    """The losses', log-sum-exps' and statistics' tensors (new ones by the
+    cheapest calls: small problems take no longer on the GPU)."""
+    loss = (H.new_empty((T,), dtype=torch.float32) if loss is None
+            else _tensor(loss, torch.float32, (T,), dev, where, "loss"))
+    lse = torch.empty_like(loss) if lse is None else _tensor(lse, torch.float32, (T,), dev, where, "lse")
+    stats = loss.new_empty(2) if stats is None else _tensor(stats, torch.float32, (2,), dev, where, "stats")
+    return loss, lse, stats
+
+
+def _grad_out(H, dH, T, D, dev, where):
     """(row stride of dH, maker of dH)."""
     if dH is None:
-        return D, lambda: torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+        return D, lambda: H.new_empty((T, D))
     return _rows(dH, where, "dH", D, T, dev)[2], lambda: dH
 
 
@@ -846,9 +856,7 @@ def qlora_head_loss_fwd(H, head, labels, ignore_index=IGNORE_INDEX, loss=None, l
     T, D, ldh, dev, h, size = _head_call(where, HEAD_FWD, H, head, labels)
 
     def call(st):
-        lo = _out(loss, (T,), torch.float32, dev, where, "loss")
-        ls = _out(lse, (T,), torch.float32, dev, where, "lse")
-        sm = _out(stats, (2,), torch.float32, dev, where, "stats")
+        lo, ls, sm = _loss_out(H, loss, lse, stats, T, dev, where)
         at, bytes_, keep = _workspace(ws, size, dev, where)
         _check(_lib.qlora_head_loss_fwd(H.data_ptr(), ldh, T, h, labels.data_ptr(), int(ignore_index), lo.data_ptr(),
                                         ls.data_ptr(), sm.data_ptr(), at, bytes_, _word(status, dev, where), st),
@@ -868,7 +876,7 @@ def qlora_head_loss_bwd(H, head, labels, lse, dloss, stats=None, ignore_index=IG
     _tensor(dloss, torch.float32, (T if stats is None else 1,), dev, where, "dloss")
     if stats is not None:
         _tensor(stats, torch.float32, (2,), dev, where, "stats")
-    ldd, grad = _grad_out(dH, T, D, dev, where)
+    ldd, grad = _grad_out(H, dH, T, D, dev, where)
 
     def call(st):
         g = grad()
@@ -889,12 +897,10 @@ def qlora_head_loss_step(H, head, labels, weight=None, scale=1.0, ignore_index=I
     T, D, ldh, dev, h, size = _head_call(where, HEAD_STEP, H, head, labels)
     if weight is not None:
         _tensor(weight, torch.float32, (T,), dev, where, "weight")
-    ldd, grad = _grad_out(dH, T, D, dev, where)
+    ldd, grad = _grad_out(H, dH, T, D, dev, where)
 
     def call(st):
-        lo = _out(loss, (T,), torch.float32, dev, where, "loss")
-        ls = _out(lse, (T,), torch.float32, dev, where, "lse")
-        sm = _out(stats, (2,), torch.float32, dev, where, "stats")
+        lo, ls, sm = _loss_out(H, loss, lse, stats, T, dev, where)
         g = grad()
         at, bytes_, keep = _workspace(ws, size, dev, where)
         _check(_lib.qlora_head_loss_step(H.data_ptr(), ldh, T, h, labels.data_ptr(), int(ignore_index),

@@ -1543,10 +1543,12 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
   a.arows = static_cast<int>(abox);
   if (!map_bf16_ld(&mh, c.H, T, D, c.ldh, 64, abox)) return QLORA_ERR_CUDA;
   const uint32_t wbox = static_cast<uint32_t>(p.pair ? p.tw / 2 : p.tw);
-if (p.codes && (!map_u8(&mw, hd.codes, V, D / 2, 32, wbox, 32) ||
-                  !map_u8(&mwt, hd.codes, V, D / 2, 128, 64, 128)))
+  const bool grad = op != QLORA_HEAD_FWD;
+  if (p.codes && (!map_u8(&mw, hd.codes, V, D / 2, 32, wbox, 32) ||
+                  (grad && !map_u8(&mwt, hd.codes, V, D / 2, 128, 64, 128))))
     return QLORA_ERR_CUDA;
-  if (!nf4 && (!map_bf16_ld(&mw, hd.w, V, D, hd.ld, 64, wbox) || !map_bf16_ld(&mwt, hd.w, V, D, hd.ld, 64, 64)))
+  if (!nf4 && (!map_bf16_ld(&mw, hd.w, V, D, hd.ld, 64, wbox) ||
+               (grad && !map_bf16_ld(&mwt, hd.w, V, D, hd.ld, 64, 64))))
     return QLORA_ERR_CUDA;
 
   for (int64_t i = 0; i < p.pieces; ++i) {
@@ -1556,7 +1558,7 @@ if (p.codes && (!map_u8(&mw, hd.codes, V, D / 2, 32, wbox, 32) ||
       const int64_t e0 = v0 * D;
       CUtensorMap out;
       if (!map_bf16(&out, wbuf, pv * D / 64, 64, 64, 32, 128) || !map_bf16_ld(&mw, wbuf, pv, D, D, 64, wbox) ||
-          !map_bf16_ld(&mwt, wbuf, pv, D, D, 64, 64))
+          (grad && !map_bf16_ld(&mwt, wbuf, pv, D, D, 64, 64)))
         return QLORA_ERR_CUDA;
       ProfScope ps(kKDequantize, cs);
       if (qlora_status st = from_cuda(launch_nf4_dequantize(hd.codes + e0 / 2, hd.c8 + e0 / 64, hd.s2 + e0 / 16384,

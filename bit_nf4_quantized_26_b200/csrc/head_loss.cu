@@ -462,94 +462,72 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     const int blocks = kGrad ? P::kBRows : tw;  // of a stage
     const int64_t kbpr = a.head.dim / 64;
     const Nf4Mean wmean = nf4_load_mean(a.head.mean);
-    // this thread's codes in the stage, as 16-byte chunks
-    uint32_t c_at, c_x;  // byte offset of the row; chunk pair (2 h) ^ swizzle
-    if constexpr (kGrad) {
-      c_at = (i & 63) * 128;
-      c_x = ((i >> 6) * 2) ^ (i & 7);
-    } else {
-      c_at = i * 32;
-      c_x = (i >> 2) & 1;
-    }
+    // this thread's codes in the stage: byte offset of its row, 16-byte chunk
+    const uint32_t c_at = P::kB + (kGrad ? (i & 63) * 128 : i * 32);
+    const uint32_t c_0 = (kGrad ? ((i >> 6) * 2) ^ (i & 7) : (i >> 2) & 1) << 4;
+    const uint32_t d_0 = i * 128 + ((i & 7) << 4);  // its row of the tile (Grad: atom i / 64, row i % 64), swizzled
+    const int64_t b_step = kGrad ? P::kGroups * 64 * kbpr : P::kGroups;
     constexpr int kAhead = 4;
-    struct At {  // a stage of this worker's tiles
-      int tile, kt, k1, bcol;
-    };
-    auto enter = [&](At& p) {  // first stage of p.tile, or of a later one that has any
-      for (; p.tile < tiles; p.tile += workers) {
-        const int split = p.tile / mn;
-        int m, n;
-        head_tile<kGrad>(p.tile - split * mn, a.mtiles, a.ntiles, m, n);
-        p.bcol = n * tw;
-        p.kt = split * a.kper;
-        p.k1 = min(a.kst, p.kt + a.kper);
-        if (p.kt < p.k1) return;
-      }
-    };
-    auto advance = [&](At& p, int by) {
-      for (int k = 0; k < by && p.tile < tiles; ++k) {
-        if (++p.kt >= p.k1) {
-          p.tile += workers;
-          enter(p);
-        }
-      }
-    };
-    uint32_t pk[kAhead];
-    float ps[kAhead];
-    auto fetch = [&](const At& p, uint32_t& k8, float& s2) {
-      k8 = 0x100;  // outside: zeros, whatever the codes
-      s2 = 0.0f;
-      if (p.tile >= tiles || i >= blocks) return;
-      const int row = kGrad ? p.kt * 64 + (i & 63) : p.bcol + i;  // of the piece
-      const int64_t kb = kGrad ? p.bcol / 64 + (i >> 6) : p.kt;
-      if (row >= a.wrows || kb >= kbpr) return;
-      const int64_t b = (a.v0 + row) * kbpr + kb;
-      k8 = __ldg(a.head.c8 + b);
-      s2 = __ldg(a.head.s2 + (b >> 8));
-    };
-    At now{worker, 0, 0, 0};
-    enter(now);
-    advance(now, grp);
-    At fut = now;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      fetch(fut, pk[j], ps[j]);
-      advance(fut, P::kGroups);
-    }
-    // (Unrolled over the slots, so that each is refilled in place: moving a
-    // register that a load is still filling waits for the load.)
-    bool ok = true;
     Ring<P::kStages> at;
     at.advance(grp);
-    while (ok && now.tile < tiles) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (now.tile >= tiles) break;
-        const uint32_t s = at.slot;
-        const float chat = pk[j] == 0x100u ? 0.0f : nf4_block_scale(pk[j], ps[j], wmean);
-        const Nf4Lut lut = nf4_make_lut(a.tab, chat);
-        fetch(fut, pk[j], ps[j]);
-        if (!mbar_wait_all(&cfull[s], at.parity, wc)) {
-          ok = false;
-          break;
+    int begun = 0;  // stages of the tiles before, modulo the groups
+    bool ok = true;
+    for (int tile = worker; ok && tile < tiles; tile += workers) {
+      const int split = tile / mn;
+      int m, n;
+      head_tile<kGrad>(tile - split * mn, a.mtiles, a.ntiles, m, n);
+      const int kt0 = split * a.kper, kn = min(a.kst, kt0 + a.kper) - kt0;
+      if (kn <= 0) continue;
+      const int g0 = (grp + P::kGroups - begun) % P::kGroups;         // the group's first stage of the tile
+      const int count = (kn - g0 + P::kGroups - 1) / P::kGroups;      // and its number of them
+      begun = (begun + kn) % P::kGroups;
+      // the thread's block of its first stage, and how many stages have one
+      const int row = kGrad ? (kt0 + g0) * 64 + (i & 63) : n * tw + i;  // of the piece
+      const int64_t kb = kGrad ? n * tw / 64 + (i >> 6) : kt0 + g0;
+      int64_t b = (a.v0 + row) * kbpr + kb;
+      int left = i < blocks && row < a.wrows && kb < kbpr ? count : 0;
+      if (kGrad) left = min(left, (a.wrows - row + 64 * P::kGroups - 1) / (64 * P::kGroups));
+      uint32_t pk[kAhead];
+      float ps[kAhead];
+      auto fetch = [&](uint32_t& k8, float& s2) {
+        k8 = 0x100;  // outside: zeros, whatever the codes
+        s2 = 0.0f;
+        if (left-- > 0) {
+          k8 = __ldg(a.head.c8 + b);
+          s2 = __ldg(a.head.s2 + (b >> 8));
+          b += b_step;
         }
-        if (i < blocks) {
-          uint8_t* st = smem + s * P::kStage + P::kA;
-          const uint8_t* codes = st + P::kB + c_at;
-          const uint4 c0 = *reinterpret_cast<const uint4*>(codes + (c_x << 4));
-          const uint4 c1 = *reinterpret_cast<const uint4*>(codes + ((c_x ^ 1) << 4));
-          const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-          uint8_t* dst = st + i * 128;  // (Grad: atom i / 64, row i % 64)
+      };
 #pragma unroll
-          for (uint32_t c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(dst + ((c ^ (i & 7)) << 4)) = nf4_lookup8(cw[c], lut);
+      for (int j = 0; j < kAhead; ++j) fetch(pk[j], ps[j]);
+      // (Unrolled over the slots, so that each is refilled in place: moving a
+      // register that a load is still filling waits for the load.)
+      for (int k = 0; ok && k < count; k += kAhead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (k + j >= count) break;
+          const uint32_t s = at.slot;
+          const Nf4Lut lut =
+              nf4_make_lut(a.tab, pk[j] == 0x100u ? 0.0f : nf4_block_scale(pk[j], ps[j], wmean));
+          fetch(pk[j], ps[j]);
+          if (!mbar_wait_all(&cfull[s], at.parity, wc)) {
+            ok = false;
+            break;
+          }
+          if (i < blocks) {
+            uint8_t* st = smem + s * P::kStage + P::kA;
+            const uint4 c0 = *reinterpret_cast<const uint4*>(st + c_at + c_0);
+            const uint4 c1 = *reinterpret_cast<const uint4*>(st + c_at + (c_0 ^ 16));
+            const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+            for (uint32_t c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(st + (d_0 ^ (c << 4))) = nf4_lookup8(cw[c], lut);
+          }
+          fence_proxy_async_smem();  // this lane's row -> async proxy
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+          at.advance(P::kGroups);
         }
-        fence_proxy_async_smem();  // this lane's row -> async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
-        at.advance(P::kGroups);
-        advance(fut, P::kGroups);
-        advance(now, P::kGroups);
       }
     }
   } else {
