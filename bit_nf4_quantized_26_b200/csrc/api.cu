@@ -1571,7 +1571,9 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     a.ncols = static_cast<int>(pv);
     a.ntiles = static_cast<int>(cdiv(pv, p.tw));
     a.kst = static_cast<int>(cdiv(D, 64));
-    a.kchunk = op == QLORA_HEAD_BWD ? 64 : 12;
+    // 64-deep stages per accumulator (head_loss.cu): a product of few tokens
+    // waits for the weight, and short chunks cost it nothing
+    a.kchunk = op == QLORA_HEAD_BWD ? 64 : (p.pair ? 12 : 4);
     a.splits = 1;
     a.kper = a.kst;
     float2* part = reinterpret_cast<float2*>(at(p.off_part));

@@ -260,8 +260,8 @@ struct Ring {
 // contraction of a loss is therefore cut into chunks (768 deep: 48 steps, a
 // drift of 6e-7) that alternate between two accumulators, and the epilogue
 // threads add each finished one to their registers, rounding to nearest, while
-// the next runs.  (512 deep costs the products 2-3%, 1024 nothing.)  Results
-// rounded to bf16 take longer ones: the backward's probabilities 4096, dH a
+// the next runs.  (512 deep costs the products 2-3%, 1024 nothing; 256 is free
+// for few tokens, whose products wait for W.)  Results rounded to bf16 take longer ones: the backward's probabilities 4096, dH a
 // whole slice of its contraction.
 //
 // Barriers (leader: the pair's first CTA, or the single one): full[s] (leader:

@@ -103,7 +103,8 @@ QLORA_API qlora_status qlora_linear_bwd_dropout_act8(const uint16_t* dY, const u
  *
  * The head: W [vocab, dim], either bf16 rows (`w`, row stride ld elements,
  * ld % 8 == 0, dim % 8 == 0) or, with w == NULL, NF4 (codes, c8, s2 and an
- * optional mean as in nf4_weight; dim % 64 == 0), dequantised piece by piece.
+ * optional mean as in nf4_weight; dim % 64 == 0), dequantised inside the
+ * products (up to 128 tokens) or piece by piece before them.
  */
 typedef struct {
   const uint16_t* w;    /* bf16 rows, or NULL for an NF4 head */
@@ -136,16 +137,16 @@ typedef struct {
  *
  * T >= 0 (0 = no-op; stats is then {0, 0}), T < 2^31, vocab in 1 .. 2^31 - 1,
  * dim in 8 .. 2^20, vocab * dim < 2^40, ld / ldh / lddh < 2^31, else
- * QLORA_ERR_SHAPE.  dH does not overlap H.  The per-token vectors and stats need
+ * QLORA_ERR_SHAPE.  dH may be H itself (the same rows).  The per-token vectors and stats need
  * their type's alignment only (a shifted view of the labels is fine).
  * Workspaces: qlora_head_loss_workspace_size(T, vocab, dim, nf4, op) bytes with
  * nf4 nonzero for an NF4 head and op one of QLORA_HEAD_FWD / _BWD / _STEP.
- * Beside per-token words it holds 8 bytes per 128 logits (fewer for few tokens;
- * forward, step), a
- * piece of the probabilities (backward, step: about 128 MB in bf16, at least
- * 2048 columns), fp32 sums [T, dim] (with several pieces, and for few tokens
- * one per slice of the contraction), and a dequantised piece of an NF4 head (at
- * most 128 MB, at least 2048 rows).
+ * Beside per-token words it holds 8 bytes per half tile of logits (128, or
+ * fewer columns where that fills the GPU; forward, step), a piece of the
+ * probabilities (backward, step: about 128 MB in bf16, at least 2048 columns),
+ * fp32 sums [T, dim] (with several pieces, and for few tokens one per slice of
+ * the contraction), and, for more than 128 tokens, a dequantised piece of an
+ * NF4 head (at most 128 MB, at least 2048 rows).
  * Accuracy: exact bf16 inputs, fp32 accumulation and softmax; the probabilities
  * enter the second product as bf16 (label term subtracted in fp32 first); dH
  * within 5e-3 relative Frobenius error of the fp64 gradient.

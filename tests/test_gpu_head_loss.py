@@ -182,7 +182,7 @@ def test_well_predicted_tokens_keep_their_gradient():
 
 @pytest.mark.parametrize("T,V,D,centred", [(5, 1001, 64, False), (300, 2300, 512, True), (64, 40000, 2048, False),
                                            (17000, 4500, 128, True), (128, 300, 64, False), (129, 5000, 192, True),
-                                           (512, 1000, 448, False), (127, 70001, 64, True), (1, 30000, 1024, False)])
+                                           (512, 1000, 448, False), (127, 70001, 64, True), (3, 1, 64, False), (70, 63, 128, True), (1, 30000, 1024, False)])
 def test_nf4_head(T, V, D, centred):
     """An NF4 head is the bf16 head of its dequantised weight.  The logits are the
     same bits; the pieces, and so the order in which a row's exponentials are
@@ -230,14 +230,17 @@ def test_ignored_rows_may_hold_anything():
     keep = torch.tensor([i for i in range(300) if i not in (5, 6, 200, 299)], device="cuda")
     a, b = (q.qlora_head_loss_fwd(x, W, Y, status=status) for x in (H, C))
     g = torch.ones(300, device="cuda")
+    g[5], g[200] = float("nan"), float("inf")  # nor are their gradients read
     assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2]) and torch.equal(a[1][keep], b[1][keep])
     da, db = q.qlora_head_loss_bwd(H, W, Y, a[1], g, status=status), q.qlora_head_loss_bwd(C, W, Y, b[1], g)
     sa, sb = q.qlora_head_loss_step(H, W, Y, status=status), q.qlora_head_loss_step(C, W, Y)
-    for x, z in ((da, db), (sa[3], sb[3]), (sa[0], sb[0]), (sa[2], sb[2])):
+    wa, wb = q.qlora_head_loss_step(H, W, Y, weight=g, status=status), q.qlora_head_loss_step(C, W, Y, weight=g)
+    for x, z in ((da, db), (wa[3], wb[3]), (sa[3], sb[3]), (sa[0], sb[0]), (sa[2], sb[2])):
         assert torch.equal(x, z)
     assert not da[5].any() and not sa[3][200].any()
     assert int(status[0]) == 0
     # a counted token's NaN stays with its row and is reported
+    g = torch.ones(300, device="cuda")
     y2 = Y.clone()
     y2[5] = 1
     s2 = q.qlora_head_loss_step(H, W, y2, weight=g, status=status)
@@ -316,6 +319,21 @@ def test_strided_rows_and_shifted_labels():
     assert bool((dH[:, :8] == 3).all()) and bool((dH[:, 8 + D:] == 3).all()) and bool((dH[T] == 3).all())
     c = q.qlora_head_loss_bwd(H, W, Y, a[1], g, dH=dH[:T, 8:8 + D])
     assert torch.equal(c, q.qlora_head_loss_bwd(h.cuda(), w.cuda(), y.cuda(), b[1], g))
+
+
+@pytest.mark.parametrize("T,V,D", [(40, 300, 64), (300, 700, 128), (16500, 4500, 64)])
+def test_gradient_in_place_of_the_hidden_states(T, V, D):
+    h, w, y = _case(T, V, D, seed=10)
+    W, Y, g = w.cuda(), y.cuda(), torch.linspace(-1, 1, T, device="cuda")
+    want = q.qlora_head_loss_step(h.cuda(), W, Y, weight=g)
+    H = h.cuda()
+    got = q.qlora_head_loss_step(H, W, Y, weight=g, dH=H)
+    assert got[3].data_ptr() == H.data_ptr()
+    for x, z in zip(got, want):
+        assert torch.equal(x, z)
+    H = h.cuda()
+    dH = q.qlora_head_loss_bwd(H, W, Y, want[1], g, dH=H)
+    assert torch.equal(dH, q.qlora_head_loss_bwd(h.cuda(), W, Y, want[1], g))
 
 
 def test_gradient_against_differences_of_the_loss():
