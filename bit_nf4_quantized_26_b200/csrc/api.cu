@@ -1336,17 +1336,18 @@ struct HeadPlanHost {
   int64_t tw = 0;                // columns of a logit tile
   int64_t ldg = 0, parts = 0;    // per piece: columns its tiles cover, and their halves
   int64_t splits = 1, kper = 0;  // slices of a piece's dH contraction, 64-deep stages each
+  int64_t cost = 0;              // of the products: waves x 64-deep stages x columns
   size_t off_cnt = 0, off_z = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_sum = 0, off_pl = 0;
   size_t off_g = 0, off_acc = 0, off_w = 0, total = 0;
 };
 
 // Slices of the dH contraction of a piece (kst stages) over `tiles` tiles and
-// `workers` CTA pairs or CTAs: waves x (stages per slice + what a slice's fp32 sums cost to
-// write and join, about 12 stages' time), slices of at least 8 stages, only
-// while all slices together are under four waves (beyond that the sums cost
-// more than the last wave's idle pairs).
-static void head_splits(int64_t tiles, int64_t kst, int64_t workers, int64_t& splits, int64_t& per) {
-  constexpr int64_t kCost = 12;
+// `workers` CTA pairs or CTAs: waves x (stages per slice + what a slice's fp32
+// sums cost to write and join, about 24 stages' time), slices of at least 8
+// stages, only while all slices together are under four waves (beyond that the
+// sums cost more than the last wave's idle pairs).  Returns waves x stages.
+static int64_t head_splits(int64_t tiles, int64_t kst, int64_t workers, int64_t& splits, int64_t& per) {
+  constexpr int64_t kCost = 24;
   int64_t best = 1, cost = cdiv(tiles, workers) * kst;
   for (int64_t s = 2; s <= kst / 8 && tiles * s <= 4 * workers; ++s) {
     const int64_t c = cdiv(tiles * s, workers) * (cdiv(kst, s) + kCost);
@@ -1357,36 +1358,38 @@ static void head_splits(int64_t tiles, int64_t kst, int64_t workers, int64_t& sp
   }
   per = cdiv(kst, best);
   splits = cdiv(kst, per);
+  return cost;
 }
 
 // Columns of a logit tile: the width that makes the fewest column-times of
-// waves of the CTA pairs or CTAs, a tile costing its width and about 16 columns' time
-// more (its token side, filling and draining).  256 when the waves are many;
-// 32000 rows of one token tile: 143 tiles of 224 instead of 125 of 256, whose
-// second wave is two thirds empty.
-static int64_t head_tile_width(int64_t mt, int64_t cols, int64_t widest, int64_t workers) {
-  int64_t best = widest, cost = -1;
+// waves of the CTA pairs or CTAs, a tile costing its width and about 16
+// columns' time more (its token side, filling and draining).  256 when the
+// waves are many; 32000 rows of one token tile: 143 tiles of 224 instead of 125
+// of 256, whose second wave is two thirds empty.  Returns waves x columns.
+static int64_t head_tile_width(int64_t mt, int64_t cols, int64_t widest, int64_t workers, int64_t& width) {
+  int64_t cost = -1;
   for (int64_t w = widest; w >= 64; w -= 32) {
     const int64_t c = cdiv(mt * cdiv(cols, w), workers) * (w + 16);
     if (cost < 0 || c < cost) {
       cost = c;
-      best = w;
+      width = w;
     }
   }
-  return best;
+  return cost;
 }
 
-static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op) {
+// The walk with one kind of token tiles.
+static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, int op, bool pair) {
   HeadPlanHost p;
   const int64_t tile = kHeadTile;
-  p.pair = T > 128;
+  p.pair = pair;
   // An NF4 head of few tokens is read from its codes.  32000 x 4096, forward /
-  // step: 64 tokens 87 / 158 us, against 116 / 168 with the head dequantised
-  // first (58 us); 256 tokens 126 / 215 against 122 / 198.
-  p.codes = nf4 && !p.pair;
-  const int64_t workers = head_workers(p.pair);
-  const int64_t vt = cdiv(V, tile), mt = cdiv(T, p.pair ? 256 : 128);
-  const int64_t trows = mt * (p.pair ? 256 : 128);
+  // step: 64 tokens 70 / 134 us, against 116 / 168 with the head dequantised
+  // first (58 us); two token tiles would dequantise everything twice.
+  p.codes = nf4 && T <= 128;
+  const int64_t workers = head_workers(pair);
+  const int64_t vt = cdiv(V, tile), mt = cdiv(T, pair ? 256 : 128);
+  const int64_t trows = mt * (pair ? 256 : 128);
   int64_t piece = vt * tile;
   if (op != QLORA_HEAD_FWD) {
     const int64_t fit = (int64_t(1) << 26) / trows / tile * tile;
@@ -1399,10 +1402,14 @@ static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op)
   p.pieces = cdiv(vt * tile, piece);
   p.piece = cdiv(vt, p.pieces) * tile;  // even pieces
   p.pieces = cdiv(vt * tile, p.piece);
-  p.tw = head_tile_width(mt, std::min(p.piece, V), p.codes ? 128 : 256, workers);
+  const int64_t cols = head_tile_width(mt, std::min(p.piece, V), p.codes ? 128 : 256, workers, p.tw);
+  p.cost = p.pieces * cols * cdiv(D, 64);
   p.ldg = cdiv(p.piece, p.tw) * p.tw;
   p.parts = 2 * cdiv(p.piece, p.tw);
-  if (op != QLORA_HEAD_FWD) head_splits(mt * cdiv(D, tile), p.piece / 64, workers, p.splits, p.kper);
+  if (op != QLORA_HEAD_FWD) {
+    const int64_t stages = head_splits(mt * cdiv(D, tile), cdiv(std::min(p.piece, V), 64), workers, p.splits, p.kper);
+    p.cost += p.pieces * stages * tile;
+  }
   size_t off = 0;
   auto take = [&off](size_t bytes) {
     const size_t at = off;
@@ -1431,6 +1438,19 @@ static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op)
   if (nf4 && !p.codes) p.off_w = take(2 * static_cast<size_t>(std::min(p.piece, V)) * static_cast<size_t>(D));
   p.total = off;
   return p;
+}
+
+// Tiles of 256 tokens on CTA pairs share W's tile between two SMs; tiles of 128
+// on single CTAs leave less of the last tile empty and fill the last wave
+// better, but take about a quarter longer per column (380 tokens x 50000 x
+// 2048, loss and gradient: 186 us against 228, the modelled costs 0.68 to 1;
+// 640 x 32000 x 4096, forward: 181 against 174, 0.83 to 1).  Up to 128 tokens
+// the pair's second CTA would have none.
+static HeadPlanHost plan_head(int64_t T, int64_t V, int64_t D, bool nf4, int op) {
+  const HeadPlanHost single = plan_head_tiles(T, V, D, nf4, op, false);
+  if (T <= 128) return single;
+  const HeadPlanHost pair = plan_head_tiles(T, V, D, nf4, op, true);
+  return T <= 2048 && 5 * single.cost < 4 * pair.cost ? single : pair;
 }
 
 static qlora_status check_head_shape(int64_t T, int64_t V, int64_t D, bool nf4) {

@@ -38,8 +38,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRefRange = 40.0f;  // tile maxima within +-kRefRange share the reference 0
 
-// PAIR: tiles of 256 tokens on CTA pairs; otherwise, for at most 128 tokens,
-// of 128 on single CTAs (twice the workers, none of the tile without tokens).
+// PAIR: tiles of 256 tokens on CTA pairs; otherwise of 128 on single CTAs.
 // NF4 (single CTAs only): W's tile is dequantised into the ring from its codes.
 template <int MODE, bool PAIR, bool NF4>
 struct HeadPlan {

@@ -82,7 +82,7 @@ class Ref:
 
 # tokens, vocabulary, width: one of each, odd ones, tile borders, widths that end inside a stage
 SHAPES = [(1, 1, 8), (1, 1000, 64), (3, 257, 72), (129, 256, 256), (200, 1003, 520), (256, 512, 64), (257, 255, 192),
-          (700, 3001, 1024), (60, 33000, 256), (128, 4000, 328), (16, 40001, 640)]
+          (700, 3001, 1024), (60, 33000, 256), (128, 4000, 328), (16, 40001, 640), (380, 20000, 512), (300, 9000, 320)]
 
 
 @pytest.mark.parametrize("T,V,D", SHAPES)
@@ -182,7 +182,7 @@ def test_well_predicted_tokens_keep_their_gradient():
 
 @pytest.mark.parametrize("T,V,D,centred", [(5, 1001, 64, False), (300, 2300, 512, True), (64, 40000, 2048, False),
                                            (17000, 4500, 128, True), (128, 300, 64, False), (129, 5000, 192, True),
-                                           (512, 1000, 448, False), (127, 70001, 64, True), (3, 1, 64, False), (70, 63, 128, True), (1, 30000, 1024, False)])
+                                           (512, 1000, 448, False), (127, 70001, 64, True), (3, 1, 64, False), (70, 63, 128, True), (380, 20000, 512, False), (1, 30000, 1024, False)])
 def test_nf4_head(T, V, D, centred):
     """An NF4 head is the bf16 head of its dequantised weight.  The logits are the
     same bits; the pieces, and so the order in which a row's exponentials are
