@@ -668,8 +668,9 @@ def act8_quantize(X, codes=None, exps=None, status=None, stream=None):
     dev = X.device
 
     def call(st):
-        c = _out(codes, (M, K), torch.uint8, dev, where, "codes")
-        e = _out(exps, (M, K // 64), torch.uint8, dev, where, "exps")
+        c = (X.new_empty((M, K), dtype=torch.uint8) if codes is None
+             else _tensor(codes, torch.uint8, (M, K), dev, where, "codes"))
+        e = c.new_empty((M, K // 64)) if exps is None else _tensor(exps, torch.uint8, (M, K // 64), dev, where, "exps")
         _check(_lib.act8_quantize(X.data_ptr(), M, K, ld, c.data_ptr(), e.data_ptr(), _word(status, dev, where), st),
                where)
         return Act8(c, e)

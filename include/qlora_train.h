@@ -135,9 +135,10 @@ typedef struct {
  *   g_t = scale / count (the gradient of scale * mean).  loss, lse and stats
  *   are those of the forward, unscaled and unweighted.
  *
- * T >= 0 (0 = no-op; stats is then {0, 0}), T < 2^31, vocab in 1 .. 2^31 - 1,
+ * T >= 0 (0 = no-op; stats is then {0, 0}), vocab >= 1, both below 2^31 - 256,
  * dim in 8 .. 2^20, vocab * dim < 2^40, ld / ldh / lddh < 2^31, else
- * QLORA_ERR_SHAPE.  dH may be H itself (the same rows).  The per-token vectors and stats need
+ * QLORA_ERR_SHAPE; so does ceil(T / 256) x ceil(max(vocab, dim) / 256) from
+ * 2^23.  dH may be H itself (the same rows).  The per-token vectors and stats need
  * their type's alignment only (a shifted view of the labels is fine).
  * Workspaces: qlora_head_loss_workspace_size(T, vocab, dim, nf4, op) bytes with
  * nf4 nonzero for an NF4 head and op one of QLORA_HEAD_FWD / _BWD / _STEP.

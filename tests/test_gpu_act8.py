@@ -57,18 +57,20 @@ def test_every_finite_bf16_value():
     assert int(status[0]) == 0
 
 
-def test_strided_rows_and_the_gap_between_them():
-    M, K, ld = 37, 192, 320
+@pytest.mark.parametrize("ld,o", [(320, 64), (320, 8), (328, 64), (200, 8)])
+def test_strided_rows_and_the_gap_between_them(ld, o):
+    """Rows aligned to 32 bytes, and to the 16 that are asked for."""
+    M, K = 37, 192
     buf = torch.full((M, ld), 7.0, dtype=torch.bfloat16, device="cuda")
     x = _x(M, K, 3)
-    buf[:, 64:64 + K] = x.cuda()
-    x8 = q.act8_quantize(buf[:, 64:64 + K])
+    buf[:, o:o + K] = x.cuda()
+    x8 = q.act8_quantize(buf[:, o:o + K])
     codes, exps = act8.quantize(bits(x))
     assert np.array_equal(x8.codes.cpu().numpy(), codes) and np.array_equal(x8.exps.cpu().numpy(), exps)
     out = torch.full((M, ld), 9.0, dtype=torch.bfloat16, device="cuda")
-    q.act8_dequantize(x8, out=out[:, 64:64 + K])
-    assert np.array_equal(out[:, 64:64 + K].double().cpu().numpy(), act8.dequantize(codes, exps))
-    assert bool((out[:, :64] == 9).all()) and bool((out[:, 64 + K:] == 9).all())
+    q.act8_dequantize(x8, out=out[:, o:o + K])
+    assert np.array_equal(out[:, o:o + K].double().cpu().numpy(), act8.dequantize(codes, exps))
+    assert bool((out[:, :o] == 9).all()) and bool((out[:, o + K:] == 9).all())
 
 
 def test_non_finite_values_keep_their_place():
