@@ -581,8 +581,11 @@ _lib.qlora_linear_bwd_dropout_act8.argtypes = [_P, _P, _P, _P, _I64, _NF4Weight,
                                                _P, _P, _P, _SZ, _P, _P]
 _lib.qlora_linear_bwd_dropout_act8.restype = ctypes.c_int
 
-EXPORTED_TRAIN = ("act8_quantize", "act8_dequantize", "qlora_linear_bwd_act8", "qlora_group_bwd_act8",
-                  "qlora_linear_bwd_dropout_act8")
+_lib.qlora_bwd_act8_workspace_size.argtypes = [_I64, _I64, _I64, _I32, _I32, _I32]
+_lib.qlora_bwd_act8_workspace_size.restype = _SZ
+
+EXPORTED_TRAIN = ("act8_quantize", "act8_dequantize", "qlora_bwd_act8_workspace_size", "qlora_linear_bwd_act8",
+                  "qlora_group_bwd_act8", "qlora_linear_bwd_dropout_act8")
 
 DEV_LABEL = 4
 ERR_SHAPE = 2
@@ -701,7 +704,11 @@ def _act8(X8, M, K, dev, where):
     _tensor(exps, torch.uint8, (M, K // 64), dev, where, "exps")
 
 
-def _bwd_act8(where, dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, size, ws, status, stream, run):
+def qlora_bwd_act8_workspace_size(M, N, K, members, r, dropout=False):
+    return int(_lib.qlora_bwd_act8_workspace_size(M, N, K, members, r, 1 if dropout else 0))
+
+
+def _bwd_act8(where, dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, drop, ws, status, stream, run):
     """Checks, outputs and workspace shared by the ``*_bwd_act8`` passes."""
     N, K = int(W.n_out), int(W.k_in)
     M = dY.shape[0]
@@ -728,7 +735,7 @@ def _bwd_act8(where, dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, size, ws, stat
         if M == 0:  # nothing to sum; the library's call is a no-op
             a.zero_()
             b.zero_()
-        at, size_, keep = _workspace(ws, lambda: size(M, N, K, r), dev, where)
+        at, size_, keep = _workspace(ws, lambda: qlora_bwd_act8_workspace_size(M, N, K, G, r, drop), dev, where)
         _check(run(M, r, x.data_ptr(), a.data_ptr(), b.data_ptr(), at, size_, _word(status, dev, where), st), where)
         return x, a, b
     return _run(dev, stream, call)
@@ -742,8 +749,8 @@ def qlora_linear_bwd_act8(dY, X8, U, W, A, B, s, dx_dtype=DTYPE_BF16, dX=None, d
         return _lib.qlora_linear_bwd_act8(dY.data_ptr(), X8[0].data_ptr(), X8[1].data_ptr(), U.data_ptr(), M,
                                           _weight(W), A.data_ptr(), B.data_ptr(), r, float(s), dX, dx_dtype, dA, dB,
                                           ws, size, status, st)
-    return _bwd_act8("qlora_linear_bwd_act8", dY, X8, U, W, 1, A, B, dx_dtype, dX, dA, dB,
-                     qlora_bwd_workspace_size, ws, status, stream, call)
+    return _bwd_act8("qlora_linear_bwd_act8", dY, X8, U, W, 1, A, B, dx_dtype, dX, dA, dB, False, ws, status, stream,
+                     call)
 
 
 def qlora_group_bwd_act8(dY, X8, U, W, n_member, A, B, s, dx_dtype=DTYPE_BF16, dX=None, dA=None, dB=None, ws=None,
@@ -751,14 +758,11 @@ def qlora_group_bwd_act8(dY, X8, U, W, n_member, A, B, s, dx_dtype=DTYPE_BF16, d
     """:func:`qlora_group_bwd` with the shared input as its 8-bit checkpoint ``X8``."""
     G, arr = _members(n_member)
 
-    def size(M, N, K, r):
-        return qlora_group_bwd_workspace_size(M, N, K, G, r)
-
     def call(M, r, dX, dA, dB, ws, size, status, st):
         return _lib.qlora_group_bwd_act8(dY.data_ptr(), X8[0].data_ptr(), X8[1].data_ptr(), U.data_ptr(), M,
                                          _weight(W), G, ctypes.cast(arr, _P), A.data_ptr(), B.data_ptr(), r, float(s),
                                          dX, dx_dtype, dA, dB, ws, size, status, st)
-    return _bwd_act8("qlora_group_bwd_act8", dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, size, ws, status, stream,
+    return _bwd_act8("qlora_group_bwd_act8", dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, False, ws, status, stream,
                      call)
 
 
@@ -770,8 +774,8 @@ def qlora_linear_bwd_dropout_act8(dY, X8_drop, U, W, A, B, s, p, seed, dx_dtype=
         return _lib.qlora_linear_bwd_dropout_act8(dY.data_ptr(), X8_drop[0].data_ptr(), X8_drop[1].data_ptr(),
                                                   U.data_ptr(), M, _weight(W), A.data_ptr(), B.data_ptr(), r, float(s),
                                                   float(p), int(seed), dX, dx_dtype, dA, dB, ws, size, status, st)
-    return _bwd_act8("qlora_linear_bwd_dropout_act8", dY, X8_drop, U, W, 1, A, B, dx_dtype, dX, dA, dB,
-                     qlora_bwd_dropout_workspace_size, ws, status, stream, call)
+    return _bwd_act8("qlora_linear_bwd_dropout_act8", dY, X8_drop, U, W, 1, A, B, dx_dtype, dX, dA, dB, True, ws,
+                     status, stream, call)
 
 
 # ------------------------------------------------------------------ loss head

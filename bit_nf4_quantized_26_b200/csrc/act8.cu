@@ -144,21 +144,21 @@ __global__ void __launch_bounds__(kActThreads) act8_dequantize_kernel(const uint
 // of dU's bf16 hi/lo columns, tiles of 128 input features, the tokens split
 // over a cluster and summed in rank order through distributed shared memory),
 // with the token-side operand turned from codes into bf16 on the way: copies
-// bring 64 tokens x 128 codes (8 KB) beside dU's 16 KB, and two groups of four
-// warps taking alternate stages write them as the MN-major 128-byte-swizzled
-// tile the tensor core reads.  A stage is a chain (copy, convert, multiply)
-// and runs beside the dX GEMM on few SMs, so what counts is how many are in
-// flight: six copies and four converted tiles, one CTA per SM.  (Three and
-// two with one group, two CTAs per SM, took 193 us for 16384 tokens of 4096
-// features on 64 CTAs.)  The rings are even, so a slot's earlier stages are
+// bring 64 tokens x 128 codes (8 KB) beside dU's three parts (32 KB), and two
+// groups of four warps taking alternate stages write them as the MN-major
+// 128-byte-swizzled tile the tensor core reads.  A stage is a chain (copy,
+// convert, multiply) and runs beside the dX GEMM on few SMs, so what counts is
+// how many are in flight: four copies and four converted tiles, one CTA per SM.
+// (Three and two with one group, two CTAs per SM, took 193 us for 16384 tokens
+// of 4096 features on 64 CTAs.)  The rings are even, so a slot's earlier stages are
 // the same group's and its parity waits cannot run a phase ahead.
 // Summed as DU and DB are (skinny.cu): two accumulators of eight stages each
 // in turn, joined in registers.
 struct ActDaPlan {
-  static constexpr uint32_t kA = 16384;    // dU hi/lo: 64 tokens x 128 columns
+  static constexpr uint32_t kA = 16384;    // dU hi/lo: 64 tokens x 128 columns; its third parts the same
   static constexpr uint32_t kRaw = 8192;   // codes: 64 tokens x 128 features
-  static constexpr uint32_t kCopy = kA + kRaw;
-  static constexpr uint32_t kCopies = 6;
+  static constexpr uint32_t kCopy = 2 * kA + kRaw;
+  static constexpr uint32_t kCopies = 4;
   static constexpr uint32_t kB = 16384;    // converted: 64 tokens x 128 features
   static constexpr uint32_t kTiles = 4;
   static constexpr uint32_t kTileOff = kCopies * kCopy;
@@ -173,7 +173,8 @@ struct ActDaPlan {
 constexpr int kActDaThreads = 320;  // copy warp, MMA warp, 2 x 4 converting warps
 
 __global__ void __launch_bounds__(kActDaThreads, 1)
-    act8_da_kernel(const __grid_constant__ CUtensorMap tm_du, const __grid_constant__ CUtensorMap tm_x,
+    act8_da_kernel(const __grid_constant__ CUtensorMap tm_du, const __grid_constant__ CUtensorMap tm_du3,
+                   const __grid_constant__ CUtensorMap tm_x,
                    const uint8_t* __restrict__ exps, const SkinnyArgs a) {
   using P = ActDaPlan;
   extern __shared__ uint8_t smem_raw[];
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(kActDaThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_du);
+    tma_prefetch_desc(&tm_du3);
     tma_prefetch_desc(&tm_x);
   }
   if (warp == 1) {
@@ -228,8 +230,10 @@ __global__ void __launch_bounds__(kActDaThreads, 1)
   tc_fence_after();
   const uint32_t tmem_d = *tmem_slot;
   const WaitCtx wc{abort_flag, a.status};
-  grid_dependency_wait();
-  grid_dependents_launch();
+  // The kernel launched just before this one (dB) writes nothing that is read
+  // here, and it let this one launch after everything older (dU, the
+  // checkpoint) had completed: dA runs beside dB, and passes the wait at its
+  // end, before it lets the next kernel launch.
 
   if (warp == 0) {
     if (lane == 0) {
@@ -239,10 +243,12 @@ __global__ void __launch_bounds__(kActDaThreads, 1)
         if (t >= static_cast<int>(P::kCopies) && !mbar_wait(&empty[s], (u - 1) & 1, wc)) break;
         uint8_t* st = smem + s * P::kCopy;
         const int m0 = (st0 + t) * 64;
-        mbar_arrive_expect_tx(&full[s], (wide ? 16384u : 8192u) + P::kRaw);
-        tma_load_2d(st + P::kA, &tm_x, &full[s], row0, m0);
+        mbar_arrive_expect_tx(&full[s], (wide ? 32768u : 16384u) + P::kRaw);
+        tma_load_2d(st + 2 * P::kA, &tm_x, &full[s], row0, m0);
         tma_load_2d(st, &tm_du, &full[s], ucol, m0);
         if (wide) tma_load_2d(st + 8192, &tm_du, &full[s], ucol + 64, m0);
+        tma_load_2d(st + P::kA, &tm_du3, &full[s], ucol, m0);
+        if (wide) tma_load_2d(st + P::kA + 8192, &tm_du3, &full[s], ucol + 64, m0);
         issued = t + 1;
       }
       for (int t = max(0, issued - static_cast<int>(P::kCopies)); t < issued; ++t)
@@ -262,11 +268,15 @@ __global__ void __launch_bounds__(kActDaThreads, 1)
       tc_fence_after();
       const uint64_t ad = sdesc_sw128(smem_u32(smem + s * P::kCopy), 8192, 1024);
       const uint64_t bd = sdesc_sw128(smem_u32(smem + P::kTileOff + b * P::kB), 8192, 1024);
+      const uint64_t ad3 = sdesc_sw128(smem_u32(smem + s * P::kCopy + P::kA), 8192, 1024);
       if (elect_one()) {
 #pragma unroll
-        for (uint32_t kk = 0; kk < 4; ++kk)  // 16 tokens = 16 rows of 128 bytes
-          umma_bf16(tmem_d + buf * 128, ad + kk * (2048u >> 4), bd + kk * (2048u >> 4), idesc,
-                    (t % P::kSumStages | kk) != 0 ? 1u : 0u);
+        for (uint32_t kk = 0; kk < 4; ++kk) {  // 16 tokens = 16 rows of 128 bytes
+          const uint32_t more = (t % P::kSumStages | kk) != 0 ? 1u : 0u;
+          umma_bf16(tmem_d + buf * 128, ad + kk * (2048u >> 4), bd + kk * (2048u >> 4), idesc, more);
+          // third parts onto the second ones' rows (zero in the first ones')
+          umma_bf16(tmem_d + buf * 128, ad3 + kk * (2048u >> 4), bd + kk * (2048u >> 4), idesc, 1u);
+        }
         umma_commit(&empty[s]);
         umma_commit(&bempty[b]);
         if (t % P::kSumStages == P::kSumStages - 1 || t == T - 1) umma_commit(&accf[buf]);
@@ -297,8 +307,8 @@ __global__ void __launch_bounds__(kActDaThreads, 1)
         pe[i] = (t < T && kok && m < a.M) ? __ldg(exps + m * kbpr + kb) : 0u;  // outside: codes are zero-filled
       }
     };
-    // TMEM row c = 32 q + lane holds part (lane / 16) of j = 16 q + lane % 16.
-    // The groups join 64 columns each; lanes 0-15 keep the first 32 of them,
+    // TMEM row c = 32 q + lane holds part (lane / 16) of j = 16 q + lane % 16
+    // (the second with the third).  The groups join 64 columns each; lanes 0-15 keep the first 32 of them,
     // lanes 16-31 the rest.
     const int q = warp & 3;
     float sum[32] = {};
@@ -315,7 +325,7 @@ __global__ void __launch_bounds__(kActDaThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float x = __uint_as_float(v[i]);
-          const float both = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));  // hi + lo
+          const float both = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
           if ((lane >= 16) == (cb == 1)) sum[i] = __fadd_rn(sum[i], both);
         }
       }
@@ -339,7 +349,7 @@ __global__ void __launch_bounds__(kActDaThreads, 1)
         ok = false;
         break;
       }
-      const uint8_t* raw = smem + s * P::kCopy + P::kA;
+      const uint8_t* raw = smem + s * P::kCopy + 2 * P::kA;
       uint8_t* tile = smem + P::kTileOff + b * P::kB + (cu >> 2) * 8192;  // 64-feature atom
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -408,6 +418,8 @@ __global__ void __launch_bounds__(kActDaThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_d, 256);
   }
+  grid_dependency_wait();
+  grid_dependents_launch();
 }
 
 }  // namespace
@@ -431,16 +443,16 @@ cudaError_t launch_act8_dequantize(const uint8_t* codes, const uint8_t* exps, in
                        dim3(1, 1, 1), codes, exps, units, K / 16, K, x, ldx);
 }
 
-cudaError_t launch_act8_da(const CUtensorMap& tm_du, const CUtensorMap& tm_x, const uint8_t* exps,
-                           const SkinnyArgs& a, int grid_rows, int splits, cudaStream_t stream) {
+cudaError_t launch_act8_da(const CUtensorMap& tm_du, const CUtensorMap& tm_du3, const CUtensorMap& tm_x,
+                           const uint8_t* exps, const SkinnyArgs& a, int grid_rows, int splits, cudaStream_t stream) {
   static uint64_t done = 0;
   if (cudaError_t e = allow_smem(act8_da_kernel, ActDaPlan::kSmem, done)) return e;
   if (splits < 1 || splits > 8) return cudaErrorInvalidValue;
   // unsplit products as clusters of two tiles, as in skinny.cu: they run
   // beside a CTA-pair GEMM and then sit on both SMs of a TPC
   const dim3 cluster = (splits == 1 && grid_rows % 2 == 0) ? dim3(2, 1, 1) : dim3(1, static_cast<unsigned>(splits), 1);
-  return launch_kernel(act8_da_kernel, dim3(grid_rows, splits, 1), dim3(kActDaThreads), ActDaPlan::kSmem, stream, cluster, tm_du,
-                       tm_x, exps, a);
+  return launch_kernel(act8_da_kernel, dim3(grid_rows, splits, 1), dim3(kActDaThreads), ActDaPlan::kSmem, stream, cluster,
+                       tm_du, tm_du3, tm_x, exps, a);
 }
 
 }  // namespace qnf4

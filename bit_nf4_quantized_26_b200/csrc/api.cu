@@ -924,15 +924,20 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
   const int G = grp.G;
   const int ra = G * r;
   const BwdPlan p = plan_bwd(M, N, K, r, G, grp.n_max);
-  const size_t need = p.total + (drop ? align256(static_cast<size_t>(M) * K * 4) : 0);
+  // An 8-bit input's pass has third parts of s U (its rows are twice as long)
+  // and dU beyond the plain workspace, and the dropout's fp32 dX after those.
+  const bool summed = !X.x;
+  const size_t third = summed ? align256(static_cast<size_t>(M) * 2 * ra * 2) : 0;
+  const size_t need = p.total + 2 * third + (drop ? align256(static_cast<size_t>(M) * K * 4) : 0);
   if (!ws || ws_bytes < need) return QLORA_ERR_WORKSPACE;
   if (!aligned16(ws)) return QLORA_ERR_ALIGN;
   if (qlora_status st = check_device()) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint8_t* wsb = static_cast<uint8_t*>(ws);
-  uint16_t* sucat = reinterpret_cast<uint16_t*>(wsb + p.off_sucat);
   uint16_t* ducat = reinterpret_cast<uint16_t*>(wsb + p.off_ducat);
-  float* dx32 = drop ? reinterpret_cast<float*>(wsb + p.total) : nullptr;
+  uint16_t* sucat = reinterpret_cast<uint16_t*>(wsb + (summed ? p.total : p.off_sucat));
+  uint16_t* ducat3 = reinterpret_cast<uint16_t*>(wsb + p.off_sucat);  // summed: sucat is elsewhere
+  float* dx32 = drop ? reinterpret_cast<float*>(wsb + p.total + 2 * third) : nullptr;
   void* dx_gemm = drop ? static_cast<void*>(dx32) : dX;           // where the GEMM writes
   const int gemm_f32 = drop ? 1 : (dx_dtype == QLORA_DTYPE_F32);
   const int gemm_r = drop ? 0 : ra;                               // adapter stages in the GEMM (all members)
@@ -964,10 +969,11 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
   sa.out_cat = ducat;
   sa.in_u = U;
   sa.out_cat2 = sucat;
+  sa.out_cat3 = summed ? ducat3 : nullptr;
   {
     ProfScope ps(kKDU, cs);
     if (qlora_status st =
-            from_cuda(launch_skinny(kSkDU, mdy128, mbl, sa, static_cast<int>(cdiv(M, 128)) * Gs, p.s_du, cs, !X.x)))
+            from_cuda(launch_skinny(kSkDU, mdy128, mbl, sa, static_cast<int>(cdiv(M, 128)) * Gs, p.s_du, cs, summed)))
       return st;
   }
 
@@ -1043,9 +1049,11 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
 
   // dB = s dY^T U per member (contraction over M split over a cluster)
   CUtensorMap mdy64, msu;
-  if (!map_bf16(&mdy64, dY, M, N, 64, 64) || !map_bf16(&msu, sucat, M, 2 * ra, 64, 64)) return QLORA_ERR_CUDA;
-  sa.stages_total = static_cast<int>(cdiv(M, 64));
-  sa.stages_per_split = p.per_db;
+  const int depth = summed ? 32 : 64;  // tokens per stage
+  if (!map_bf16(&mdy64, dY, M, N, 64, depth) || !map_bf16(&msu, sucat, M, (summed ? 4 : 2) * ra, 64, depth))
+    return QLORA_ERR_CUDA;
+  sa.stages_total = static_cast<int>(cdiv(M, depth));
+  sa.stages_per_split = p.per_db * (64 / depth);
   sa.s = 1.0f;
   sa.out_f32 = dB;
   sa.out_cat = nullptr;
@@ -1055,13 +1063,13 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
     ProfScope ps(kKDB, side);
     if (qlora_status st =
             from_cuda(launch_skinny(kSkDB, mdy64, msu, sa, static_cast<int>(cdiv(N, 128)) * (chunks ? Gs : 1), p.s_db,
-                                    side, !X.x)))
+                                    side, summed)))
       return st;
   }
 
   // dA = dU^T X per member (contraction over M split over a cluster)
-  CUtensorMap mduc, mx;
-  if (!map_bf16(&mduc, ducat, M, 2 * ra, 64, 64) ||
+  CUtensorMap mduc, mduc3, mx;
+  if (!map_bf16(&mduc, ducat, M, 2 * ra, 64, 64) || !map_bf16(&mduc3, ducat3, M, 2 * ra, 64, 64) ||
       !(X.x ? map_bf16(&mx, X.x, M, K, 64, 64) : map_u8(&mx, X.codes, M, K, 128, 64)))
     return QLORA_ERR_CUDA;
   {
@@ -1074,7 +1082,7 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
     const int rows = static_cast<int>(cdiv(K, 128)) * Gs;
     ProfScope ps(X.x ? kKDA : kKActDA, side);
     if (qlora_status st = from_cuda(X.x ? launch_skinny(kSkDA, mduc, mx, da, rows, p.s_da, side)
-                                        : launch_act8_da(mduc, mx, X.exps, da, rows, p.s_da, side)))
+                                        : launch_act8_da(mduc, mduc3, mx, X.exps, da, rows, p.s_da, side)))
       return st;
   }
 
@@ -1287,6 +1295,12 @@ qlora_status act8_dequantize(const uint8_t* codes, const uint8_t* exps, int64_t 
   if (qlora_status st = check_device()) return st;
   ProfScope ps(kKActDequantize, static_cast<cudaStream_t>(stream));
   return from_cuda(launch_act8_dequantize(codes, exps, M, K, X, ldx, static_cast<cudaStream_t>(stream)));
+}
+
+size_t qlora_bwd_act8_workspace_size(int64_t M, int64_t N, int64_t K, int32_t members, int32_t r, int32_t dropout) {
+  if (M <= 0 || N <= 0 || K <= 0 || r <= 0 || members < 1 || members > 4) return 0;
+  return plan_bwd(M, N, K, r, members, N).total + 2 * align256(static_cast<size_t>(M) * 2 * members * r * 2) +
+         (dropout ? align256(static_cast<size_t>(M) * K * 4) : 0);
 }
 
 qlora_status qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* codes, const uint8_t* exps, const float* U,

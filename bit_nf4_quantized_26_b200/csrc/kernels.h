@@ -98,7 +98,8 @@ struct SkinnyArgs {
   float* out_f32;       // DOWN: U [M, G r]; DB: dB [N, r]; DA: dA [G r, K]
   uint16_t* out_cat;    // DOWN: hi/lo of s*U [M, 2 G r]; DU: hi/lo of dU [M, 2 G r]
   const float* in_u;    // DU: the saved U [M, G r]
-  uint16_t* out_cat2;   // DU: hi/lo of s*U [M, 2 G r] (the dB operand)
+  uint16_t* out_cat2;   // DU: hi/lo of s*U [M, 2 G r] (the dB operand); summed: [M, 4 G r], third parts behind
+  uint16_t* out_cat3;   // DU, summed: third parts of dU [M, 2 G r] in the same layout (see skinny.cu)
   int32_t* status;
   int groups;           // G (1..4)
   int grp_n[5];         // member offsets along N (grp_n[0] = 0, grp_n[G] = N)

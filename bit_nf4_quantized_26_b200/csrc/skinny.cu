@@ -24,13 +24,18 @@
 namespace qnf4 {
 
 // Shared-memory ring per mode: about 97 KB, so two CTAs fit on an SM (each
-// with three or four 24-32 KB stages in flight).
-template <int MODE>
+// with three or four 24-32 KB stages in flight).  The summed DB, with a third
+// part of its operand, takes stages of 32 tokens.
+template <int MODE, bool SUMMED>
 struct SkPlan {
-  static constexpr uint32_t kA = 16384;
-  static constexpr uint32_t kB = (MODE == kSkDA || MODE == kSkDB) ? 16384 : 8192;
-  static constexpr uint32_t kStage = kA + kB;
-  static constexpr uint32_t kStages = (MODE == kSkDA || MODE == kSkDB) ? 3 : 4;
+  static constexpr bool kThird = SUMMED && MODE == kSkDB;
+  static constexpr int kDepth = kThird ? 32 : 64;              // of a stage's contraction
+  static constexpr uint32_t kAtom = kDepth * 128;              // DA, DB: 64 columns of a stage
+  static constexpr uint32_t kA = (MODE == kSkDA || MODE == kSkDB) ? 2 * kAtom : 16384;
+  static constexpr uint32_t kB = (MODE == kSkDA || MODE == kSkDB) ? 2 * kAtom : 8192;
+  static constexpr uint32_t kStage = kA + kB + (kThird ? kB : 0);
+  static constexpr uint32_t kStages = (MODE == kSkDA || (MODE == kSkDB && !kThird)) ? 3 : 4;
+  static constexpr int kSumStages = 512 / kDepth;              // per accumulator of a summed form
   static constexpr uint32_t kCtasPerSm = 2;
   static constexpr uint32_t kBarOff = kStages * kStage;
   static constexpr uint32_t kSmem = 1024 + kBarOff + 256;
@@ -47,6 +52,16 @@ struct SkPlan {
 
 __device__ __forceinline__ int hilo_col(int j) { return 32 * (j >> 4) + (j & 15); }
 
+// What the pair of store_hilo leaves of v, rounded to bf16 (24 bits in all), in
+// the same layout: at the second part's column, and zero at the first's, so
+// that it is summed onto the second part's product.
+__device__ __forceinline__ void store_third(uint16_t* cat, int m, int ld, int col0, int j, float v) {
+  const float rest = __fsub_rn(v, bf16_bits_to_float(bf16_bits(v)));  // both differences are exact
+  uint16_t* row = cat + static_cast<int64_t>(m) * ld + col0;
+  row[hilo_col(j)] = 0;
+  row[hilo_col(j) + 16] = bf16_bits(__fsub_rn(rest, bf16_bits_to_float(bf16_bits(rest))));
+}
+
 // v -> (bf16(v), bf16(v - bf16(v))) at the interleaved hi/lo columns of row m
 // (row stride `ld` elements; the member's columns start at `col0`).
 __device__ __forceinline__ void store_hilo(uint16_t* cat, int m, int ld, int col0, int j, float v) {
@@ -57,13 +72,11 @@ __device__ __forceinline__ void store_hilo(uint16_t* cat, int m, int ld, int col
   row[hilo_col(j) + 16] = lo;
 }
 
-constexpr int kSumStages = 8;  // stages per accumulator of a summed form
-
 template <int MODE, bool SUMMED>
-__global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
+__global__ void __launch_bounds__(192, (SkPlan<MODE, SUMMED>::kCtasPerSm))
     skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const SkinnyArgs a) {
-  using P = SkPlan<MODE>;
+  using P = SkPlan<MODE, SUMMED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBarOff);
@@ -73,6 +86,7 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + (SUMMED ? 5 : 1));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   constexpr uint32_t kTmemCols = (SUMMED ? 2 : 1) * P::kTmemCols;
+  constexpr int kSumStages = P::kSumStages;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Tile origin: DOWN/DU rows are tokens, DB rows are output features, DA's
@@ -148,11 +162,16 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
           tma_load_2d(sb, &tmB, &full[s], a.chunks ? g * a.r : 0, nbase + kt * 64);  // and rows of B
         } else if (MODE == kSkDB) {
           const bool a2 = row0 + 64 < a.N;
-          mbar_arrive_expect_tx(&full[s], 8192u * ((a2 ? 2 : 1) + nc / 64));
-          tma_load_2d(sa, &tmA, &full[s], row0, kt * 64);
-          if (a2) tma_load_2d(sa + 8192, &tmA, &full[s], row0 + 64, kt * 64);
-          tma_load_2d(sb, &tmB, &full[s], ucol, kt * 64);
-          if (nc == 128) tma_load_2d(sb + 8192, &tmB, &full[s], ucol + 64, kt * 64);
+          const int m0 = kt * P::kDepth;
+          mbar_arrive_expect_tx(&full[s], P::kAtom * ((a2 ? 2 : 1) + (P::kThird ? 2 : 1) * nc / 64));
+          tma_load_2d(sa, &tmA, &full[s], row0, m0);
+          if (a2) tma_load_2d(sa + P::kAtom, &tmA, &full[s], row0 + 64, m0);
+          tma_load_2d(sb, &tmB, &full[s], ucol, m0);
+          if (nc == 128) tma_load_2d(sb + P::kAtom, &tmB, &full[s], ucol + 64, m0);
+          if (P::kThird) {  // columns 2 ra .. of the same rows
+            tma_load_2d(sb + P::kB, &tmB, &full[s], 2 * ra + ucol, m0);
+            if (nc == 128) tma_load_2d(sb + P::kB + P::kAtom, &tmB, &full[s], 2 * ra + ucol + 64, m0);
+          }
         } else {  // DA
           int nb = 0;
           for (int i = 0; i < 2; ++i) nb += (row0 + 64 * i < a.K) ? 1 : 0;
@@ -166,6 +185,45 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
       for (int t = max(0, issued - static_cast<int>(P::kStages)); t < issued; ++t)
         mbar_drain(&full[t % P::kStages], (t / P::kStages) & 1, a.status);
     }
+  } else if (SUMMED && warp == 1) {
+    // The whole warp runs the loop and an elected lane issues, as in the GEMMs
+    // (issued from a divergent lane each MMA takes about 90 cycles).
+    const bool a_mn = MODE == kSkDB;
+    const uint32_t idesc = idesc_bf16_f32(128, MODE == kSkDB ? nc : 64, a_mn ? 1 : 0, 1);
+    const uint32_t a_step = a_mn ? (2048u >> 4) : (32u >> 4);
+    bool ok = true;
+    for (int t = 0; ok && t < T; ++t) {
+      const uint32_t s = t % P::kStages, u = t / P::kStages;
+      const int ch = t / kSumStages, buf = ch & 1;
+      ok = (t % kSumStages != 0 || ch < 2 || mbar_wait_all(&acce[buf], ((ch >> 1) - 1) & 1, wc)) &&
+           mbar_wait_all(&full[s], u & 1, wc);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sa = smem_u32(smem + s * P::kStage), sb = sa + P::kA;
+      const uint32_t d = tmem_d + buf * P::kTmemCols;
+      const uint64_t adesc = a_mn ? sdesc_sw128(sa, P::kAtom, 1024) : sdesc_sw128(sa, 16, 1024);
+      const uint64_t bdesc = sdesc_sw128(sb, P::kAtom, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (uint32_t kk = 0; kk < P::kDepth / 16; ++kk)
+          umma_bf16(d, adesc + kk * a_step, bdesc + kk * (2048u >> 4), idesc,
+                    (t % kSumStages | kk) != 0 ? 1u : 0u);
+        if (P::kThird) {  // onto the second parts' columns (the first parts' are zero)
+          const uint64_t cdesc = sdesc_sw128(sb + P::kB, P::kAtom, 1024);
+#pragma unroll
+          for (uint32_t kk = 0; kk < P::kDepth / 16; ++kk)
+            umma_bf16(d, adesc + kk * a_step, cdesc + kk * (2048u >> 4), idesc, 1u);
+        }
+        umma_commit(&empty[s]);
+        if (t % kSumStages == kSumStages - 1 || t == T - 1) umma_commit(&accf[buf]);
+      }
+      __syncwarp();
+    }
+    if (!ok && elect_one()) {  // wait for what is in flight
+      umma_commit(acce + 2);
+      mbar_drain(acce + 2, 0, a.status);
+    }
+    __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
       const bool a_mn = (MODE == kSkDB || MODE == kSkDA);
@@ -177,11 +235,6 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
       bool aborted = false;
       for (int t = 0; t < T; ++t) {
         const uint32_t s = t % P::kStages, u = t / P::kStages;
-        const int ch = t / kSumStages, buf = SUMMED ? ch & 1 : 0;
-        if (SUMMED && t % kSumStages == 0 && ch >= 2 && !mbar_wait(&acce[buf], ((ch >> 1) - 1) & 1, wc)) {
-          aborted = true;
-          break;
-        }
         if (!mbar_wait(&full[s], u & 1, wc)) { aborted = true; break; }
         tc_fence_after();
         const uint32_t sa = smem_u32(smem + s * P::kStage), sb = sa + P::kA;
@@ -189,19 +242,11 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
         const uint64_t bdesc = b_mn ? sdesc_sw128(sb, 8192, 1024) : sdesc_sw128(sb, 16, 1024);
 #pragma unroll
         for (uint32_t kk = 0; kk < 4; ++kk)
-          umma_bf16(tmem_d + buf * P::kTmemCols, adesc + kk * a_step, bdesc + kk * b_step, idesc,
-                    ((SUMMED ? t % kSumStages : t) | kk) != 0 ? 1u : 0u);
+          umma_bf16(tmem_d, adesc + kk * a_step, bdesc + kk * b_step, idesc, (t | kk) != 0 ? 1u : 0u);
         umma_commit(&empty[s]);
-        if (SUMMED && (t % kSumStages == kSumStages - 1 || t == T - 1)) umma_commit(&accf[buf]);
       }
-      if (!SUMMED) {
-        umma_commit(accf);
-        if (aborted) mbar_drain(accf, 0, a.status);
-      } else if (aborted) {  // the MMAs in flight end with the stages' own commits; wait for the last
-        uint64_t* last = acce + 2;
-        umma_commit(last);
-        mbar_drain(last, 0, a.status);
-      }
+      umma_commit(accf);
+      if (aborted) mbar_drain(accf, 0, a.status);
     }
   } else {
     // ------------------------------------------------ TMEM -> own partial tile
@@ -347,13 +392,21 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
             *reinterpret_cast<float4*>(a.out_f32 + static_cast<int64_t>(m) * ra + g * a.r + col) = acc;
 #pragma unroll
           for (int i = 0; i < 4; ++i) store_hilo(a.out_cat, m, 2 * ra, ucol, col + i, __fmul_rn(a.s, vals[i]));
+          if (SUMMED && MODE == kSkDU) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store_third(a.out_cat3, m, 2 * ra, ucol, col + i, __fmul_rn(a.s, vals[i]));
+          }
           if (MODE == kSkDU) {
             // The same rows of the saved U, as the bf16 hi/lo of s*U for dB.
             const float4 uv =
                 __ldg(reinterpret_cast<const float4*>(a.in_u + static_cast<int64_t>(m) * ra + g * a.r + col));
             const float us[4] = {uv.x, uv.y, uv.z, uv.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) store_hilo(a.out_cat2, m, 2 * ra, ucol, col + i, __fmul_rn(a.s, us[i]));
+            for (int i = 0; i < 4; ++i) {
+              // summed: rows of 4 ra columns, the third parts behind the pairs
+              store_hilo(a.out_cat2, m, (SUMMED ? 4 : 2) * ra, ucol, col + i, __fmul_rn(a.s, us[i]));
+              if (SUMMED) store_third(a.out_cat2, m, 4 * ra, 2 * ra + ucol, col + i, __fmul_rn(a.s, us[i]));
+            }
           }
         }
       } else if (MODE == kSkDB) {
@@ -383,7 +436,7 @@ __global__ void __launch_bounds__(192, SkPlan<MODE>::kCtasPerSm)
 template <int MODE, bool SUMMED = false>
 static cudaError_t launch_skinny_impl(const CUtensorMap& tmA, const CUtensorMap& tmB, const SkinnyArgs& a,
                                       int grid_rows, int splits, cudaStream_t stream) {
-  using P = SkPlan<MODE>;
+  using P = SkPlan<MODE, SUMMED>;
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(skinny_kernel<MODE, SUMMED>, cudaFuncAttributeMaxDynamicSharedMemorySize,

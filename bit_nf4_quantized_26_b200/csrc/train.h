@@ -31,9 +31,10 @@ cudaError_t launch_act8_dequantize(const uint8_t* codes, const uint8_t* exps, in
 
 // dA[j, k] = sum_m dU[m, j] X'[m, k] from the checkpoint (SkinnyArgs as for
 // mode DA of skinny.cu): tm_du the bf16 hi/lo of dU [M, 2 ra] box {64, 64}
-// SW128, tm_x the codes [M, K] u8 box {128, 64}; exps [M, K / 64].
-cudaError_t launch_act8_da(const CUtensorMap& tm_du, const CUtensorMap& tm_x, const uint8_t* exps,
-                           const SkinnyArgs& a, int grid_rows, int splits, cudaStream_t stream);
+// SW128, tm_du3 its third parts the same, tm_x the codes [M, K] u8 box {128,
+// 64}; exps [M, K / 64].
+cudaError_t launch_act8_da(const CUtensorMap& tm_du, const CUtensorMap& tm_du3, const CUtensorMap& tm_x,
+                           const uint8_t* exps, const SkinnyArgs& a, int grid_rows, int splits, cudaStream_t stream);
 
 // ------------------------------------------------------------- head_loss.cu
 

@@ -63,11 +63,17 @@ QLORA_API qlora_status act8_dequantize(const uint8_t* codes, const uint8_t* exps
  * The backward passes of qlora_nf4.h with the adapter's input given as its
  * 8-bit checkpoint (of X; for the dropout form, of X_drop, whose zeros stay
  * zeros): dA = dU^T X', everything else by the same formulas.  The rank-r
- * products (dU, dB, dA) join their accumulator's sums every 512 terms in fp32
- * with rounding to nearest: dA and dB within 1e-5 relative Frobenius error,
- * whatever the number of tokens.  Arguments, constraints, workspaces and errors
- * as for qlora_linear_bwd, qlora_group_bwd and qlora_linear_bwd_dropout.
+ * products (dU, dB, dA) take dU and s U as three bf16 parts (24 bits) and join
+ * their accumulator's sums every 512 terms in fp32 with rounding to nearest: dA
+ * and dB within 4e-6 relative Frobenius error, whatever the number of tokens.
+ * Arguments, constraints and errors as for qlora_linear_bwd, qlora_group_bwd
+ * and qlora_linear_bwd_dropout; the workspace is
+ * qlora_bwd_act8_workspace_size(M, N, K, members, r, dropout) bytes (members 1
+ * for a single linear; dropout nonzero for the dropout form): the plain pass's
+ * and 8 M members r more.
  */
+QLORA_API size_t qlora_bwd_act8_workspace_size(int64_t M, int64_t N, int64_t K, int32_t members, int32_t r,
+                                               int32_t dropout);
 QLORA_API qlora_status qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* codes, const uint8_t* exps,
                                              const float* U, int64_t M, nf4_weight W, const uint16_t* A,
                                              const uint16_t* B, int32_t r, float s, void* dX, int32_t dx_dtype,

@@ -19,7 +19,7 @@ FAKE = 1 << 20  # a 16-byte aligned non-null value; never dereferenced
 def test_header_declarations_are_exported():
     text = open(os.path.join(ROOT, "include", "qlora_train.h")).read()
     names = sorted(set(re.findall(r"QLORA_API\s+[\w\s\*]+?\b(\w+)\s*\(", text)))
-    assert sorted(q.EXPORTED_TRAIN) == names and len(names) == 9
+    assert sorted(q.EXPORTED_TRAIN) == names and len(names) == 10
     for n in names:
         assert hasattr(q.raw(), n), n
 
@@ -74,6 +74,15 @@ def test_bwd_act8_refusals_are_the_backwards():
 
     assert drop(1.0) == SHAPE and drop(-0.5) == SHAPE and drop(float("nan")) == SHAPE
     assert drop(0.5, codes=None) == NULL and drop(0.5) == WS
+
+
+def test_bwd_act8_workspace_size():
+    f, g = q.qlora_bwd_act8_workspace_size, q.qlora_group_bwd_workspace_size
+    assert f(0, 4096, 4096, 1, 64) == 0 and f(64, 4096, 4096, 0, 64) == 0 and f(64, 4096, 4096, 5, 64) == 0
+    assert f(4096, 4096, 4096, 1, 64) == q.qlora_bwd_workspace_size(4096, 4096, 4096, 64) + 8 * 4096 * 64
+    assert f(1000, 8192, 512, 2, 16) <= g(1000, 8192, 512, 2, 16) + 8 * 1000 * 2 * 16 + 512
+    assert f(64, 512, 256, 1, 16, True) == f(64, 512, 256, 1, 16) + 64 * 256 * 4
+    assert _bwd(wsb=f(64, 4096, 4096, 1, 64) - 1) == WS
 
 
 def _h(w=FAKE, ld=512, V=1000, D=512, codes=None, c8=None, s2=None, mean=None):

@@ -39,7 +39,7 @@ class Step:
         self.loss, self.lse, self.stats, self.dY = e(M), e(M), e(2), e(M, D, dt=b16)
         self.dX, self.dA, self.dB = e(M, K, dt=b16), e(r, K), e(D, r)
         self.status = torch.zeros(4, dtype=torch.int32, device="cuda")
-        size = max(q.qlora_fwd_workspace_size(M, D, K, r), q.qlora_bwd_workspace_size(M, D, K, r),
+        size = max(q.qlora_fwd_workspace_size(M, D, K, r), q.qlora_bwd_act8_workspace_size(M, D, K, 1, r),
                    q.qlora_head_loss_workspace_size(M, V, D, nf4, q.HEAD_STEP), 16)
         self.ws = e(size, dt=u8)
 
@@ -85,7 +85,7 @@ def test_chain_matches_oracle(M, K, D, V, r, nf4):
     dU = st.s * (dY @ B)
     x = q.act8_dequantize(st.x8).double()
     for got, want in ((out["dA"], dU.t() @ x), (out["dB"], st.s * (dY.t() @ out["U"].double()))):
-        assert float((got.double() - want).norm() / want.norm()) <= 1e-5
+        assert float((got.double() - want).norm() / want.norm()) <= 4e-6
     assert not out["dX"][st.y == -100].any()
     # what the 8-bit input costs dA: E4M3's half step, 2^-4 relative an element, averaged over the tokens
     full = dU.t() @ st.X.double()
