@@ -1010,7 +1010,10 @@ def run_case(args):
     --case fwd:M:N:K or bwd:M:N:K (r=64, alpha=16), quant:N:K / dequant:N:K (NF4
     quantisation / dequantisation of an N x K weight), cquant:N:K (the same with
     mean-centred double quantisation), adamw8:n (one 8-bit AdamW
-    step over n parameters), or layer:M (the decoder-layer step with M tokens);
+    step over n parameters), layer:M (the decoder-layer step with M tokens),
+    loss:T:V:D / lossgrad:T:V:D / lossstep:T:V:D (the loss head on T tokens, a
+    vocabulary of V and width D; with :nf4 behind, an NF4 head), act8:M:K (8-bit
+    checkpoint of M x K and back) or bwd8:M:N:K (bwd from such a checkpoint);
     --steps calls after 2 warm-up calls.
     """
     import torch
@@ -1067,13 +1070,46 @@ def run_case(args):
         torch.cuda.synchronize()
         print(json.dumps({"case": args.case, "ok": True}))
         return
+    if args.case.startswith("loss"):
+        kind, T, V, D = args.case.split(":")[:4]
+        T, V, D = int(T), int(V), int(D)
+        gen = torch.Generator(device="cuda").manual_seed(7)
+        H = torch.randn(T, D, generator=gen, device="cuda").to(torch.bfloat16)
+        head = synth.weight_bf16(V, D, seed=2, device="cuda")
+        if args.case.endswith(":nf4"):
+            head = lib.quantize_weight(head)
+        labels = torch.randint(0, V, (T,), generator=gen, device="cuda")
+        lse = lib.qlora_head_loss_fwd(H, head, labels)[1] if kind == "lossgrad" else None
+        dloss = torch.full((T,), 1.0 / T, device="cuda")
+        for _ in range(2 + args.steps):
+            if kind == "loss":
+                lib.qlora_head_loss_fwd(H, head, labels)
+            elif kind == "lossgrad":
+                lib.qlora_head_loss_bwd(H, head, labels, lse, dloss)
+            else:
+                lib.qlora_head_loss_step(H, head, labels)
+        torch.cuda.synchronize()
+        print(json.dumps({"case": args.case, "ok": True}))
+        return
+    if args.case.startswith("act8:"):
+        _, M, K = args.case.split(":")
+        gen = torch.Generator(device="cuda").manual_seed(8)
+        X = torch.randn(int(M), int(K), generator=gen, device="cuda").to(torch.bfloat16)
+        for _ in range(2 + args.steps):
+            lib.act8_dequantize(lib.act8_quantize(X))
+        torch.cuda.synchronize()
+        print(json.dumps({"case": args.case, "ok": True}))
+        return
     kind, M, N, K = args.case.split(":")
     M, N, K, r = int(M), int(N), int(K), 64
     d = {k: v.cuda() for k, v in synth.linear_inputs(synth.Linear("case", N, K), M, r, 0).items()}
     W = lib.quantize_weight(d["W"])
     Y, U = lib.qlora_linear_fwd(d["X"], W, d["A"], d["B"], 0.25)
+    x8 = lib.act8_quantize(d["X"]) if kind == "bwd8" else None
     for _ in range(2 + args.steps):
-        if kind == "fwd":
+        if kind == "bwd8":
+            lib.qlora_linear_bwd_act8(d["dY"], x8, U, W, d["A"], d["B"], 0.25)
+        elif kind == "fwd":
             lib.qlora_linear_fwd(d["X"], W, d["A"], d["B"], 0.25, Y=Y, U=U)
         else:
             lib.qlora_linear_bwd(d["dY"], d["X"], U, W, d["A"], d["B"], 0.25)
@@ -1094,7 +1130,8 @@ def main():
     ap.add_argument("--kernels-only", action="store_true",
                     help="only the timed steps (for profiler captures): no e2e, no extras, no CPU baseline")
     ap.add_argument("--case", default=None,
-                    help="profiler driver: fwd:M:N:K, bwd:M:N:K, quant:N:K, cquant:N:K, dequant:N:K, adamw8:n or layer:M")
+                    help="profiler driver: fwd:M:N:K, bwd:M:N:K, quant:N:K, cquant:N:K, dequant:N:K, adamw8:n, layer:M, "
+                         "loss:T:V:D[:nf4], lossgrad:T:V:D[:nf4], lossstep:T:V:D[:nf4], act8:M:K or bwd8:M:N:K")
     args = ap.parse_args()
     if args.case:
         run_case(args)
