@@ -603,6 +603,8 @@ def _run(dev, stream, call):
             return _run(dev, stream, call)
     if stream is None:
         return call(torch._C._cuda_getCurrentRawStream(dev.index))
+    if stream.device != dev:
+        _refuse(ERR_SHAPE, "stream", f"is on {stream.device}, the tensors on {dev}")
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 
@@ -652,6 +654,17 @@ def _word(status, dev, where):
     if status.dtype != torch.int32 or status.numel() < 1 or status.device != dev:
         _refuse(ERR_DTYPE, where, "status is not an int32 word on the call's device")
     return status.data_ptr()
+
+
+def _nf4(W, dev, where, name):
+    """An NF4 storage of the sizes its shape has, on this device."""
+    nc, nb, ns = nf4_sizes(int(W.n_out) * int(W.k_in))
+    for t, dtype, n in ((W.codes, torch.uint8, nc), (W.c8, torch.uint8, nb), (W.s2, torch.float32, ns)):
+        if t.dtype != dtype or t.numel() != n or t.device != dev or not t.is_contiguous():
+            _refuse(ERR_SHAPE, where, f"{name} is no NF4 storage of {int(W.n_out)} x {int(W.k_in)} on {dev}")
+    mean = getattr(W, "mean", None)
+    if mean is not None and (mean.dtype != torch.float32 or mean.numel() < 1 or mean.device != dev):
+        _refuse(ERR_SHAPE, where, f"{name}'s mean is no fp32 word on {dev}")
 
 
 def _workspace(ws, size, dev, where):
@@ -725,8 +738,7 @@ def _bwd_act8(where, dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, drop, ws, stat
     _tensor(U, torch.float32, (M, G * r), dev, where, "U")
     _tensor(A, torch.bfloat16, (G * r, K), dev, where, "A")
     _tensor(B, torch.bfloat16, (N, r), dev, where, "B")
-    if W.codes.device != dev:
-        _refuse(ERR_SHAPE, where, f"W is on {W.codes.device}, not {dev}")
+    _nf4(W, dev, where, "W")
 
     def call(st):
         x = _out(dX, (M, K), torch.float32 if dx_dtype == DTYPE_F32 else torch.bfloat16, dev, where, "dX")
@@ -816,8 +828,7 @@ def _head(head, dev, where):
         return _Head(head.data_ptr(), ld, None, None, None, None, V, D), V, D, False
     V, D = int(head.n_out), int(head.k_in)
     mean = getattr(head, "mean", None)
-    if head.codes.device != dev:
-        _refuse(ERR_SHAPE, where, f"head is on {head.codes.device}, not {dev}")
+    _nf4(head, dev, where, "head")
     return _Head(None, 0, head.codes.data_ptr(), head.c8.data_ptr(), head.s2.data_ptr(),
                  None if mean is None else mean.data_ptr(), V, D), V, D, True
 

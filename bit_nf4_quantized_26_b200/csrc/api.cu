@@ -1450,7 +1450,7 @@ static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, i
       p.off_acc = take(4 * static_cast<size_t>(p.splits * trows) * static_cast<size_t>(cdiv(D, tile) * tile));
   }
   if (nf4 && !p.codes) p.off_w = take(2 * static_cast<size_t>(std::min(p.piece, V)) * static_cast<size_t>(D));
-  p.total = off;
+  p.total = off + 256;  // the parts are laid out from a 256-byte boundary
   return p;
 }
 
@@ -1533,7 +1533,7 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
   if (!aligned16(ws)) return QLORA_ERR_ALIGN;
   if (qlora_status st = check_device()) return st;
 
-  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  uint8_t* wsb = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(ws)));
   auto at = [wsb](size_t off) { return wsb + off; };
   uint16_t* g = reinterpret_cast<uint16_t*>(at(p.off_g));
   uint16_t* wbuf = reinterpret_cast<uint16_t*>(at(p.off_w));

@@ -6,17 +6,16 @@
 //   l = H W^T    lse = log sum exp l    loss = lse - l[label]
 //   dH = g (exp(l - lse) - onehot) W
 //
-// The logits exist only as fp32 tiles in tensor memory.  One GEMM kernel
-// makes every product; what its epilogue does with a tile
-// is the mode:
+// The logits exist only as fp32 tiles in tensor memory.  One GEMM kernel makes
+// every product; what its epilogue does with a tile is the mode:
 //
 //   Loss  per row and half tile the maximum m and sum exp(l - m): 8 bytes
 //   Prob  exp(l - lse), less 1 at the label (in fp32), rounded to bf16
 //   Exp   exp(l - ref), 0 at the label, rounded to bf16, and (ref, sum): the
 //         gradient's operand before lse is known.  ref is 0 while the maximum
-//         of the row's half tile lies within +-40 (exp then stays far inside bf16's and
-//         fp32's range, and the reference costs no precision: both types
-//         float), else that maximum
+//         of the row's half tile lies within +-40 (exp then stays far inside
+//         bf16's and fp32's range, and the reference costs no precision: both
+//         types float), else that maximum
 //   Grad  (second product) the piece's bf16 [T, piece] operand times W's rows
 //         of the piece, added to the fp32 sum of the pieces before
 //
@@ -260,16 +259,17 @@ struct Ring {
 // drift of 6e-7) that alternate between two accumulators, and the epilogue
 // threads add each finished one to their registers, rounding to nearest, while
 // the next runs.  (512 deep costs the products 2-3%, 1024 nothing; 256 is free
-// for few tokens, whose products wait for W.)  Results rounded to bf16 take longer ones: the backward's probabilities 4096, dH a
-// whole slice of its contraction.
+// for few tokens, whose products wait for W.)  Results rounded to bf16 take
+// longer ones: the backward's probabilities 4096, dH a whole slice of its
+// contraction.
 //
 // Barriers (leader: the pair's first CTA, or the single one): full[s] (leader:
 // the stage's copies landed, and its dequantised tiles are written), empty[s]
 // (all: the stage's MMAs are done), cfull[s] (each: an NF4 stage's codes
-// landed), accf[b] (all: the chunk's accumulator is
-// final), acce[b] (leader: all epilogue warps have read it), done (leader: the
-// last commit).  What an earlier kernel of the same call wrote is read past L1
-// (__ldcg): launches overlap, and nothing is kept there from one to the next.
+// landed), accf[b] (all: the chunk's accumulator is final), acce[b] (leader: all
+// epilogue warps have read it), done (leader: the last commit).  What an earlier
+// kernel of the same call wrote is read past L1 (__ldcg): launches overlap, and
+// nothing is kept there from one to the next.
 template <int MODE, bool PAIR, bool NF4>
 __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,

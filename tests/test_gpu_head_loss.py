@@ -336,6 +336,21 @@ def test_gradient_in_place_of_the_hidden_states(T, V, D):
     assert torch.equal(dH, q.qlora_head_loss_bwd(h.cuda(), W, Y, want[1], g))
 
 
+@pytest.mark.parametrize("T,nf4", [(40, True), (200, False), (200, True)])
+def test_workspace_of_any_16_byte_alignment(T, nf4):
+    h, w, y = _case(T, 700, 128, seed=11)
+    H, Y, W = h.cuda(), y.cuda(), w.cuda()
+    W = q.quantize_weight(W) if nf4 else W
+    want = q.qlora_head_loss_step(H, W, Y)
+    n = q.qlora_head_loss_workspace_size(T, 700, 128, nf4, q.HEAD_STEP)
+    buf = torch.full((n + 4096,), 255, dtype=torch.uint8, device="cuda")
+    for o in (16, 48, 240):
+        got = q.qlora_head_loss_step(H, W, Y, ws=buf[o:o + n])
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert bool((buf[240 + n:] == 255).all())  # and nothing behind it
+
+
 def test_gradient_against_differences_of_the_loss():
     """The gradient along a direction against the loss at two points on it."""
     h, w, y = _case(128, 700, 256, seed=9, lean=10.0)
@@ -358,6 +373,12 @@ def test_refusals_on_device_tensors():
     h, w, y = _case(8, 50, 64)
     H, W, Y = h.cuda(), w.cuda(), y.cuda()
     g = torch.ones(8, device="cuda")
+    N = q.quantize_weight(W)
+    assert q.qlora_head_loss_fwd(H, N, Y)[0].shape == (8,)
+    for bad in (N._replace(codes=N.codes[:-1]), N._replace(c8=N.c8[:-1]), N._replace(s2=N.s2[:0]),
+                N._replace(n_out=51), N._replace(codes=N.codes.cpu()), N._replace(s2=N.s2.double())):
+        with pytest.raises(q.QloraError):
+            q.qlora_head_loss_fwd(H, bad, Y)
     for f in (lambda: q.qlora_head_loss_fwd(H, W[:, :56], Y), lambda: q.qlora_head_loss_fwd(H, W, Y[:7]),
               lambda: q.qlora_head_loss_fwd(H, W, Y.int()), lambda: q.qlora_head_loss_fwd(H, W, y),
               lambda: q.qlora_head_loss_fwd(H, W.float(), Y), lambda: q.qlora_head_loss_fwd(H.t(), W, Y),
