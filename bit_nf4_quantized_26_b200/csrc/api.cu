@@ -237,12 +237,12 @@ qlora_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLORA_OK : QLO
 enum KernelId {
   kKQuantize = 0, kKDequantize, kKDown, kKFusedFwd, kKFinishFwd, kKLowFwd, kKLowFinish, kKDU, kKDB, kKFusedDX,
   kKDA, kKAdamW8, kKDropout, kKDropoutDx, kKActQuantize, kKActDequantize, kKActDA, kKHeadLogits, kKHeadGrad,
-  kKHeadCombine, kKCount
+  kKHeadCombine, kKHeadRows, kKCount
 };
 const char* const kKernelNames[kKCount] = {
     "nf4_quantize", "nf4_dequantize", "lora_down", "fused_fwd", "finish_fwd", "lowm_fwd", "lowm_finish",
     "lora_du", "lora_db", "fused_dx", "lora_da", "adamw8", "dropout", "dropout_dx", "act8_quantize",
-    "act8_dequantize", "act8_da", "head_logits", "head_grad", "head_combine"};
+    "act8_dequantize", "act8_da", "head_logits", "head_grad", "head_combine", "head_rows"};
 
 struct ProfRecord {
   int id;
@@ -1352,7 +1352,14 @@ struct HeadPlanHost {
   int64_t splits = 1, kper = 0;  // slices of a piece's dH contraction, 64-deep stages each
   int64_t cost = 0;              // of the products: waves x 64-deep stages x columns
   size_t off_cnt = 0, off_z = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_sum = 0, off_pl = 0;
-  size_t off_g = 0, off_acc = 0, off_w = 0, total = 0;
+  size_t off_g = 0, off_acc = 0, off_w = 0, off_rows = 0, off_place = 0, off_nrows = 0, off_h = 0, total = 0;
+  // dH's products take the rows that count only (the backward's both, the
+  // step's second; losses need every row's lse).  Listing and gathering them
+  // costs 3-8 us; backward without against with it, a quarter of the tokens
+  // ignored: 512 x 20000 x 1024 (4e10 operations) 48 / 53 us, 1000 x 25000 x
+  // 1024 (1e11) 119 / 108, 2048 x 50000 x 1024 337 / 313, 4096 x 32000 x 2048
+  // 818 / 702; none ignored, 512 x 50000 x 1024: 104 / 106.
+  bool compact = false;
 };
 
 // Slices of the dH contraction of a piece (kst stages) over `tiles` tiles and
@@ -1448,6 +1455,13 @@ static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, i
     p.off_g = take(2 * t * static_cast<size_t>(p.ldg));
     if (p.pieces > 1 || p.splits > 1)
       p.off_acc = take(4 * static_cast<size_t>(p.splits * trows) * static_cast<size_t>(cdiv(D, tile) * tile));
+  }
+  p.compact = op != QLORA_HEAD_FWD && T > 256 && 4.0 * T * V * D >= 1e11;
+  if (p.compact) {
+    p.off_rows = take(4 * t);
+    p.off_place = take(4 * t);
+    p.off_nrows = take(4);
+    if (op == QLORA_HEAD_BWD) p.off_h = take(2 * t * static_cast<size_t>(D));
   }
   if (nf4 && !p.codes) p.off_w = take(2 * static_cast<size_t>(std::min(p.piece, V)) * static_cast<size_t>(D));
   p.total = off + 256;  // the parts are laid out from a 256-byte boundary
@@ -1575,7 +1589,31 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
   CUtensorMap mh, mg, mw, mwt;
   const uint32_t abox = static_cast<uint32_t>(std::min<int64_t>(128, cdiv(T, 8) * 8));
   a.arows = static_cast<int>(abox);
-  if (!map_bf16_ld(&mh, c.H, T, D, c.ldh, 64, abox)) return QLORA_ERR_CUDA;
+  int32_t* rows = reinterpret_cast<int32_t*>(at(p.off_rows));
+  int32_t* place = reinterpret_cast<int32_t*>(at(p.off_place));
+  int32_t* nrows = reinterpret_cast<int32_t*>(at(p.off_nrows));
+  const bool gather = p.compact && op == QLORA_HEAD_BWD;
+  uint16_t* hrows = reinterpret_cast<uint16_t*>(at(p.off_h));
+  if (!(gather ? map_bf16_ld(&mh, hrows, T, D, D, 64, abox) : map_bf16_ld(&mh, c.H, T, D, c.ldh, 64, abox)))
+    return QLORA_ERR_CUDA;
+  if (p.compact) {
+    ProfScope ps(kKHeadRows, cs);
+    if (qlora_status st =
+            from_cuda(launch_head_index(c.labels, c.ignore, V, T, rows, place, nrows, d_status, cs)))
+      return st;
+    if (gather)
+      if (qlora_status st = from_cuda(launch_head_gather(c.H, c.ldh, T, D, place, hrows, c.dH, c.lddh, cs))) return st;
+  }
+  if (gather) {
+    a.nrows = nrows;
+    a.rows = rows;
+  } else if (p.compact) {
+    a.place = place;
+    cb.place = place;
+    cb.dh = c.dH;
+    cb.ldd = c.lddh;
+    cb.dim = D;
+  }
   const uint32_t wbox = static_cast<uint32_t>(p.pair ? p.tw / 2 : p.tw);
   const bool grad = op != QLORA_HEAD_FWD;
   if (p.codes && (!map_u8(&mw, hd.codes, V, D / 2, 32, wbox, 32) ||
@@ -1650,6 +1688,10 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
       d.ldd = c.lddh;
       d.dloss = c.dloss;
       d.stats = c.stats_in;
+      if (p.compact) {
+        d.nrows = nrows;
+        d.rows = rows;
+      }
       if (op == QLORA_HEAD_STEP) {
         d.alpha = cb.alpha;
         d.row_sum = cb.row_sum;

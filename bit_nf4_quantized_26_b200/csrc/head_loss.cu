@@ -169,6 +169,9 @@ constexpr int kSumCols = kHeadTile / 2;                 // a thread's columns
 constexpr int kSumStride = 32 * kEpiWarps;              // float4 per row
 constexpr int kSumBlock = kSumCols / 4 * kSumStride;    // float4 per CTA of a tile
 
+// Rows of a product's token-side operand.
+__device__ __forceinline__ int operand_rows(const HeadArgs& a) { return a.nrows ? __ldcg(a.nrows) : a.T; }
+
 // dH_t = ca * (the row's sum over the vocabulary) + cl * W[label].
 __device__ __forceinline__ void grad_row_factors(const HeadArgs& a, int t, float& ca, float& cl) {
   if (a.row_sum) {
@@ -292,9 +295,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;
   const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
-  const int mn = a.mtiles * a.ntiles;
-  const int tw = kGrad ? kHeadTile : a.tw;           // columns of a tile
-  const int tiles = mn * (kGrad ? a.splits : 1);     // (split, tile)
+  const int tw = kGrad ? kHeadTile : a.tw;  // columns of a tile
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < P::kStages; ++s) {
@@ -332,6 +333,10 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
   const WaitCtx wc{abort_flag, a.status};
   grid_dependency_wait();
   grid_dependents_launch();
+  const int T = operand_rows(a);
+  const int mtiles = (T + kTokens - 1) / kTokens;
+  const int mn = mtiles * a.ntiles;
+  const int tiles = mn * (kGrad ? a.splits : 1);  // (split, tile)
   if ((MODE == kHeadLoss || MODE == kHeadExp) && blockIdx.x == 0)
     for (int i = threadIdx.x; i < a.zero_count; i += blockDim.x) a.zero[i] = 0u;
 
@@ -344,12 +349,12 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
       for (int tile = worker; ok && tile < tiles; tile += workers) {
         int m, n;
         const int split = tile / mn;
-        head_tile<kGrad>(tile - split * mn, a.mtiles, a.ntiles, m, n);
+        head_tile<kGrad>(tile - split * mn, mtiles, a.ntiles, m, n);
         const int arow = m * kTokens + static_cast<int>(rank) * 128;
         const int bcol = n * tw + static_cast<int>(rank) * (tw / 2);
         const int k1 = min(a.kst, (split + 1) * a.kper);
-        const bool mine = arow < a.T;  // else the CTA's rows hold no token: nothing to copy
-        const uint32_t bytes = (PAIR && arow + 128 < a.T ? 2 : 1) * a.arows * 128u + (NF4 ? 0 : tw * 128u);
+        const bool mine = arow < T;  // else the CTA's rows hold no token: nothing to copy
+        const uint32_t bytes = (PAIR && arow + 128 < T ? 2 : 1) * a.arows * 128u + (NF4 ? 0 : tw * 128u);
         for (int kt = split * a.kper; kt < k1; ++kt, at.advance()) {
           const uint32_t s = at.slot;
           if (issued == P::kStages && !mbar_wait(&empty[s], at.parity ^ 1, wc)) {
@@ -474,7 +479,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     for (int tile = worker; ok && tile < tiles; tile += workers) {
       const int split = tile / mn;
       int m, n;
-      head_tile<kGrad>(tile - split * mn, a.mtiles, a.ntiles, m, n);
+      head_tile<kGrad>(tile - split * mn, mtiles, a.ntiles, m, n);
       const int kt0 = split * a.kper, kn = min(a.kst, kt0 + a.kper) - kt0;
       if (kn <= 0) continue;
       const int g0 = (grp + P::kGroups - begun) % P::kGroups;         // the group's first stage of the tile
@@ -548,15 +553,17 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     for (int tile = worker; tile < tiles; tile += workers) {
       int m, n;
       const int split = tile / mn;
-      head_tile<kGrad>(tile - split * mn, a.mtiles, a.ntiles, m, n);
+      head_tile<kGrad>(tile - split * mn, mtiles, a.ntiles, m, n);
       const int kn = min(a.kst, (split + 1) * a.kper) - split * a.kper;
-      const int t = m * kTokens + static_cast<int>(rank) * 128 + q * 32 + lane;
-      const bool rok = t < a.T;
+      const int row = m * kTokens + static_cast<int>(rank) * 128 + q * 32 + lane;  // of the operand
+      const bool rok = row < T;
       const int n0 = n * tw + half * hw;
       const int nv = min(hw, a.ncols - n0);  // this thread's columns (may be none)
+      int t = row;  // the token
       int64_t label = -1;
       bool counted = false;
       if (rok) {
+        if (a.rows) t = __ldcg(a.rows + row);
         label = __ldg(a.labels + t);
         counted = counts(label, a.ignore, a.vocab);
       }
@@ -653,7 +660,8 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         }
         if (rok) {
           a.part[static_cast<int64_t>(2 * n + half) * a.T + t] = make_float2(ref, (p[0] + p[1]) + (p[2] + p[3]));
-          store_bf16(a.g + static_cast<int64_t>(t) * a.ldg + n0, hw, l);
+          const int at = a.place ? __ldcg(a.place + t) : t;
+          if (at >= 0) store_bf16(a.g + static_cast<int64_t>(at) * a.ldg + n0, hw, l);
         }
       } else if (MODE == kHeadProb) {
         const float lse = rok ? __ldcg(a.lse + t) : 0.0f;
@@ -665,7 +673,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
           if (j == lj) l[j] = pl;
         }
         if (rok) {
-          store_bf16(a.g + static_cast<int64_t>(t) * a.ldg + n0, hw, l);
+          store_bf16(a.g + static_cast<int64_t>(row) * a.ldg + n0, hw, l);
           if (n0 == 0 && a.v0 == 0 && !counted && label != a.ignore && a.status) atomicOr(a.status, QLORA_DEV_LABEL);
         }
       }
@@ -683,6 +691,79 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
   }
 }
 
+// ------------------------------------------------------------- rows that count
+//
+// An ignored token has no gradient: its row is left out of the products that
+// make dH (a fine-tuning batch ignores its prompts).  The index lists the
+// tokens that count in order; the device keeps their number.
+
+constexpr int kIndexThreads = 1024;
+constexpr int kIndexEach = 4;
+
+// One block: rows[i] the i-th token that counts, place[t] its i or -1.
+__global__ void __launch_bounds__(kIndexThreads) head_index_kernel(const int64_t* __restrict__ labels, int64_t ignore,
+                                                                   int64_t vocab, int T, int32_t* rows, int32_t* place,
+                                                                   int32_t* nrows, int32_t* status) {
+  __shared__ int warp_sum[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int base = 0;
+  bool bad = false;
+  for (int64_t t0 = 0; t0 < T; t0 += kIndexThreads * kIndexEach) {
+    const int64_t t = t0 + threadIdx.x * kIndexEach;
+    bool in[kIndexEach];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kIndexEach; ++i) {
+      const int64_t label = t + i < T ? labels[t + i] : ignore;
+      in[i] = counts(label, ignore, vocab);
+      bad |= !in[i] && label != ignore;
+      n += in[i] ? 1 : 0;
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = base, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int x = warp_sum[w];
+      if (w < warp) before += x;
+      all += x;
+    }
+    int at = before + incl - n;
+#pragma unroll
+    for (int i = 0; i < kIndexEach; ++i) {
+      if (t + i < T) {
+        place[t + i] = in[i] ? at : -1;
+        if (in[i]) rows[at++] = static_cast<int32_t>(t + i);
+      }
+    }
+    base += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *nrows = base;
+  if (bad && status) atomicOr(status, QLORA_DEV_LABEL);
+}
+
+// Block t: row t of H to its place among the rows that count, or zeros to row t
+// of dH (which may be H's).
+__global__ void __launch_bounds__(128) head_gather_kernel(const uint16_t* h, int64_t ldh, int64_t dim,
+                                                          const int32_t* place, uint16_t* out, uint16_t* dh,
+                                                          int64_t ldd) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t t = blockIdx.x;
+  const int at = __ldcg(place + t);
+  const uint4* src = reinterpret_cast<const uint4*>(h + t * ldh);
+  uint4* dst = reinterpret_cast<uint4*>(at >= 0 ? out + static_cast<int64_t>(at) * dim : dh + t * ldd);
+  for (int64_t j = threadIdx.x; j < dim / 8; j += 128) dst[j] = at >= 0 ? src[j] : make_uint4(0, 0, 0, 0);
+}
+
 // ------------------------------------------------------------------- finish
 //
 // A split contraction's sums joined in split order, and dH's rows from them.
@@ -690,15 +771,19 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
 __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_constant__ HeadArgs a) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const int mn = a.mtiles * a.ntiles;
   const int ctas = a.pair ? 2 : 1;
+  const int T = operand_rows(a);
+  const int mtiles = (T + 128 * ctas - 1) / (128 * ctas);
+  const int mn = mtiles * a.ntiles;
   const int tile = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  if (tile >= mn) return;
   int m, n;
-  head_tile<true>(tile, a.mtiles, a.ntiles, m, n);
+  head_tile<true>(tile, mtiles, a.ntiles, m, n);
   const int et = threadIdx.x, w = et >> 5, lane = et & 31;
-  const int t = (m * ctas + rank) * 128 + ((w + 2) & 3) * 32 + lane;  // as in the product's epilogue
+  const int row = (m * ctas + rank) * 128 + ((w + 2) & 3) * 32 + lane;  // as in the product's epilogue
   const int d = n * kHeadTile + (w >> 2) * kSumCols + blockIdx.y * 32;
-  if (t >= a.T || d >= a.ncols) return;
+  if (row >= T || d >= a.ncols) return;
+  const int t = a.rows ? __ldcg(a.rows + row) : row;
   const float4* sum = reinterpret_cast<const float4*>(a.acc) + static_cast<int64_t>(blockIdx.x) * kSumBlock +
                       static_cast<int>(blockIdx.y) * 8 * kSumStride + et;
   float l[32] = {};
@@ -847,14 +932,22 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
           todo &= todo - 1;
           const float fr = __shfl_sync(0xFFFFFFFFu, f, src);
           const int js = __shfl_sync(0xFFFFFFFFu, j, src), ts = __shfl_sync(0xFFFFFFFFu, t, src);
-          if (4 * lane >= a.part_cols) continue;
-          uint2* at = reinterpret_cast<uint2*>(a.e + static_cast<int64_t>(ts) * a.lde +
+          const int row = a.place ? __ldcg(a.place + ts) : ts;
+          if (row < 0 || 4 * lane >= a.part_cols) continue;
+          uint2* at = reinterpret_cast<uint2*>(a.e + static_cast<int64_t>(row) * a.lde +
                                                static_cast<int64_t>(js) * a.part_cols) + lane;
           const uint2 v = __ldcg(at);
           *at = make_uint2(pack_bf16x2(__uint_as_float(v.x << 16) * fr, __uint_as_float(v.x & 0xFFFF0000u) * fr),
                            pack_bf16x2(__uint_as_float(v.y << 16) * fr, __uint_as_float(v.y & 0xFFFF0000u) * fr));
         }
       }
+    }
+  }
+  if (a.last && a.place) {  // rows of dH that no product writes
+    for (int i = 0; i < TB && t0 + i < a.T; ++i) {
+      if (__ldcg(a.place + t0 + i) >= 0) continue;
+      uint4* dst = reinterpret_cast<uint4*>(a.dh + static_cast<int64_t>(t0 + i) * a.ldd);
+      for (int64_t j = threadIdx.x; j < a.dim / 8; j += kCombineWarps * 32) dst[j] = make_uint4(0, 0, 0, 0);
     }
   }
   if (a.last && last_block) {
@@ -908,6 +1001,18 @@ cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMa
 cudaError_t launch_head_finish(const HeadArgs& a, cudaStream_t stream) {
   return launch_kernel(head_finish_kernel, dim3((a.pair ? 2 : 1) * a.mtiles * a.ntiles, kSumCols / 32),
                        dim3(kSumStride), 0, stream, dim3(1, 1, 1), a);
+}
+
+cudaError_t launch_head_index(const int64_t* labels, int64_t ignore, int64_t vocab, int64_t T, int32_t* rows,
+                              int32_t* place, int32_t* nrows, int32_t* status, cudaStream_t stream) {
+  return launch_kernel(head_index_kernel, dim3(1), dim3(kIndexThreads), 0, stream, dim3(1, 1, 1), labels, ignore, vocab,
+                       static_cast<int>(T), rows, place, nrows, status);
+}
+
+cudaError_t launch_head_gather(const uint16_t* h, int64_t ldh, int64_t T, int64_t dim, const int32_t* place,
+                               uint16_t* out, uint16_t* dh, int64_t ldd, cudaStream_t stream) {
+  return launch_kernel(head_gather_kernel, dim3(static_cast<unsigned>(T)), dim3(128), 0, stream, dim3(1, 1, 1), h, ldh,
+                       dim, place, out, dh, ldd);
 }
 
 // Tokens of a combine block: 32, or for few tokens 4 (then at most 512 blocks).

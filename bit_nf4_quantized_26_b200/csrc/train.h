@@ -53,6 +53,12 @@ constexpr int head_workers(bool pair) { return pair ? 74 : 148; }
 struct HeadArgs {
   int pair, nf4;          // which kernel: tiles of 256 tokens on CTA pairs; (single CTAs) W from its codes
   int T;                  // tokens
+  // The rows that count (see head_loss.cu), or null where the operand's rows
+  // are the tokens: their number, the token of a row (Prob, Grad), and the row
+  // of a token or -1 (Exp).
+  const int32_t* nrows;
+  const int32_t* rows;
+  const int32_t* place;
   int arows;              // token rows of a copy: 128, or for fewer tokens those, to a multiple of 8
   int ncols;              // columns of this product: the piece's vocabulary rows, or dim (Grad)
   int kst;                // 64-deep contraction stages
@@ -69,7 +75,7 @@ struct HeadArgs {
   float* label_logit;     // Loss, Exp: [T]
   float2* part;           // Loss, Exp: (reference, sum of exponentials) [half tile][T], from the piece's first
   const float* lse;       // Prob: [T]
-  uint16_t* g;            // Prob, Exp: [T, ldg]
+  uint16_t* g;            // Prob, Exp: [rows, ldg]
   int64_t ldg;
   uint32_t* zero;         // Loss, Exp: words cleared by the first CTA (combine's counters)
   int zero_count;
@@ -97,6 +103,13 @@ struct HeadArgs {
 cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
                              cudaStream_t stream);
 
+// rows [T], place [T], nrows [1] of the tokens that count.
+cudaError_t launch_head_index(const int64_t* labels, int64_t ignore, int64_t vocab, int64_t T, int32_t* rows,
+                              int32_t* place, int32_t* nrows, int32_t* status, cudaStream_t stream);
+// Their rows of h to `out` [T, dim]; zeros to the other rows of dh.
+cudaError_t launch_head_gather(const uint16_t* h, int64_t ldh, int64_t T, int64_t dim, const int32_t* place,
+                               uint16_t* out, uint16_t* dh, int64_t ldd, cudaStream_t stream);
+
 // Grad with splits > 1: joins the splits' sums after the last piece.
 cudaError_t launch_head_finish(const HeadArgs& a, cudaStream_t stream);
 
@@ -112,8 +125,11 @@ struct HeadCombineArgs {
   int first, last;         // of the pieces (the forward combines once: both)
   float2* run;             // step: running (reference, sum) [T]
   float* alpha;            // step: [T]
-  uint16_t* e;             // step: the piece's exponentials [T, lde], or null
+  uint16_t* e;             // step: the piece's exponentials [rows, lde], or null
   int64_t lde;
+  const int32_t* place;    // step: row of a token in e or -1, or null; then, with the last piece,
+  uint16_t* dh;            //   the other rows of dH become zero
+  int64_t ldd, dim;
   float* row_sum;          // step: [T]
   float* p_label;          // step: [T]
   int32_t* counters;       // [2]: tokens that count, blocks done; cleared before

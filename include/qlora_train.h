@@ -104,8 +104,9 @@ QLORA_API qlora_status qlora_linear_bwd_dropout_act8(const uint16_t* dY, const u
  * A token counts unless its label is ignore_index (or out of range, see
  * QLORA_DEV_LABEL).  An ignored token's row of H may hold anything, NaN
  * included: its loss and its row of dH are exactly 0 (its lse is that of the
- * row as it stands).  A non-finite lse of a token that counts sets
- * QLORA_DEV_NONFINITE.
+ * row as it stands).  Larger calls leave ignored rows out of the products that
+ * make dH: a batch whose prompts are ignored costs that much less.  A
+ * non-finite lse of a token that counts sets QLORA_DEV_NONFINITE.
  *
  * The head: W [vocab, dim], either bf16 rows (`w`, row stride ld elements,
  * ld % 8 == 0, dim % 8 == 0) or, with w == NULL, NF4 (codes, c8, s2 and an
@@ -151,7 +152,8 @@ typedef struct {
  * Beside per-token words it holds 8 bytes per half tile of logits (128, or
  * fewer columns where that fills the GPU; forward, step), a piece of the
  * probabilities (backward, step: about 128 MB in bf16, at least 2048 columns),
- * fp32 sums [T, dim] (with several pieces, and for few tokens one per slice of
+ * the rows of H that count (backward of larger calls: bf16 [T, dim]), fp32 sums
+ * [T, dim] (with several pieces, and for few tokens one per slice of
  * the contraction), and, for more than 128 tokens, a dequantised piece of an
  * NF4 head (at most 128 MB, at least 2048 rows).
  * Accuracy: exact bf16 inputs, fp32 accumulation and softmax; the probabilities

@@ -164,6 +164,77 @@ def test_large_logits_take_other_references(T, V, D, scale):
     r.check_grad(dH[sel], np.ones(rows.size), roundings=2)
 
 
+# large enough that dH's products take the rows that count only: token tiles of
+# both kinds, several pieces, a split contraction, NF4, logits with other references
+COMPACT = [(300, 33000, 2560, False, 0.3, 1.0), (1153, 5000, 4400, True, 0.6, 1.0), (3000, 9000, 1024, False, 0.25, 1.0),
+           (16500, 4500, 448, False, 0.5, 30.0), (2000, 12500, 1024, False, 0.999, 1.0),
+           (2000, 12500, 1024, True, 0.0, 1.0)]
+
+
+@pytest.mark.parametrize("T,V,D,nf4,ignored,scale", [c if not c[3] else (c[0], c[1], c[2] // 64 * 64) + c[3:]
+                                                     for c in COMPACT])
+def test_rows_that_count(T, V, D, nf4, ignored, scale):
+    assert T > 256 and 4.0 * T * V * D >= 1e11
+    h, w, y = _case(T, V, D, seed=12, ignored=ignored, scale=scale, lean=0.0 if scale > 1 else 5.0)
+    y[T // 2] = V - 1                                     # one at least counts
+    h[y == -100] = float("nan")
+    H, Y, W = h.cuda(), y.cuda(), w.cuda()
+    if nf4:
+        W = q.quantize_weight(W)
+        w = q.nf4_dequantize(W.codes, W.c8, W.s2, V * D).view(V, D).cpu()
+    count = torch.nonzero(y != -100)[:, 0]
+    rows = count[torch.linspace(0, count.numel() - 1, min(120, count.numel())).long()].unique()
+    r = Ref(h[rows], w, y[rows])
+    sel, gone = rows.cuda(), (y == -100).cuda()
+    g = torch.linspace(-1, 2, T)
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    _, lse, _ = q.qlora_head_loss_fwd(H, W, Y)
+    buf = torch.full((T, D + 16), 5.0, dtype=torch.bfloat16, device="cuda")
+    for dH in (None, buf[:, 8:8 + D]):
+        d = q.qlora_head_loss_bwd(H, W, Y, lse, g.cuda(), dH=dH, status=status)
+        r.check_grad(d[sel], g.numpy()[rows], roundings=2)
+        assert not d[gone].any()
+    assert bool((buf[:, :8] == 5).all()) and bool((buf[:, 8 + D:] == 5).all())
+    buf.fill_(5.0)
+    for dH in (None, buf[:, 8:8 + D]):
+        l2, lse2, st, d = q.qlora_head_loss_step(H, W, Y, weight=g.cuda(), dH=dH, status=status)
+        r.check_grad(d[sel], g.numpy()[rows], roundings=2)
+        assert not d[gone].any() and int(st[1]) == count.numel()
+        assert np.all(np.abs(l2.cpu().numpy()[rows] - r.loss) <= r.loss_tol)
+    assert bool((buf[:, :8] == 5).all()) and bool((buf[:, 8 + D:] == 5).all())
+    assert int(status[0]) == 0
+    again = H.clone()                                     # in place of the hidden states
+    inplace = q.qlora_head_loss_step(again, W, Y, weight=g.cuda(), dH=again)[3]
+    assert torch.equal(inplace, d)
+    again = H.clone()
+    want = q.qlora_head_loss_bwd(H, W, Y, lse, g.cuda())
+    assert torch.equal(q.qlora_head_loss_bwd(again, W, Y, lse, g.cuda(), dH=again), want)
+
+
+@pytest.mark.parametrize("case", ["none", "first", "last", "bad"])
+def test_rows_that_count_at_the_ends(case):
+    T, V, D = 3000, 9000, 1024
+    h, w, y = _case(T, V, D, seed=13, ignored=0.0)
+    k = {"none": [], "first": [0], "last": [T - 1], "bad": [5, 2500]}[case]
+    z = torch.full_like(y, -100)
+    z[k] = y[k]
+    if case == "bad":
+        z[7], z[2999], z[4] = V, -3, 1 << 40
+    H, W, Y = h.cuda(), w.cuda(), z.cuda()
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    loss, lse, stats, dH = q.qlora_head_loss_step(H, W, Y, scale=2.0, status=status)
+    assert int(status[0]) == (q.DEV_LABEL if case == "bad" else 0) and int(stats[1]) == len(k)
+    status.zero_()
+    dB = q.qlora_head_loss_bwd(H, W, Y, lse, torch.full((1,), 2.0, device="cuda"), stats=stats, status=status)
+    assert int(status[0]) == (q.DEV_LABEL if case == "bad" else 0)
+    keep = torch.zeros(T, dtype=torch.bool)
+    keep[k] = True
+    for d in (dH, dB):
+        assert not d[~keep.cuda()].any()
+        if k:
+            Ref(h[k], w, y[k]).check_grad(d[k], np.full(len(k), 2.0 / len(k)), roundings=2)
+
+
 def test_well_predicted_tokens_keep_their_gradient():
     """p close to 1 at the label: the gradient is the small difference."""
     h, w, y = _case(64, 500, 256, seed=4, ignored=0.0)
