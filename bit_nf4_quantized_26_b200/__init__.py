@@ -626,8 +626,10 @@ def _tensor(t, dtype, shape, dev, where, name):
     return t
 
 
-def _out(t, shape, dtype, dev, where, name):
-    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _tensor(t, dtype, shape, dev, where, name)
+def _out(t, like, shape, where, name):
+    """``t``, or a new tensor of ``like``'s type on its device (the cheapest way to
+    one: small problems take no longer on the GPU)."""
+    return like.new_empty(shape) if t is None else _tensor(t, like.dtype, shape, like.device, where, name)
 
 
 def _rows(t, where, name, cols=None, rows=None, dev=None):
@@ -667,11 +669,11 @@ def _nf4(W, dev, where, name):
         _refuse(ERR_SHAPE, where, f"{name}'s mean is no fp32 word on {dev}")
 
 
-def _workspace(ws, size, dev, where):
-    """(address, bytes, tensor) of the workspace, allocated if not given."""
+def _workspace(ws, size, like, where):
+    """(address, bytes, tensor) of the workspace, allocated on ``like``'s device if not given."""
     if ws is None:
-        ws = torch.empty(max(size(), 16), dtype=torch.uint8, device=dev)
-    elif ws.device != dev or not ws.is_contiguous():
+        ws = like.new_empty(max(size(), 16), dtype=torch.uint8)
+    elif ws.device != like.device or not ws.is_contiguous():
         _refuse(ERR_SHAPE, where, f"ws is on {ws.device}, or not contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
@@ -705,7 +707,7 @@ def act8_dequantize(X8, out=None, stream=None):
     ld = K if out is None else _rows(out, where, "out", K, M, dev)[2]
 
     def call(st):
-        x = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if out is None else out
+        x = codes.new_empty((M, K), dtype=torch.bfloat16) if out is None else out
         _check(_lib.act8_dequantize(codes.data_ptr(), exps.data_ptr(), M, K, x.data_ptr(), ld, st), where)
         return x
     return _run(dev, stream, call)
@@ -724,6 +726,8 @@ def qlora_bwd_act8_workspace_size(M, N, K, members, r, dropout=False):
 def _bwd_act8(where, dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, drop, ws, status, stream, run):
     """Checks, outputs and workspace shared by the ``*_bwd_act8`` passes."""
     N, K = int(W.n_out), int(W.k_in)
+    if dY.dim() != 2:
+        _refuse(ERR_SHAPE, where, f"dY has {dY.dim()} dimensions, not 2")
     M = dY.shape[0]
     dev = dY.device
     if dx_dtype not in (DTYPE_BF16, DTYPE_F32):
@@ -741,13 +745,13 @@ def _bwd_act8(where, dY, X8, U, W, G, A, B, dx_dtype, dX, dA, dB, drop, ws, stat
     _nf4(W, dev, where, "W")
 
     def call(st):
-        x = _out(dX, (M, K), torch.float32 if dx_dtype == DTYPE_F32 else torch.bfloat16, dev, where, "dX")
-        a = _out(dA, (G * r, K), torch.float32, dev, where, "dA")
-        b = _out(dB, (N, r), torch.float32, dev, where, "dB")
+        x = _out(dX, U if dx_dtype == DTYPE_F32 else dY, (M, K), where, "dX")
+        a = _out(dA, U, (G * r, K), where, "dA")
+        b = _out(dB, U, (N, r), where, "dB")
         if M == 0:  # nothing to sum; the library's call is a no-op
             a.zero_()
             b.zero_()
-        at, size_, keep = _workspace(ws, lambda: qlora_bwd_act8_workspace_size(M, N, K, G, r, drop), dev, where)
+        at, size_, keep = _workspace(ws, lambda: qlora_bwd_act8_workspace_size(M, N, K, G, r, drop), U, where)
         _check(run(M, r, x.data_ptr(), a.data_ptr(), b.data_ptr(), at, size_, _word(status, dev, where), st), where)
         return x, a, b
     return _run(dev, stream, call)
@@ -845,8 +849,7 @@ def _head_call(where, op, H, head, labels):
 
 
 def _loss_out(H, loss, lse, stats, T, dev, where):
-    """The losses', log-sum-exps' and statistics' tensors (new ones by the
-    cheapest calls: small problems take no longer on the GPU)."""
+    """The losses', log-sum-exps' and statistics' tensors."""
     loss = (H.new_empty((T,), dtype=torch.float32) if loss is None
             else _tensor(loss, torch.float32, (T,), dev, where, "loss"))
     lse = torch.empty_like(loss) if lse is None else _tensor(lse, torch.float32, (T,), dev, where, "lse")
@@ -873,7 +876,7 @@ def qlora_head_loss_fwd(H, head, labels, ignore_index=IGNORE_INDEX, loss=None, l
 
     def call(st):
         lo, ls, sm = _loss_out(H, loss, lse, stats, T, dev, where)
-        at, bytes_, keep = _workspace(ws, size, dev, where)
+        at, bytes_, keep = _workspace(ws, size, H, where)
         _check(_lib.qlora_head_loss_fwd(H.data_ptr(), ldh, T, h, labels.data_ptr(), int(ignore_index), lo.data_ptr(),
                                         ls.data_ptr(), sm.data_ptr(), at, bytes_, _word(status, dev, where), st),
                where)
@@ -896,7 +899,7 @@ def qlora_head_loss_bwd(H, head, labels, lse, dloss, stats=None, ignore_index=IG
 
     def call(st):
         g = grad()
-        at, bytes_, keep = _workspace(ws, size, dev, where)
+        at, bytes_, keep = _workspace(ws, size, H, where)
         _check(_lib.qlora_head_loss_bwd(H.data_ptr(), ldh, T, h, labels.data_ptr(), int(ignore_index), lse.data_ptr(),
                                         dloss.data_ptr(), None if stats is None else stats.data_ptr(), g.data_ptr(),
                                         ldd, at, bytes_, _word(status, dev, where), st), where)
@@ -918,7 +921,7 @@ def qlora_head_loss_step(H, head, labels, weight=None, scale=1.0, ignore_index=I
     def call(st):
         lo, ls, sm = _loss_out(H, loss, lse, stats, T, dev, where)
         g = grad()
-        at, bytes_, keep = _workspace(ws, size, dev, where)
+        at, bytes_, keep = _workspace(ws, size, H, where)
         _check(_lib.qlora_head_loss_step(H.data_ptr(), ldh, T, h, labels.data_ptr(), int(ignore_index),
                                          None if weight is None else weight.data_ptr(), float(scale), lo.data_ptr(),
                                          ls.data_ptr(), sm.data_ptr(), g.data_ptr(), ldd, at, bytes_,

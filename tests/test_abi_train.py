@@ -173,3 +173,15 @@ def test_binding_refuses_wrong_tensors():
                  lambda: q.qlora_head_loss_bwd(H, W, y, None, None)):
         with pytest.raises(q.QloraError):
             call()
+
+
+@pytest.mark.parametrize("dY", [_cpu(64), torch.zeros((), dtype=torch.bfloat16), _cpu(2, 4, 64), _cpu(4, 64)])
+def test_binding_refuses_other_gradients(dY):
+    """Not a matrix, or not on a GPU: an error of the library, not Python's."""
+    class W:
+        n_out, k_in = 64, 64
+    X8 = q.Act8(_cpu(4, 64, dtype=torch.uint8), _cpu(4, 1, dtype=torch.uint8))
+    for f, more in ((q.qlora_linear_bwd_act8, ()), (q.qlora_linear_bwd_dropout_act8, (0.1, 3))):
+        with pytest.raises(q.QloraError) as e:
+            f(dY, X8, _cpu(4, 8, dtype=torch.float32), W, _cpu(8, 64), _cpu(64, 8), 1.0, *more)
+        assert e.value.code == SHAPE
