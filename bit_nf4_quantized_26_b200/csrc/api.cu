@@ -1349,7 +1349,8 @@ struct HeadPlanHost {
   int64_t pieces = 0;
   int64_t tw = 0;                // columns of a logit tile
   int64_t ldg = 0, parts = 0;    // per piece: columns its tiles cover, and their halves
-  int64_t splits = 1, kper = 0;  // slices of a piece's dH contraction, 64-deep stages each
+  int64_t kfull = 0;             // 64-deep stages of a piece's dH contraction
+  int64_t tails = 0;             // dH's tiles that may be in parts
   int64_t cost = 0;              // of the products: waves x 64-deep stages x columns
   size_t off_cnt = 0, off_z = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_sum = 0, off_pl = 0;
   size_t off_g = 0, off_acc = 0, off_w = 0, off_rows = 0, off_place = 0, off_nrows = 0, off_h = 0, total = 0;
@@ -1361,26 +1362,6 @@ struct HeadPlanHost {
   // 818 / 702; none ignored, 512 x 50000 x 1024: 104 / 106.
   bool compact = false;
 };
-
-// Slices of the dH contraction of a piece (kst stages) over `tiles` tiles and
-// `workers` CTA pairs or CTAs: waves x (stages per slice + what a slice's fp32
-// sums cost to write and join, about 24 stages' time), slices of at least 8
-// stages, only while all slices together are under four waves (beyond that the
-// sums cost more than the last wave's idle pairs).  Returns waves x stages.
-static int64_t head_splits(int64_t tiles, int64_t kst, int64_t workers, int64_t& splits, int64_t& per) {
-  constexpr int64_t kCost = 24;
-  int64_t best = 1, cost = cdiv(tiles, workers) * kst;
-  for (int64_t s = 2; s <= kst / 8 && tiles * s <= 4 * workers; ++s) {
-    const int64_t c = cdiv(tiles * s, workers) * (cdiv(kst, s) + kCost);
-    if (c < cost) {
-      cost = c;
-      best = s;
-    }
-  }
-  per = cdiv(kst, best);
-  splits = cdiv(kst, per);
-  return cost;
-}
 
 // Columns of a logit tile: the width that makes the fewest column-times of
 // waves of the CTA pairs or CTAs, a tile costing its width and about 16
@@ -1428,8 +1409,10 @@ static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, i
   p.ldg = cdiv(p.piece, p.tw) * p.tw;
   p.parts = 2 * cdiv(p.piece, p.tw);
   if (op != QLORA_HEAD_FWD) {
-    const int64_t stages = head_splits(mt * cdiv(D, tile), cdiv(std::min(p.piece, V), 64), workers, p.splits, p.kper);
-    p.cost += p.pieces * stages * tile;
+    p.kfull = cdiv(std::min(p.piece, V), 64);
+    const HeadTail t = head_tail(static_cast<int>(mt * cdiv(D, tile)), static_cast<int>(p.kfull),
+                                 static_cast<int>(workers));
+    p.cost += p.pieces * tile * (t.full * p.kfull + (t.rest == 0 ? 0 : t.per + (t.parts > 1 ? kHeadPartCost : 0)));
   }
   size_t off = 0;
   auto take = [&off](size_t bytes) {
@@ -1453,10 +1436,18 @@ static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, i
   }
   if (op != QLORA_HEAD_FWD) {
     p.off_g = take(2 * t * static_cast<size_t>(p.ldg));
-    if (p.pieces > 1 || p.splits > 1)
-      p.off_acc = take(4 * static_cast<size_t>(p.splits * trows) * static_cast<size_t>(cdiv(D, tile) * tile));
   }
   p.compact = op != QLORA_HEAD_FWD && T > 256 && 4.0 * T * V * D >= 1e11;
+  if (op != QLORA_HEAD_FWD) {
+    // sums of the pieces so far, of whole tiles and of parts (at most one more
+    // than tiles per worker); the rows that count are known on the device only
+    const int64_t tiles = mt * cdiv(D, tile);
+    const HeadTail t = head_tail(static_cast<int>(tiles), static_cast<int>(p.kfull), static_cast<int>(workers));
+    p.tails = p.compact ? std::min(tiles, workers) : t.parts > 1 ? t.rest : 0;
+    int64_t slots = p.pieces > 1 ? tiles : p.tails;
+    if (p.tails) slots += p.compact ? workers : t.rest * (t.parts - 1);
+    if (slots) p.off_acc = take(4 * static_cast<size_t>(slots) * static_cast<size_t>((pair ? 256 : 128) * tile));
+  }
   if (p.compact) {
     p.off_rows = take(4 * t);
     p.off_place = take(4 * t);
@@ -1646,8 +1637,6 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     // 64-deep stages per accumulator (head_loss.cu): a product of few tokens
     // waits for the weight, and short chunks cost it nothing
     a.kchunk = op == QLORA_HEAD_BWD ? 64 : (p.pair ? 12 : 4);
-    a.splits = 1;
-    a.kper = a.kst;
     float2* part = reinterpret_cast<float2*>(at(p.off_part));
     a.part = op == QLORA_HEAD_FWD ? part + i * p.parts * T : part;
     {
@@ -1678,9 +1667,9 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
       d.ncols = static_cast<int>(D);
       d.ntiles = static_cast<int>(cdiv(D, kHeadTile));
       d.kst = static_cast<int>(cdiv(pv, 64));
-      d.splits = static_cast<int>(p.splits);  // of every piece: their sums run through the pieces
-      d.kper = static_cast<int>(cdiv(d.kst, p.splits));
-      d.kchunk = d.kper;
+      d.kfull = static_cast<int>(p.kfull);  // parts end at the same stages in every piece: their sums run through
+      d.workers = head_workers(p.pair);
+      d.kchunk = d.kfull;
       d.first = first;
       d.last = last;
       d.acc = reinterpret_cast<float*>(at(p.off_acc));
@@ -1702,8 +1691,8 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
       }
       ProfScope ps(kKHeadGrad, cs);
       if (qlora_status st = from_cuda(launch_head_gemm(kHeadGrad, mg, mwt, d, cs))) return st;
-      if (last && d.splits > 1)
-        if (qlora_status st = from_cuda(launch_head_finish(d, cs))) return st;
+      if (last && p.tails)
+        if (qlora_status st = from_cuda(launch_head_finish(d, static_cast<int>(p.tails), cs))) return st;
     }
   }
   return QLORA_OK;

@@ -162,7 +162,7 @@ __device__ __forceinline__ void store_bf16(uint16_t* dst, int cols, const float 
   }
 }
 
-// fp32 sums between pieces and of split contractions: per (split, tile) and
+// fp32 sums between pieces and of parts of a contraction: per tile or part and
 // CTA, the epilogue threads' registers as 32 rows of 256 float4, so that every
 // access of a warp is 512 contiguous bytes.
 constexpr int kSumCols = kHeadTile / 2;                 // a thread's columns
@@ -171,6 +171,59 @@ constexpr int kSumBlock = kSumCols / 4 * kSumStride;    // float4 per CTA of a t
 
 // Rows of a product's token-side operand.
 __device__ __forceinline__ int operand_rows(const HeadArgs& a) { return a.nrows ? __ldcg(a.nrows) : a.T; }
+
+// A worker's tiles, or parts of tiles, of a product in turn: for logits every
+// workers-th tile, for dH as head_tail says (train.h).
+template <bool GRAD>
+struct HeadItems {
+  int kst, workers, i, end;           // whole tiles in turn
+  int j = 0, j_end = 0, part = 0;     // then tiles in parts, counted from `end`
+  int t0 = 0, t1 = 0;                 //   and the part's stages
+  int base = 0, parts = 1;
+  int tile, k0, kn;  // the item: its tile, first stage, and stages (none: a short piece ends before)
+  int slot;          // Grad: of its sums
+  bool whole;        // the tile is not in parts
+
+  __device__ __forceinline__ HeadItems(const HeadArgs& a, int mn, int worker, int workers_)
+      : kst(a.kst), workers(workers_), i(worker), end(mn) {
+    if (!GRAD) return;
+    const HeadTail t = head_tail(mn, a.kfull, workers);
+    end = t.full * workers;
+    base = a.first && a.last ? 0 : end;  // (whole tiles of an only piece need no sums)
+    parts = t.parts;
+    if (t.help && worker >= t.rest) {
+      part = 1;
+      j = (worker - t.rest) * t.help;
+      j_end = min(j + t.help, t.rest);
+      t0 = t.per;
+      t1 = a.kfull;
+    } else if (worker < t.rest * parts) {
+      part = worker / t.rest;
+      j = worker - part * t.rest;
+      j_end = j + 1;
+      t0 = part * t.per;
+      t1 = min(t0 + t.per, a.kfull);
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    if (i < end) {
+      tile = slot = i;
+      i += workers;
+      k0 = 0;
+      kn = kst;
+      whole = true;
+      return true;
+    }
+    if (!GRAD || j >= j_end) return false;
+    tile = end + j;
+    k0 = t0;
+    kn = min(kst, t1) - t0;
+    whole = parts == 1;
+    slot = base + j * parts + part;
+    ++j;
+    return true;
+  }
+};
 
 // dH_t = ca * (the row's sum over the vocabulary) + cl * W[label].
 __device__ __forceinline__ void grad_row_factors(const HeadArgs& a, int t, float& ca, float& cl) {
@@ -263,8 +316,8 @@ struct Ring {
 // threads add each finished one to their registers, rounding to nearest, while
 // the next runs.  (512 deep costs the products 2-3%, 1024 nothing; 256 is free
 // for few tokens, whose products wait for W.)  Results rounded to bf16 take
-// longer ones: the backward's probabilities 4096, dH a whole slice of its
-// contraction.
+// longer ones: the backward's probabilities 4096, dH all of its
+// tile's or part's contraction.
 //
 // Barriers (leader: the pair's first CTA, or the single one): full[s] (leader:
 // the stage's copies landed, and its dequantised tiles are written), empty[s]
@@ -294,7 +347,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;
-  const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
+  const int worker = blockIdx.x / kCtas, workers = kGrad ? a.workers : gridDim.x / kCtas;
   const int tw = kGrad ? kHeadTile : a.tw;  // columns of a tile
 
   if (threadIdx.x == 0) {
@@ -335,8 +388,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
   grid_dependents_launch();
   const int T = operand_rows(a);
   const int mtiles = (T + kTokens - 1) / kTokens;
-  const int mn = mtiles * a.ntiles;
-  const int tiles = mn * (kGrad ? a.splits : 1);  // (split, tile)
+  HeadItems<kGrad> it(a, mtiles * a.ntiles, worker, workers);
   if ((MODE == kHeadLoss || MODE == kHeadExp) && blockIdx.x == 0)
     for (int i = threadIdx.x; i < a.zero_count; i += blockDim.x) a.zero[i] = 0u;
 
@@ -346,16 +398,15 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
       Ring<P::kStages> at;
       uint32_t issued = 0;  // stages, up to a full ring
       bool ok = true;
-      for (int tile = worker; ok && tile < tiles; tile += workers) {
+      while (ok && it.next()) {
         int m, n;
-        const int split = tile / mn;
-        head_tile<kGrad>(tile - split * mn, mtiles, a.ntiles, m, n);
+        head_tile<kGrad>(it.tile, mtiles, a.ntiles, m, n);
         const int arow = m * kTokens + static_cast<int>(rank) * 128;
         const int bcol = n * tw + static_cast<int>(rank) * (tw / 2);
-        const int k1 = min(a.kst, (split + 1) * a.kper);
+        const int k1 = it.k0 + it.kn;
         const bool mine = arow < T;  // else the CTA's rows hold no token: nothing to copy
         const uint32_t bytes = (PAIR && arow + 128 < T ? 2 : 1) * a.arows * 128u + (NF4 ? 0 : tw * 128u);
-        for (int kt = split * a.kper; kt < k1; ++kt, at.advance()) {
+        for (int kt = it.k0; kt < k1; ++kt, at.advance()) {
           const uint32_t s = at.slot;
           if (issued == P::kStages && !mbar_wait(&empty[s], at.parity ^ 1, wc)) {
             ok = false;
@@ -409,9 +460,8 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
       Ring<P::kStages> at;
       int acc = 0;  // chunks begun
       bool ok = true;
-      for (int tile = worker; ok && tile < tiles; tile += workers) {
-        const int split = tile / mn;
-        const int kn = min(a.kst, (split + 1) * a.kper) - split * a.kper;
+      while (ok && it.next()) {
+        const int kn = it.kn;
         for (int k0 = 0; ok && k0 < kn; k0 += a.kchunk, ++acc) {
           const int buf = acc & 1;
           if (acc >= 2 && !mbar_wait_all(&acce[buf], ((acc >> 1) - 1) & 1, wc)) {
@@ -476,11 +526,10 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     at.advance(grp);
     int begun = 0;  // stages of the tiles before, modulo the groups
     bool ok = true;
-    for (int tile = worker; ok && tile < tiles; tile += workers) {
-      const int split = tile / mn;
+    while (ok && it.next()) {
       int m, n;
-      head_tile<kGrad>(tile - split * mn, mtiles, a.ntiles, m, n);
-      const int kt0 = split * a.kper, kn = min(a.kst, kt0 + a.kper) - kt0;
+      head_tile<kGrad>(it.tile, mtiles, a.ntiles, m, n);
+      const int kt0 = it.k0, kn = it.kn;
       if (kn <= 0) continue;
       const int g0 = (grp + P::kGroups - begun) % P::kGroups;         // the group's first stage of the tile
       const int count = (kn - g0 + P::kGroups - 1) / P::kGroups;      // and its number of them
@@ -550,11 +599,10 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         else mbar_arrive(&acce[buf]);
       }
     };
-    for (int tile = worker; tile < tiles; tile += workers) {
+    while (it.next()) {
       int m, n;
-      const int split = tile / mn;
-      head_tile<kGrad>(tile - split * mn, mtiles, a.ntiles, m, n);
-      const int kn = min(a.kst, (split + 1) * a.kper) - split * a.kper;
+      head_tile<kGrad>(it.tile, mtiles, a.ntiles, m, n);
+      const int kn = it.kn;
       const int row = m * kTokens + static_cast<int>(rank) * 128 + q * 32 + lane;  // of the operand
       const bool rok = row < T;
       const int n0 = n * tw + half * hw;
@@ -572,15 +620,15 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
       const int lj = lc >= 0 && lc < nv ? static_cast<int>(lc) : -1;
 
       if (MODE == kHeadGrad) {
-        // one chunk per tile (bf16 results), 32 columns at a time
+        // one chunk per item (bf16 results), 32 columns at a time
         const int buf = acc & 1;
-        if (kn > 0) {  // an empty slice (of a short last piece) adds nothing
+        if (kn > 0) {  // an empty part (of a short last piece) adds nothing
           if (!mbar_wait_warp(&accf[buf], (acc >> 1) & 1, wc)) break;
           tc_fence_after();
         }
-        float4* sum = reinterpret_cast<float4*>(a.acc) + (static_cast<int64_t>(tile) * kCtas + rank) * kSumBlock + et;
+        float4* sum = reinterpret_cast<float4*>(a.acc) + (static_cast<int64_t>(it.slot) * kCtas + rank) * kSumBlock + et;
         const float al = (!a.first && a.alpha && rok) ? __ldcg(a.alpha + t) : 1.0f;
-        const bool out = a.last && a.splits == 1;
+        const bool out = a.last && it.whole;
         float ca = 0.0f, cl = 0.0f;
         if (out && counted) grad_row_factors(a, t, ca, cl);
         for (int cb = 0; cb < kSumCols / 32; ++cb) {
@@ -766,17 +814,20 @@ __global__ void __launch_bounds__(128) head_gather_kernel(const uint16_t* h, int
 
 // ------------------------------------------------------------------- finish
 //
-// A split contraction's sums joined in split order, and dH's rows from them.
-// blockIdx.x: (tile, CTA of it); blockIdx.y: 32 of a thread's 128 columns.
+// The parts of a tile joined in order, and dH's rows from them.  blockIdx.x:
+// (tile of those that fill no wave, CTA of it); blockIdx.y: 32 of a thread's 128
+// columns.
 __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_constant__ HeadArgs a) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int ctas = a.pair ? 2 : 1;
   const int T = operand_rows(a);
   const int mtiles = (T + 128 * ctas - 1) / (128 * ctas);
-  const int mn = mtiles * a.ntiles;
-  const int tile = blockIdx.x / ctas, rank = blockIdx.x % ctas;
-  if (tile >= mn) return;
+  const HeadTail tail = head_tail(mtiles * a.ntiles, a.kfull, a.workers);
+  const int j = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  if (j >= tail.rest || tail.parts == 1) return;
+  const int tile = tail.full * a.workers + j;
+  const int slot = (a.first && a.last ? 0 : tail.full * a.workers) + j * tail.parts;
   int m, n;
   head_tile<true>(tile, mtiles, a.ntiles, m, n);
   const int et = threadIdx.x, w = et >> 5, lane = et & 31;
@@ -784,11 +835,11 @@ __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_co
   const int d = n * kHeadTile + (w >> 2) * kSumCols + blockIdx.y * 32;
   if (row >= T || d >= a.ncols) return;
   const int t = a.rows ? __ldcg(a.rows + row) : row;
-  const float4* sum = reinterpret_cast<const float4*>(a.acc) + static_cast<int64_t>(blockIdx.x) * kSumBlock +
-                      static_cast<int>(blockIdx.y) * 8 * kSumStride + et;
+  const int at_row = static_cast<int>(blockIdx.y) * 8 * kSumStride + et;
   float l[32] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const float4* at = sum + static_cast<int64_t>(s) * mn * ctas * kSumBlock;
+  for (int part = 0; part < tail.parts; ++part) {
+    const float4* at = reinterpret_cast<const float4*>(a.acc) +
+                       (static_cast<int64_t>(slot + part) * ctas + rank) * kSumBlock + at_row;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float4 o = __ldcg(at + j * kSumStride);
@@ -973,8 +1024,12 @@ static cudaError_t launch_head_gemm_impl(const CUtensorMap& tm_a, const CUtensor
   using P = HeadPlan<MODE, PAIR, NF4>;
   static uint64_t done = 0;
   if (cudaError_t e = allow_smem(head_gemm_kernel<MODE, PAIR, NF4>, P::kSmem, done)) return e;
-  const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles * a.splits;
-  const int workers = static_cast<int>(std::min<int64_t>(tiles, head_workers(PAIR)));
+  const int tiles = a.mtiles * a.ntiles;
+  int workers = std::min(tiles, head_workers(PAIR));
+  if (MODE == kHeadGrad) {
+    const HeadTail t = head_tail(tiles, a.kfull, a.workers);
+    workers = t.full > 0 || t.help || a.nrows ? a.workers : t.rest * t.parts;
+  }
   return launch_kernel(head_gemm_kernel<MODE, PAIR, NF4>, dim3((PAIR ? 2 : 1) * workers), dim3(P::kThreads), P::kSmem,
                        stream, dim3(PAIR ? 2 : 1, 1, 1), tm_a, tm_b, a);
 }
@@ -998,9 +1053,9 @@ cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMa
   }
 }
 
-cudaError_t launch_head_finish(const HeadArgs& a, cudaStream_t stream) {
-  return launch_kernel(head_finish_kernel, dim3((a.pair ? 2 : 1) * a.mtiles * a.ntiles, kSumCols / 32),
-                       dim3(kSumStride), 0, stream, dim3(1, 1, 1), a);
+cudaError_t launch_head_finish(const HeadArgs& a, int tiles, cudaStream_t stream) {
+  return launch_kernel(head_finish_kernel, dim3((a.pair ? 2 : 1) * tiles, kSumCols / 32), dim3(kSumStride), 0, stream,
+                       dim3(1, 1, 1), a);
 }
 
 cudaError_t launch_head_index(const int64_t* labels, int64_t ignore, int64_t vocab, int64_t T, int32_t* rows,

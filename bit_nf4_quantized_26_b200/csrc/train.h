@@ -50,6 +50,42 @@ enum HeadMode {
 // CTA pairs, or CTAs, of a persistent launch: one per TPC, one per SM.
 constexpr int head_workers(bool pair) { return pair ? 74 : 148; }
 
+// How dH's tiles go over the workers: whole tiles in turn, `full` each, then
+// the `rest` that do not fill a wave, in parts of their contraction where the
+// parts' sums (about 24 stages' time to write and join) cost less than the idle
+// workers.  Up to half a wave: as many slices of `per` stages as there are
+// workers for.  More: a worker a tile does the first `per` stages, and every
+// worker left over the remaining ones of `help` tiles.  Either way the workers
+// on one operand's rows walk the same stages together (ranges that start
+// anywhere balance better, and read the operands from memory once per tile:
+// 2048 x 50000 x 1024 412 us against 375).  8192 x 50257 x 1024, three quarters
+// of the tokens counting: 96 tiles, 92 us a piece in parts, 105 whole.
+struct HeadTail {
+  int full, rest, parts, per, help;
+};
+constexpr int kHeadPartCost = 24;
+
+inline __host__ __device__ HeadTail head_tail(int tiles, int kst, int workers) {
+  HeadTail t{tiles / workers, tiles % workers, 1, kst, 0};
+  if (t.rest == 0) return t;
+  int parts = workers / t.rest, per = 0, help = 0;
+  if (parts > 1) {
+    per = (kst + parts - 1) / parts;
+    per = per < 8 ? 8 : per;
+    parts = (kst + per - 1) / per;
+  } else {
+    help = (t.rest + workers - t.rest - 1) / (workers - t.rest);
+    per = (kst * help + help) / (help + 1);
+    parts = 2;
+  }
+  if (per + kHeadPartCost < kst) {
+    t.parts = parts;
+    t.per = per;
+    t.help = help;
+  }
+  return t;
+}
+
 struct HeadArgs {
   int pair, nf4;          // which kernel: tiles of 256 tokens on CTA pairs; (single CTAs) W from its codes
   int T;                  // tokens
@@ -63,7 +99,7 @@ struct HeadArgs {
   int ncols;              // columns of this product: the piece's vocabulary rows, or dim (Grad)
   int kst;                // 64-deep contraction stages
   int kchunk;             // stages summed in one accumulator
-  int splits, kper;       // Grad: slices of the contraction and their stages (else 1, kst)
+  int kfull, workers;     // Grad: stages of a full piece, and CTA pairs or CTAs, for head_tail
   int b_row0;             // the piece's first row in W's tensor map
   int64_t v0;             // the piece's first vocabulary index
   int wrows;              // the piece's vocabulary rows
@@ -81,7 +117,7 @@ struct HeadArgs {
   int zero_count;
   // Grad
   int first, last;        // of the pieces
-  float* acc;             // fp32 sums of the pieces so far, and of each split (blocked by tile)
+  float* acc;             // fp32 sums of the pieces so far, and of parts (blocked by tile)
   const float* alpha;     // [T] factor of the sum so far (null: 1)
   uint16_t* dh;           // [T, ldd]
   int64_t ldd;
@@ -110,8 +146,9 @@ cudaError_t launch_head_index(const int64_t* labels, int64_t ignore, int64_t voc
 cudaError_t launch_head_gather(const uint16_t* h, int64_t ldh, int64_t T, int64_t dim, const int32_t* place,
                                uint16_t* out, uint16_t* dh, int64_t ldd, cudaStream_t stream);
 
-// Grad with splits > 1: joins the splits' sums after the last piece.
-cudaError_t launch_head_finish(const HeadArgs& a, cudaStream_t stream);
+// Joins the parts of Grad's tiles after the last piece; `tiles`: an upper bound
+// of those in parts.
+cudaError_t launch_head_finish(const HeadArgs& a, int tiles, cudaStream_t stream);
 
 // Joins the per-tile statistics of every row; see head_loss.cu.
 struct HeadCombineArgs {

@@ -153,8 +153,8 @@ typedef struct {
  * fewer columns where that fills the GPU; forward, step), a piece of the
  * probabilities (backward, step: about 128 MB in bf16, at least 2048 columns),
  * the rows of H that count (backward of larger calls: bf16 [T, dim]), fp32 sums
- * [T, dim] (with several pieces, and for few tokens one per slice of
- * the contraction), and, for more than 128 tokens, a dequantised piece of an
+ * [T, dim] (with several pieces) and of tiles of dH whose contraction is
+ * divided (at most 39 MB), and, for more than 128 tokens, a dequantised piece of an
  * NF4 head (at most 128 MB, at least 2048 rows).
  * Accuracy: exact bf16 inputs, fp32 accumulation and softmax; the probabilities
  * enter the second product as bf16 (label term subtracted in fp32 first); dH

@@ -82,7 +82,8 @@ class Ref:
 
 # tokens, vocabulary, width: one of each, odd ones, tile borders, widths that end inside a stage
 SHAPES = [(1, 1, 8), (1, 1000, 64), (3, 257, 72), (129, 256, 256), (200, 1003, 520), (256, 512, 64), (257, 255, 192),
-          (700, 3001, 1024), (60, 33000, 256), (128, 4000, 328), (16, 40001, 640), (380, 20000, 512), (300, 9000, 320)]
+          (700, 3001, 1024), (60, 33000, 256), (128, 4000, 328), (16, 40001, 640), (380, 20000, 512), (300, 9000, 320),
+          (2000, 9000, 1304)]  # the last: 48 tiles of dH on 74 pairs, each in two parts
 
 
 @pytest.mark.parametrize("T,V,D", SHAPES)
@@ -112,10 +113,10 @@ def test_loss_and_gradient_match_oracle(T, V, D):
 
 
 
-@pytest.mark.parametrize("T,V,D", [(16500, 4500, 64), (33000, 2500, 128)])
+@pytest.mark.parametrize("T,V,D", [(16500, 4500, 64), (33000, 2500, 128), (1000, 70000, 64), (2048, 36000, 336)])
 def test_several_pieces(T, V, D):
-    """Token counts at which the vocabulary runs in more than one piece: the
-    fp32 sum carried between pieces."""
+    """Sizes at which the vocabulary runs in more than one piece: the fp32 sum
+    carried between pieces (whole tiles', and parts' whose last piece is shorter)."""
     assert q.qlora_head_loss_workspace_size(T, V, D, False, q.HEAD_BWD) < 2 * T * V  # not the whole operand
     h, w, y = _case(T, V, D, seed=1, lean=10.0)
     rows = np.unique(np.linspace(0, T - 1, 400).astype(int))
@@ -135,7 +136,7 @@ def test_several_pieces(T, V, D):
 
 
 @pytest.mark.parametrize("scale", [30.0, 200.0])
-@pytest.mark.parametrize("T,V,D", [(100, 2000, 256), (16500, 4500, 64)])
+@pytest.mark.parametrize("T,V,D", [(100, 2000, 256), (16500, 4500, 64), (1000, 70000, 64)])
 def test_large_logits_take_other_references(T, V, D, scale):
     """Logits of some hundreds, of either sign and far apart between tiles and
     pieces: rows whose tiles have different references, a row far below zero."""
@@ -253,7 +254,8 @@ def test_well_predicted_tokens_keep_their_gradient():
 
 @pytest.mark.parametrize("T,V,D,centred", [(5, 1001, 64, False), (300, 2300, 512, True), (64, 40000, 2048, False),
                                            (17000, 4500, 128, True), (128, 300, 64, False), (129, 5000, 192, True),
-                                           (512, 1000, 448, False), (127, 70001, 64, True), (3, 1, 64, False), (70, 63, 128, True), (380, 20000, 512, False), (1, 30000, 1024, False)])
+                                           (512, 1000, 448, False), (127, 70001, 64, True), (3, 1, 64, False), (70, 63, 128, True), (380, 20000, 512, False), (1, 30000, 1024, False),
+                                           (8, 6000, 20480, False)])
 def test_nf4_head(T, V, D, centred):
     """An NF4 head is the bf16 head of its dequantised weight.  The logits are the
     same bits; the pieces, and so the order in which a row's exponentials are
