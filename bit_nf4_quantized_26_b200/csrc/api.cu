@@ -1589,11 +1589,9 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     return QLORA_ERR_CUDA;
   if (p.compact) {
     ProfScope ps(kKHeadRows, cs);
-    if (qlora_status st =
-            from_cuda(launch_head_index(c.labels, c.ignore, V, T, rows, place, nrows, d_status, cs)))
-      return st;
-    if (gather)
-      if (qlora_status st = from_cuda(launch_head_gather(c.H, c.ldh, T, D, place, hrows, c.dH, c.lddh, cs))) return st;
+    const HeadRowsArgs r{c.labels, c.ignore, V,   T,     0, rows, place, nrows, d_status,
+                         c.H,      c.ldh,    D,   gather ? hrows : nullptr,     c.dH,  c.lddh};
+    if (qlora_status st = from_cuda(launch_head_rows(r, cs))) return st;
   }
   if (gather) {
     a.nrows = nrows;

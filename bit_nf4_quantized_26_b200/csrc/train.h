@@ -139,12 +139,18 @@ struct HeadArgs {
 cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMap& tm_b, const HeadArgs& a,
                              cudaStream_t stream);
 
-// rows [T], place [T], nrows [1] of the tokens that count.
-cudaError_t launch_head_index(const int64_t* labels, int64_t ignore, int64_t vocab, int64_t T, int32_t* rows,
-                              int32_t* place, int32_t* nrows, int32_t* status, cudaStream_t stream);
-// Their rows of h to `out` [T, dim]; zeros to the other rows of dh.
-cudaError_t launch_head_gather(const uint16_t* h, int64_t ldh, int64_t T, int64_t dim, const int32_t* place,
-                               uint16_t* out, uint16_t* dh, int64_t ldd, cudaStream_t stream);
+// The tokens that count: rows [T], place [T], nrows [1]; with `out` their rows
+// of h to out [T, dim], and zeros to the other rows of dh (which may be h).
+struct HeadRowsArgs {
+  const int64_t* labels;
+  int64_t ignore, vocab, T, chunk;
+  int32_t *rows, *place, *nrows, *status;
+  const uint16_t* h;
+  int64_t ldh, dim;
+  uint16_t *out, *dh;
+  int64_t ldd;
+};
+cudaError_t launch_head_rows(HeadRowsArgs a, cudaStream_t stream);
 
 // Joins the parts of Grad's tiles after the last piece; `tiles`: an upper bound
 // of those in parts.
