@@ -9,10 +9,11 @@
 // The logits exist only as fp32 tiles in tensor memory.  One GEMM kernel makes
 // every product; what its epilogue does with a tile is the mode:
 //
-//   Loss  per row and half tile the maximum m and sum exp(l - m): 8 bytes
+//   Loss  per row and half tile the maximum m and sum exp(l - m): 8 bytes (the
+//         label's column apart, its logit kept)
 //   Prob  exp(l - lse), less 1 at the label (in fp32), rounded to bf16
-//   Exp   exp(l - ref), 0 at the label, rounded to bf16, and (ref, sum): the
-//         gradient's operand before lse is known.  ref is 0 while the maximum
+//   Exp   exp(l - ref), 0 at the label, rounded to bf16, and (ref, sum), the
+//         label apart: the gradient's operand before lse is known.  ref is 0 while the maximum
 //         of the row's half tile lies within +-40 (exp then stays far inside
 //         bf16's and fp32's range, and the reference costs no precision: both
 //         types float), else that maximum
@@ -22,9 +23,13 @@
 // The step joins each piece's (ref, sum) per row (head_combine_kernel); rows
 // whose tiles took different references have those tiles' exponentials
 // rescaled to a common one, and `alpha` rescales the sum of earlier pieces:
-// both leave ordinary rows alone.  The label's column is left out of Exp and
+// both leave ordinary rows alone.
+//
+// The label's column stays apart: loss = log1p(sum over the others of exp(l -
+// l_label)), which keeps its digits where the label dominates (lse - l_label
+// would leave 1e-6 of a logit of 14, whatever the loss), and its term of dH is
 // added after the last piece in fp32, (p_label - 1) W[label] with p_label - 1 =
-// expm1(l_label - lse): rounding p to bf16 first would lose the gradient of a
+// expm1(-loss): rounding p to bf16 first would lose the gradient of a
 // well-predicted token.
 #include <algorithm>
 
@@ -126,6 +131,18 @@ __device__ __forceinline__ float max_all(const float (&l)[N]) {
 #pragma unroll
   for (int j = 4; j < N; ++j) m[j & 3] = fmaxf(m[j & 3], l[j]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Element `at` of l, which becomes -inf there: the label's column leaves its tile.
+template <int N>
+__device__ __forceinline__ float take(float (&l)[N], int at) {
+  float z = 0.0f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    z = j == at ? l[j] : z;
+    l[j] = j == at ? -INFINITY : l[j];
+  }
+  return z;
 }
 
 // Element `at` of l (0 if there is none there).
@@ -687,24 +704,23 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
           if (j >= nv) l[j] = -INFINITY;
       }
       if (MODE == kHeadLoss) {
+        if (lj >= 0) a.label_logit[t] = take(l, lj);
         const float mx = max_all(l);
         const float base = mx == -INFINITY ? 0.0f : mx * kLog2e;
-        if (lj >= 0) a.label_logit[t] = pick(l, lj);
         float p[4] = {};
 #pragma unroll
         for (int j = 0; j < kCols; ++j) p[j & 3] += exp2_fast(fmaf(l[j], kLog2e, -base));
         if (rok) a.part[static_cast<int64_t>(2 * n + half) * a.T + t] = make_float2(mx, (p[0] + p[1]) + (p[2] + p[3]));
       } else if (MODE == kHeadExp) {
+        if (lj >= 0) a.label_logit[t] = take(l, lj);
         const float mx = max_all(l);
         const float ref = (fabsf(mx) <= kRefRange || mx == -INFINITY) ? 0.0f : mx;
         const float base = ref * kLog2e;
-        if (lj >= 0) a.label_logit[t] = pick(l, lj);
         float p[4] = {};
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
           l[j] = exp2_fast(fmaf(l[j], kLog2e, -base));
           p[j & 3] += l[j];
-          if (j == lj) l[j] = 0.0f;
         }
         if (rok) {
           a.part[static_cast<int64_t>(2 * n + half) * a.T + t] = make_float2(ref, (p[0] + p[1]) + (p[2] + p[3]));
@@ -858,7 +874,7 @@ __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_co
 // ------------------------------------------------------------------ combine
 //
 // Joins the (reference, sum) pairs of a row's parts (half tiles): R = max ref,
-// S = sum of s exp(ref - R).  Step: R and S run over the pieces, exponentials of
+// S = sum of s exp(ref - R), of all columns but the label's.  Step: R and S run over the pieces, exponentials of
 // parts whose reference is not R are rescaled in place (rows with logits beyond
 // +-40 only), and alpha = exp(R_old - R).  With the last piece: lse, loss, and
 // the mean in fp64 (per-block sums, added in block order by the block that
@@ -939,15 +955,20 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
       if (a.last && rok) {
         const int64_t label = a.labels[t];
         counted = counts(label, a.ignore, a.vocab);
-        const float lse = R + logf(S);
-        const float z = counted ? __ldcg(a.label_logit + t) : lse;
-        const float loss = counted ? lse - z : 0.0f;
+        float lse = R + logf(S), loss = 0.0f;
+        if (counted) {
+          const float z = __ldcg(a.label_logit + t), top = fmaxf(R, z);
+          // exp(l - l_label) over the others; where that is near overflow, its log is log S + R - l_label
+          const float x = S * expf(R - z);
+          loss = x < 1e30f ? log1pf(x) : (R - z) + logf(S);
+          lse = top + logf(S * expf(R - top) + expf(z - top));  // (no others: R = -inf, S = 0)
+          if (a.row_sum) {
+            a.row_sum[t] = S + expf(z - R);  // inf: the others' share is below 1e-38
+            a.p_label[t] = expm1f(-loss);
+          }
+        }
         a.lse[t] = lse;
         a.loss[t] = loss;
-        if (a.row_sum) {
-          a.row_sum[t] = S;
-          a.p_label[t] = expm1f(z - lse);
-        }
         sum = loss;
         if (a.status) {
           if (counted && !isfinite(lse)) atomicOr(a.status, QLORA_DEV_NONFINITE);

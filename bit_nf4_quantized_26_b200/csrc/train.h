@@ -109,7 +109,7 @@ struct HeadArgs {
   const int64_t* labels;
   int64_t ignore;
   float* label_logit;     // Loss, Exp: [T]
-  float2* part;           // Loss, Exp: (reference, sum of exponentials) [half tile][T], from the piece's first
+  float2* part;         // Loss, Exp: (reference, sum of the others' exponentials) [half tile][T], from the piece's first
   const float* lse;       // Prob: [T]
   uint16_t* g;            // Prob, Exp: [rows, ldg]
   int64_t ldg;

@@ -156,7 +156,8 @@ typedef struct {
  * [T, dim] (with several pieces) and of tiles of dH whose contraction is
  * divided (at most 39 MB), and, for more than 128 tokens, a dequantised piece of an
  * NF4 head (at most 128 MB, at least 2048 rows).
- * Accuracy: exact bf16 inputs, fp32 accumulation and softmax; the probabilities
+ * Accuracy: exact bf16 inputs, fp32 accumulation and softmax; a small loss keeps
+ * its digits (the label's logit stays out of the sum); the probabilities
  * enter the second product as bf16 (label term subtracted in fp32 first); dH
  * within 5e-3 relative Frobenius error of the fp64 gradient.
  */

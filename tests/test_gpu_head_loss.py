@@ -252,6 +252,41 @@ def test_well_predicted_tokens_keep_their_gradient():
     assert np.all(err <= 2 * 2.0 ** -8 + r.loss_tol / small)
 
 
+@pytest.mark.parametrize("T,V,D,sign", [(3, 500, 256, 1.0), (64, 3000, 256, 1.0), (300, 9000, 320, 1.0),
+                                        (1000, 70000, 64, 1.0), (64, 3000, 256, -1.0)])
+def test_losses_keep_their_digits(T, V, D, sign):
+    """Losses from below 1e-7 to some tens, label logits far above the others (or far
+    below).  With x = sum over the others of exp(l_v - l_label), loss =
+    log1p(x): x is off by rel (the two logits' errors and the exponentials'),
+    log1p by no more than that relative and its own 2^-22; the reference is one
+    step of fp32 around.  The label's p - 1 = -x / (1 + x) likewise."""
+    h, w, y = _case(T, V, D, seed=14, ignored=0.1)
+    lead = torch.linspace(2.0, 38.0, T)[:, None]
+    safe = y.clamp(min=0)
+    unit = w[safe].float() / (w[safe].float() ** 2).sum(1, keepdim=True)
+    h = (sign * lead * unit + 0.1 * h.float()).to(torch.bfloat16)
+    rows = np.unique(np.linspace(0, T - 1, 200).astype(int))
+    r = Ref(h[rows], w, y[rows])
+    c = hl.counted(r.y, V)
+    z = hl._f64(bits(h[rows])) @ hl._f64(bits(w)).T
+    zy = z[np.arange(rows.size), np.where(c, r.y, 0)]
+    others = np.exp(z - zy[:, None])
+    others[np.arange(rows.size), np.where(c, r.y, 0)] = 0.0
+    loss = np.where(c, np.log1p(others.sum(1)), 0.0)
+    if sign > 0:
+        assert loss[c].min() < 1e-7 and loss[c].max() > 1.0  # the oracle's: 1.3e-8 at 70000 x 64, far less elsewhere
+    H, W, Y, sel = h.cuda(), w.cuda(), y.cuda(), torch.from_numpy(rows).cuda()
+    tol = (r.rel + 2.0 ** -21) * loss
+    got = q.qlora_head_loss_step(H, W, Y, weight=torch.ones(T, device="cuda"))
+    for out in (q.qlora_head_loss_fwd(H, W, Y), got):
+        assert np.all(np.abs(out[0][sel].double().cpu().numpy() - loss) <= tol)
+        assert np.all(np.abs(out[1][sel].double().cpu().numpy() - r.lse) <= r.lse_tol)
+    g = np.abs(r.p)
+    ref = r.p @ r.W
+    bound = (r.rel[:, None] + 2.0 ** -21 + 2 * 2.0 ** -8 * 1.01) * g @ np.abs(r.W) + 2.0 ** -8 * np.abs(ref) + 1e-37
+    assert np.all(np.abs(got[3][sel].double().cpu().numpy() - ref)[c] <= bound[c])
+
+
 @pytest.mark.parametrize("T,V,D,centred", [(5, 1001, 64, False), (300, 2300, 512, True), (64, 40000, 2048, False),
                                            (17000, 4500, 128, True), (128, 300, 64, False), (129, 5000, 192, True),
                                            (512, 1000, 448, False), (127, 70001, 64, True), (3, 1, 64, False), (70, 63, 128, True), (380, 20000, 512, False), (1, 30000, 1024, False),
