@@ -1352,7 +1352,7 @@ struct HeadPlanHost {
   int64_t kfull = 0;             // 64-deep stages of a piece's dH contraction
   int64_t tails = 0;             // dH's tiles that may be in parts
   int64_t cost = 0;              // of the products: waves x 64-deep stages x columns
-  size_t off_cnt = 0, off_z = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_sum = 0, off_pl = 0;
+  size_t off_cnt = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_sum = 0, off_pl = 0;
   size_t off_g = 0, off_acc = 0, off_w = 0, off_rows = 0, off_place = 0, off_nrows = 0, off_h = 0, total = 0;
   // dH's products take the rows that count only (the backward's both, the
   // step's second; losses need every row's lse).  Listing and gathering them
@@ -1424,7 +1424,6 @@ static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, i
   if (op != QLORA_HEAD_BWD) {
     const int64_t parts = (op == QLORA_HEAD_FWD ? p.pieces : 1) * p.parts;
     p.off_cnt = take(8);
-    p.off_z = take(4 * t);
     p.off_part = take(8 * t * static_cast<size_t>(parts));
     p.off_bsum = take(8 * static_cast<size_t>(head_combine_blocks(T)));
   }
@@ -1560,11 +1559,13 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
   a.head = hd;
   HeadCombineArgs cb{};
   if (op != QLORA_HEAD_BWD) {
-    a.label_logit = reinterpret_cast<float*>(at(p.off_z));
     a.zero = reinterpret_cast<uint32_t*>(at(p.off_cnt));
     a.zero_count = 2;
     cb.T = a.T;
-    cb.label_logit = a.label_logit;
+    cb.h = c.H;
+    cb.ldh = c.ldh;
+    cb.head = hd;
+    cb.tab = a.tab;
     cb.labels = c.labels;
     cb.ignore = c.ignore;
     cb.vocab = V;
@@ -1634,7 +1635,7 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     a.kst = static_cast<int>(cdiv(D, 64));
     // 64-deep stages per accumulator (head_loss.cu): a product of few tokens
     // waits for the weight, and short chunks cost it nothing
-    a.kchunk = op == QLORA_HEAD_BWD ? 64 : (p.pair ? 12 : 4);
+    a.kchunk = op == QLORA_HEAD_BWD ? 16 : (p.pair ? 12 : 4);
     float2* part = reinterpret_cast<float2*>(at(p.off_part));
     a.part = op == QLORA_HEAD_FWD ? part + i * p.parts * T : part;
     {

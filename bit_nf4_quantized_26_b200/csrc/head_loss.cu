@@ -10,7 +10,7 @@
 // every product; what its epilogue does with a tile is the mode:
 //
 //   Loss  per row and half tile the maximum m and sum exp(l - m): 8 bytes (the
-//         label's column apart, its logit kept)
+//         label's column apart: head_combine_kernel makes its logit)
 //   Prob  exp(l - lse), less 1 at the label (in fp32), rounded to bf16
 //   Exp   exp(l - ref), 0 at the label, rounded to bf16, and (ref, sum), the
 //         label apart: the gradient's operand before lse is known.  ref is 0 while the maximum
@@ -131,18 +131,6 @@ __device__ __forceinline__ float max_all(const float (&l)[N]) {
 #pragma unroll
   for (int j = 4; j < N; ++j) m[j & 3] = fmaxf(m[j & 3], l[j]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-}
-
-// Element `at` of l, which becomes -inf there: the label's column leaves its tile.
-template <int N>
-__device__ __forceinline__ float take(float (&l)[N], int at) {
-  float z = 0.0f;
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    z = j == at ? l[j] : z;
-    l[j] = j == at ? -INFINITY : l[j];
-  }
-  return z;
 }
 
 // Element `at` of l (0 if there is none there).
@@ -333,7 +321,7 @@ struct Ring {
 // threads add each finished one to their registers, rounding to nearest, while
 // the next runs.  (512 deep costs the products 2-3%, 1024 nothing; 256 is free
 // for few tokens, whose products wait for W.)  Results rounded to bf16 take
-// longer ones: the backward's probabilities 4096, dH all of its
+// longer ones: the backward's probabilities 1024, dH all of its
 // tile's or part's contraction.
 //
 // Barriers (leader: the pair's first CTA, or the single one): full[s] (leader:
@@ -703,8 +691,12 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         for (int j = 0; j < kCols; ++j)
           if (j >= nv) l[j] = -INFINITY;
       }
+      if (MODE != kHeadProb && lj >= 0) {  // the label's column leaves the tile
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+          if (j == lj) l[j] = -INFINITY;
+      }
       if (MODE == kHeadLoss) {
-        if (lj >= 0) a.label_logit[t] = take(l, lj);
         const float mx = max_all(l);
         const float base = mx == -INFINITY ? 0.0f : mx * kLog2e;
         float p[4] = {};
@@ -712,7 +704,6 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         for (int j = 0; j < kCols; ++j) p[j & 3] += exp2_fast(fmaf(l[j], kLog2e, -base));
         if (rok) a.part[static_cast<int64_t>(2 * n + half) * a.T + t] = make_float2(mx, (p[0] + p[1]) + (p[2] + p[3]));
       } else if (MODE == kHeadExp) {
-        if (lj >= 0) a.label_logit[t] = take(l, lj);
         const float mx = max_all(l);
         const float ref = (fabsf(mx) <= kRefRange || mx == -INFINITY) ? 0.0f : mx;
         const float base = ref * kLog2e;
@@ -878,7 +869,13 @@ __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_co
 // parts whose reference is not R are rescaled in place (rows with logits beyond
 // +-40 only), and alpha = exp(R_old - R).  With the last piece: lse, loss, and
 // the mean in fp64 (per-block sums, added in block order by the block that
-// finishes last).  A block takes TB tokens; its threads split their parts.  TB
+// finishes last).  The label's logit is made here, in fp32 rounded to nearest:
+// the tensor core's drift grows with a logit, and the label's is the one that
+// stands out (with the tiles' own, losses of some tenths were 2-5e-6 off at dim
+// 640 to 4096; so, below 1e-6).  Made in the tiles it took the products 5-10%
+// (a wait for two rows in the epilogue, while the next chunk is due).  It reads
+// nothing of the kernel before, and runs while that ends.
+// A block takes TB tokens; its threads split their parts.  TB
 // is 32 (whole sectors of a part's row) or, for few tokens, where the chain of
 // loads is what takes the time, fewer, so that a thread has a few parts only.
 
@@ -894,6 +891,30 @@ __device__ __forceinline__ void join(float& R, float& S, float ref, float s) {
   R = top;
 }
 
+// A lane's share of the logit of label `label` for the row h: columns in runs
+// of 32, `parts` warps in turn.  fp32 sums rounded to nearest.
+__device__ __forceinline__ float label_dot(const HeadCombineArgs& a, const uint16_t* h, int64_t label, int part,
+                                           int parts, int lane) {
+  float z = 0.0f;
+  const int dim = static_cast<int>(a.head.dim);
+  for (int d = (part * 32 + lane) * 32; d < dim; d += 1024 * parts) {
+    const int n = min(32, dim - d);
+    float w[32];
+    load_head_row(a.head, a.tab, label, d, n, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 v = 8 * j < n ? __ldcg(reinterpret_cast<const uint4*>(h + d) + j) : make_uint4(0, 0, 0, 0);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z = fmaf(__uint_as_float(u[i] << 16), w[8 * j + 2 * i], z);
+        z = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), w[8 * j + 2 * i + 1], z);
+      }
+    }
+  }
+  return z;
+}
+
 }  // namespace
 
 template <int TB>
@@ -903,9 +924,22 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
   __shared__ bool last_block;
   __shared__ double sums[kCombineWarps];
   constexpr int kSlices = kCombineWarps * 32 / TB;
+  constexpr int kDotParts = TB < kCombineWarps ? kCombineWarps / TB : 1;  // warps on a token's label
+  __shared__ float dot[TB][kDotParts];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (a.last) {
+    for (int i = warp / kDotParts; i < TB && blockIdx.x * TB + i < a.T; i += kCombineWarps / kDotParts) {
+      const int64_t row = blockIdx.x * TB + i, label = a.labels[row];
+      float z = 0.0f;
+      if (counts(label, a.ignore, a.vocab))
+        z = label_dot(a, a.h + row * a.ldh, label, warp % kDotParts, kDotParts, lane);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+      if (lane == 0) dot[i][warp % kDotParts] = z;
+    }
+  }
   grid_dependency_wait();
   grid_dependents_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tok = threadIdx.x % TB, slice = threadIdx.x / TB;
   const int t0 = blockIdx.x * TB, t = t0 + tok;
   const bool rok = t < a.T;
@@ -957,7 +991,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
         counted = counts(label, a.ignore, a.vocab);
         float lse = R + logf(S), loss = 0.0f;
         if (counted) {
-          const float z = __ldcg(a.label_logit + t), top = fmaxf(R, z);
+          float z = dot[lane][0];
+          for (int i = 1; i < kDotParts; ++i) z += dot[lane][i];
+          const float top = fmaxf(R, z);
           // exp(l - l_label) over the others; where that is near overflow, its log is log S + R - l_label
           const float x = S * expf(R - z);
           loss = x < 1e30f ? log1pf(x) : (R - z) + logf(S);

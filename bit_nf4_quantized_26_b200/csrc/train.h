@@ -108,7 +108,6 @@ struct HeadArgs {
   int tw;                 // columns of a tile: a multiple of 32 up to 256, NF4 128 (Grad: 256)
   const int64_t* labels;
   int64_t ignore;
-  float* label_logit;     // Loss, Exp: [T]
   float2* part;         // Loss, Exp: (reference, sum of the others' exponentials) [half tile][T], from the piece's first
   const float* lse;       // Prob: [T]
   uint16_t* g;            // Prob, Exp: [rows, ldg]
@@ -161,7 +160,10 @@ struct HeadCombineArgs {
   int T, nparts;
   int part_cols;           // columns a part covers
   const float2* part;      // [nparts][T]
-  const float* label_logit;
+  const uint16_t* h;       // H [T, ldh], and the head: the label's logit
+  int64_t ldh;
+  qlora_head head;
+  Nf4Tables tab;
   const int64_t* labels;
   int64_t ignore;
   int64_t vocab;
