@@ -236,6 +236,35 @@ def test_rows_that_count_at_the_ends(case):
             Ref(h[k], w, y[k]).check_grad(d[k], np.full(len(k), 2.0 / len(k)), roundings=2)
 
 
+def test_rows_that_count_change_between_replays():
+    """Captured once, replayed with other labels: the rows that count, their
+    tiles and those tiles' parts are the replay's own."""
+    T, V, D = 600, 20000, 2304
+    assert 4.0 * T * V * D >= 1e11
+    h, w, y = _case(T, V, D, seed=15, ignored=0.0)
+    H, W, Y = h.cuda(), w.cuda(), y.cuda()
+    g, buf = torch.linspace(-1, 1, T, device="cuda"), torch.empty(T, dtype=torch.int64, device="cuda")
+    buf.copy_(Y)
+
+    def call():
+        step = q.qlora_head_loss_step(H, W, buf, weight=g)
+        return (*step, q.qlora_head_loss_bwd(H, W, buf, step[1], g))
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call()
+    for keep in (1.0, 0.5, 0.0, 0.1, 0.9):
+        buf.copy_(torch.where(torch.rand(T, generator=torch.Generator().manual_seed(int(10 * keep))) < keep, y,
+                              torch.full_like(y, -100)))
+        for o in outs:
+            o.fill_(7.0)
+        graph.replay()
+        for got, want in zip(outs, call()):
+            assert torch.equal(got, want)
+        assert not outs[3][buf == -100].any() and not outs[4][buf == -100].any()
+
+
 def test_well_predicted_tokens_keep_their_gradient():
     """p close to 1 at the label: the gradient is the small difference."""
     h, w, y = _case(64, 500, 256, seed=4, ignored=0.0)
