@@ -891,6 +891,11 @@ __device__ __forceinline__ void join(float& R, float& S, float ref, float s) {
   R = top;
 }
 
+__device__ __forceinline__ void store_mean(const HeadCombineArgs& a, double sum, int count) {
+  a.stats[0] = count > 0 ? static_cast<float>(sum / count) : 0.0f;
+  a.stats[1] = static_cast<float>(count);
+}
+
 // A lane's share of the logit of label `label` for the row h: columns in runs
 // of 32, `parts` warps in turn.  fp32 sums rounded to nearest.
 __device__ __forceinline__ float label_dot(const HeadCombineArgs& a, const uint16_t* h, int64_t label, int part,
@@ -1017,10 +1022,17 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
       const uint32_t votes = __ballot_sync(0xFFFFFFFFu, counted);
       if (lane == 0) {
-        a.block_sum[blockIdx.x] = sum;
-        atomicAdd(&a.counters[0], __popc(votes));
-        __threadfence();
-        last_block = atomicAdd(&a.counters[1], 1) == static_cast<int>(gridDim.x) - 1;
+        const int count = __popc(votes);
+        last_block = false;
+        if (gridDim.x == 1) {
+          a.counters[0] = count;
+          store_mean(a, sum, count);
+        } else {
+          a.block_sum[blockIdx.x] = sum;
+          atomicAdd(&a.counters[0], count);
+          __threadfence();
+          last_block = atomicAdd(&a.counters[1], 1) == static_cast<int>(gridDim.x) - 1;
+        }
       }
     }
   }
@@ -1067,9 +1079,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
     __syncthreads();
     if (threadIdx.x == 0) {
       for (int w = 1; w < kCombineWarps; ++w) sum += sums[w];
-      const int count = __ldcg(a.counters);
-      a.stats[0] = count > 0 ? static_cast<float>(sum / count) : 0.0f;
-      a.stats[1] = static_cast<float>(count);
+      store_mean(a, sum, __ldcg(a.counters));
     }
   }
 }
