@@ -237,12 +237,12 @@ qlora_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLORA_OK : QLO
 enum KernelId {
   kKQuantize = 0, kKDequantize, kKDown, kKFusedFwd, kKFinishFwd, kKLowFwd, kKLowFinish, kKDU, kKDB, kKFusedDX,
   kKDA, kKAdamW8, kKDropout, kKDropoutDx, kKActQuantize, kKActDequantize, kKActDA, kKHeadLogits, kKHeadGrad,
-  kKHeadCombine, kKHeadRows, kKCount
+  kKHeadCombine, kKHeadRows, kKHeadLabel, kKCount
 };
 const char* const kKernelNames[kKCount] = {
     "nf4_quantize", "nf4_dequantize", "lora_down", "fused_fwd", "finish_fwd", "lowm_fwd", "lowm_finish",
     "lora_du", "lora_db", "fused_dx", "lora_da", "adamw8", "dropout", "dropout_dx", "act8_quantize",
-    "act8_dequantize", "act8_da", "head_logits", "head_grad", "head_combine", "head_rows"};
+    "act8_dequantize", "act8_da", "head_logits", "head_grad", "head_combine", "head_rows", "head_label"};
 
 struct ProfRecord {
   int id;
@@ -1431,9 +1431,9 @@ static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, i
     p.off_run = take(8 * t);
     p.off_alpha = take(4 * t);
     p.off_sum = take(4 * t);
-    p.off_pl = take(4 * t);
   }
   if (op != QLORA_HEAD_FWD) {
+    p.off_pl = take(4 * t);
     p.off_g = take(2 * t * static_cast<size_t>(p.ldg));
   }
   p.compact = op != QLORA_HEAD_FWD && T > 256 && 4.0 * T * V * D >= 1e11;
@@ -1680,10 +1680,16 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
         d.nrows = nrows;
         d.rows = rows;
       }
+      d.p_label = reinterpret_cast<float*>(at(p.off_pl));
+      if (op == QLORA_HEAD_BWD && last) {
+        const HeadLabelArgs la{c.labels, c.ignore, V,        T, c.H, c.ldh, hd, a.tab, c.lse_in,
+                               reinterpret_cast<float*>(at(p.off_pl)), 0};
+        ProfScope ps(kKHeadLabel, cs);
+        if (qlora_status st = from_cuda(launch_head_label(la, cs))) return st;
+      }
       if (op == QLORA_HEAD_STEP) {
         d.alpha = cb.alpha;
         d.row_sum = cb.row_sum;
-        d.p_label = cb.p_label;
         d.weight = c.weight;
         d.scale = c.scale;
         d.count = cb.counters;

@@ -11,7 +11,7 @@
 //
 //   Loss  per row and half tile the maximum m and sum exp(l - m): 8 bytes (the
 //         label's column apart: head_combine_kernel makes its logit)
-//   Prob  exp(l - lse), less 1 at the label (in fp32), rounded to bf16
+//   Prob  exp(l - lse), 0 at the label, rounded to bf16
 //   Exp   exp(l - ref), 0 at the label, rounded to bf16, and (ref, sum), the
 //         label apart: the gradient's operand before lse is known.  ref is 0 while the maximum
 //         of the row's half tile lies within +-40 (exp then stays far inside
@@ -29,8 +29,8 @@
 // l_label)), which keeps its digits where the label dominates (lse - l_label
 // would leave 1e-6 of a logit of 14, whatever the loss), and its term of dH is
 // added after the last piece in fp32, (p_label - 1) W[label] with p_label - 1 =
-// expm1(-loss): rounding p to bf16 first would lose the gradient of a
-// well-predicted token.
+// expm1(-loss), in the backward expm1(l_label - lse): rounding p to bf16 first
+// would lose the gradient of a well-predicted token.
 #include <algorithm>
 
 #include "train.h"
@@ -133,15 +133,6 @@ __device__ __forceinline__ float max_all(const float (&l)[N]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// Element `at` of l (0 if there is none there).
-template <int N>
-__device__ __forceinline__ float pick(const float (&l)[N], int at) {
-  float z = 0.0f;
-#pragma unroll
-  for (int j = 0; j < N; ++j) z = j == at ? l[j] : z;
-  return z;
-}
-
 // 32 bf16 (64 bytes, 16-byte aligned) from fp32; `n` valid (a multiple of 8).
 __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32], int n) {
 #pragma unroll
@@ -230,16 +221,16 @@ struct HeadItems {
   }
 };
 
-// dH_t = ca * (the row's sum over the vocabulary) + cl * W[label].
+// dH_t = ca * (the row's sum over the vocabulary but the label) + cl * W[label].
 __device__ __forceinline__ void grad_row_factors(const HeadArgs& a, int t, float& ca, float& cl) {
+  float g;
   if (a.row_sum) {
-    const float g = a.weight ? a.scale * __ldcg(a.weight + t) : a.scale / static_cast<float>(__ldcg(a.count));
+    g = a.weight ? a.scale * __ldcg(a.weight + t) : a.scale / static_cast<float>(__ldcg(a.count));
     ca = g / __ldcg(a.row_sum + t);
-    cl = g * __ldcg(a.p_label + t);
   } else {
-    ca = a.stats ? __ldcg(a.dloss) / __ldcg(a.stats + 1) : __ldcg(a.dloss + t);
-    cl = 0.0f;
+    g = ca = a.stats ? __ldcg(a.dloss) / __ldcg(a.stats + 1) : __ldcg(a.dloss + t);
   }
+  cl = g * __ldcg(a.p_label + t);
 }
 
 // Columns d .. d + 31 of row `row` of the head as fp32 (`n` valid, a multiple of 8).
@@ -271,20 +262,50 @@ __device__ __forceinline__ void load_head_row(const qlora_head& h, const Nf4Tabl
   }
 }
 
+// A lane's share of the logit of label `label` for the row h: runs of 8
+// columns, `parts` warps in turn.  fp32 sums rounded to nearest.
+__device__ __forceinline__ float label_dot(const qlora_head& head, const Nf4Tables& tab, const uint16_t* h,
+                                           int64_t label, int part, int parts, int lane) {
+  float z = 0.0f;
+  const int dim = static_cast<int>(head.dim);
+  auto add = [&z](const uint4& x, const uint4& y) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), z);
+      z = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), z);
+    }
+  };
+  const int d0 = (part * 32 + lane) * 8, step = parts * 256;
+  if (head.w) {
+    const uint16_t* w = head.w + label * head.ld;
+#pragma unroll 4
+    for (int d = d0; d < dim; d += step)
+      add(__ldcg(reinterpret_cast<const uint4*>(h + d)), __ldg(reinterpret_cast<const uint4*>(w + d)));
+  } else {
+    const Nf4Mean mean = nf4_load_mean(head.mean);
+#pragma unroll 2
+    for (int d = d0; d < dim; d += step) {
+      const int64_t e = label * head.dim + d, b = e >> 6;
+      const Nf4Lut lut = nf4_make_lut(tab, nf4_block_scale(__ldg(head.c8 + b), __ldg(head.s2 + (b >> 8)), mean));
+      add(__ldcg(reinterpret_cast<const uint4*>(h + d)),
+          nf4_lookup8(__ldg(reinterpret_cast<const uint32_t*>(head.codes + (e >> 1))), lut));
+    }
+  }
+  return z;
+}
+
 // Columns d .. d + 31 (`n` of them valid) of dH's row t from its sums l.
 __device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t label, bool counted, float ca, float cl,
                                              int d, int n, float (&l)[32]) {
   if (!counted) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) l[j] = 0.0f;
-  } else if (a.row_sum) {
+  } else {
     float w[32];
     load_head_row(a.head, a.tab, label, d, n, w);
 #pragma unroll
     for (int j = 0; j < 32; ++j) l[j] = fmaf(cl, w[j], ca * l[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) l[j] *= ca;
   }
   store_bf16x32(a.dh + static_cast<int64_t>(t) * a.ldd + d, l, n);
 }
@@ -691,7 +712,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         for (int j = 0; j < kCols; ++j)
           if (j >= nv) l[j] = -INFINITY;
       }
-      if (MODE != kHeadProb && lj >= 0) {  // the label's column leaves the tile
+      if (lj >= 0) {  // the label's column leaves the tile
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
           if (j == lj) l[j] = -INFINITY;
@@ -721,12 +742,8 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
       } else if (MODE == kHeadProb) {
         const float lse = rok ? __ldcg(a.lse + t) : 0.0f;
         const float base = lse * kLog2e;
-        const float pl = lj >= 0 ? expm1f(pick(l, lj) - lse) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          l[j] = counted ? exp2_fast(fmaf(l[j], kLog2e, -base)) : 0.0f;
-          if (j == lj) l[j] = pl;
-        }
+        for (int j = 0; j < kCols; ++j) l[j] = counted ? exp2_fast(fmaf(l[j], kLog2e, -base)) : 0.0f;
         if (rok) {
           store_bf16(a.g + static_cast<int64_t>(row) * a.ldg + n0, hw, l);
           if (n0 == 0 && a.v0 == 0 && !counted && label != a.ignore && a.status) atomicOr(a.status, QLORA_DEV_LABEL);
@@ -818,6 +835,35 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const __grid_co
   if (end == T && threadIdx.x == 0) *a.nrows = at;
 }
 
+// ---------------------------------------------------------------- label's term
+//
+// Backward: p_label - 1 = expm1(l_label - lse), with the label's logit in fp32
+// rounded to nearest, as the losses and so lse have it (head_combine_kernel).
+// Launched behind the last piece's probabilities, of which it reads nothing.
+constexpr int kLabelWarps = 8;
+
+__global__ void __launch_bounds__(kLabelWarps * 32) head_label_kernel(const __grid_constant__ HeadLabelArgs a) {
+  __shared__ float dot[kLabelWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kLabelWarps / a.parts) + warp / a.parts;
+  float z = 0.0f;
+  if (t < a.T) {
+    const int64_t label = a.labels[t];
+    if (counts(label, a.ignore, a.vocab))
+      z = label_dot(a.head, a.tab, a.h + t * a.ldh, label, warp % a.parts, a.parts, lane);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+  if (lane == 0) dot[warp] = z;
+  __syncthreads();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (lane == 0 && warp % a.parts == 0 && t < a.T) {
+    for (int i = 1; i < a.parts; ++i) z += dot[warp + i];
+    a.p_label[t] = expm1f(z - a.lse[t]);
+  }
+}
+
 // ------------------------------------------------------------------- finish
 //
 // The parts of a tile joined in order, and dH's rows from them.  blockIdx.x:
@@ -896,30 +942,6 @@ __device__ __forceinline__ void store_mean(const HeadCombineArgs& a, double sum,
   a.stats[1] = static_cast<float>(count);
 }
 
-// A lane's share of the logit of label `label` for the row h: columns in runs
-// of 32, `parts` warps in turn.  fp32 sums rounded to nearest.
-__device__ __forceinline__ float label_dot(const HeadCombineArgs& a, const uint16_t* h, int64_t label, int part,
-                                           int parts, int lane) {
-  float z = 0.0f;
-  const int dim = static_cast<int>(a.head.dim);
-  for (int d = (part * 32 + lane) * 32; d < dim; d += 1024 * parts) {
-    const int n = min(32, dim - d);
-    float w[32];
-    load_head_row(a.head, a.tab, label, d, n, w);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 v = 8 * j < n ? __ldcg(reinterpret_cast<const uint4*>(h + d) + j) : make_uint4(0, 0, 0, 0);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z = fmaf(__uint_as_float(u[i] << 16), w[8 * j + 2 * i], z);
-        z = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), w[8 * j + 2 * i + 1], z);
-      }
-    }
-  }
-  return z;
-}
-
 }  // namespace
 
 template <int TB>
@@ -937,7 +959,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
       const int64_t row = blockIdx.x * TB + i, label = a.labels[row];
       float z = 0.0f;
       if (counts(label, a.ignore, a.vocab))
-        z = label_dot(a, a.h + row * a.ldh, label, warp % kDotParts, kDotParts, lane);
+        z = label_dot(a.head, a.tab, a.h + row * a.ldh, label, warp % kDotParts, kDotParts, lane);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
       if (lane == 0) dot[i][warp % kDotParts] = z;
@@ -1122,6 +1144,13 @@ cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMa
 cudaError_t launch_head_finish(const HeadArgs& a, int tiles, cudaStream_t stream) {
   return launch_kernel(head_finish_kernel, dim3((a.pair ? 2 : 1) * tiles, kSumCols / 32), dim3(kSumStride), 0, stream,
                        dim3(1, 1, 1), a);
+}
+
+cudaError_t launch_head_label(HeadLabelArgs a, cudaStream_t stream) {
+  a.parts = a.T <= 4096 ? 4 : 1;  // warps on a token: few tokens wait for a row's loads
+  const int64_t per = kLabelWarps / a.parts;
+  return launch_kernel(head_label_kernel, dim3(static_cast<unsigned>((a.T + per - 1) / per)), dim3(kLabelWarps * 32), 0,
+                       stream, dim3(1, 1, 1), a);
 }
 
 cudaError_t launch_head_rows(HeadRowsArgs a, cudaStream_t stream) {

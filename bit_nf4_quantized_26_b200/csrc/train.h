@@ -42,7 +42,7 @@ constexpr int kHeadTile = 256;  // tokens, and columns, of a CTA pair's tile
 
 enum HeadMode {
   kHeadLoss = 0,  // logits of a piece -> per-tile softmax statistics
-  kHeadProb = 1,  // logits of a piece -> probabilities less the label's one, bf16
+  kHeadProb = 1,  // logits of a piece -> probabilities, bf16 (0 at the label)
   kHeadExp = 2,   // logits of a piece -> exponentials, bf16, and the statistics
   kHeadGrad = 3   // those times the piece's weight -> dH (or its fp32 sum so far)
 };
@@ -123,11 +123,11 @@ struct HeadArgs {
   const float* dloss;     // per-token gradients, or one number with `stats` (backward)
   const float* stats;
   const float* row_sum;   // [T] softmax denominators (step), null in the backward
-  const float* p_label;   // [T] probability of the label less 1 (step)
+  const float* p_label;   // [T] probability of the label less 1
   const float* weight;    // [T] or null (step)
   float scale;
   const int32_t* count;   // tokens that count (step, weight null)
-  qlora_head head;        // step: the label's row of W; NF4: its codes
+  qlora_head head;        // the label's row of W; NF4: its codes
   Nf4Tables tab;
   int32_t* status;
 };
@@ -150,6 +150,20 @@ struct HeadRowsArgs {
   int64_t ldd;
 };
 cudaError_t launch_head_rows(HeadRowsArgs a, cudaStream_t stream);
+
+// Backward: p_label [T], the label's probability less 1 (of tokens that count).
+struct HeadLabelArgs {
+  const int64_t* labels;
+  int64_t ignore, vocab, T;
+  const uint16_t* h;
+  int64_t ldh;
+  qlora_head head;
+  Nf4Tables tab;
+  const float* lse;
+  float* p_label;
+  int parts;
+};
+cudaError_t launch_head_label(HeadLabelArgs a, cudaStream_t stream);
 
 // Joins the parts of Grad's tiles after the last piece; `tiles`: an upper bound
 // of those in parts.

@@ -158,7 +158,7 @@ typedef struct {
  * NF4 head (at most 128 MB, at least 2048 rows).
  * Accuracy: exact bf16 inputs, fp32 accumulation and softmax; a small loss keeps
  * its digits (the label's logit stays out of the sum); the probabilities
- * enter the second product as bf16 (label term subtracted in fp32 first); dH
+ * enter the second product as bf16 (the label's term is added in fp32); dH
  * within 5e-3 relative Frobenius error of the fp64 gradient.
  */
 #define QLORA_HEAD_FWD 0

@@ -310,6 +310,8 @@ def test_losses_keep_their_digits(T, V, D, sign):
     for out in (q.qlora_head_loss_fwd(H, W, Y), got):
         assert np.all(np.abs(out[0][sel].double().cpu().numpy() - loss) <= tol)
         assert np.all(np.abs(out[1][sel].double().cpu().numpy() - r.lse) <= r.lse_tol)
+    back = q.qlora_head_loss_bwd(H, W, Y, got[1], torch.ones(T, device="cuda"))
+    r.check_grad(back[sel], np.ones(rows.size))
     g = np.abs(r.p)
     ref = r.p @ r.W
     bound = (r.rel[:, None] + 2.0 ** -21 + 2 * 2.0 ** -8 * 1.01) * g @ np.abs(r.W) + 2.0 ** -8 * np.abs(ref) + 1e-37
