@@ -237,12 +237,12 @@ qlora_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLORA_OK : QLO
 enum KernelId {
   kKQuantize = 0, kKDequantize, kKDown, kKFusedFwd, kKFinishFwd, kKLowFwd, kKLowFinish, kKDU, kKDB, kKFusedDX,
   kKDA, kKAdamW8, kKDropout, kKDropoutDx, kKActQuantize, kKActDequantize, kKActDA, kKHeadLogits, kKHeadGrad,
-  kKHeadCombine, kKHeadRows, kKHeadLabel, kKCount
+  kKHeadCombine, kKHeadRows, kKCount
 };
 const char* const kKernelNames[kKCount] = {
     "nf4_quantize", "nf4_dequantize", "lora_down", "fused_fwd", "finish_fwd", "lowm_fwd", "lowm_finish",
     "lora_du", "lora_db", "fused_dx", "lora_da", "adamw8", "dropout", "dropout_dx", "act8_quantize",
-    "act8_dequantize", "act8_da", "head_logits", "head_grad", "head_combine", "head_rows", "head_label"};
+    "act8_dequantize", "act8_da", "head_logits", "head_grad", "head_combine", "head_rows"};
 
 struct ProfRecord {
   int id;
@@ -1594,6 +1594,8 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
                          c.H,      c.ldh,    D,   gather ? hrows : nullptr,     c.dH,  c.lddh};
     if (qlora_status st = from_cuda(launch_head_rows(r, cs))) return st;
   }
+  a.h = gather ? hrows : c.H;
+  a.ldh = gather ? D : c.ldh;
   if (gather) {
     a.nrows = nrows;
     a.rows = rows;
@@ -1639,6 +1641,7 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     float2* part = reinterpret_cast<float2*>(at(p.off_part));
     a.part = op == QLORA_HEAD_FWD ? part + i * p.parts * T : part;
     {
+      a.p_label_out = op == QLORA_HEAD_BWD && last ? reinterpret_cast<float*>(at(p.off_pl)) : nullptr;
       const int mode = op == QLORA_HEAD_FWD ? kHeadLoss : op == QLORA_HEAD_BWD ? kHeadProb : kHeadExp;
       ProfScope ps(kKHeadLogits, cs);
       if (qlora_status st = from_cuda(launch_head_gemm(mode, mh, mw, a, cs))) return st;
@@ -1681,12 +1684,6 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
         d.rows = rows;
       }
       d.p_label = reinterpret_cast<float*>(at(p.off_pl));
-      if (op == QLORA_HEAD_BWD && last) {
-        const HeadLabelArgs la{c.labels, c.ignore, V,        T, c.H, c.ldh, hd, a.tab, c.lse_in,
-                               reinterpret_cast<float*>(at(p.off_pl)), 0};
-        ProfScope ps(kKHeadLabel, cs);
-        if (qlora_status st = from_cuda(launch_head_label(la, cs))) return st;
-      }
       if (op == QLORA_HEAD_STEP) {
         d.alpha = cb.alpha;
         d.row_sum = cb.row_sum;

@@ -59,7 +59,10 @@ struct HeadPlan {
   static constexpr uint32_t kStage = kA + kB + kC;
   // Warp 0: copies; warp 1: MMAs; then eight epilogue warps (two per quarter of
   // the rows, each with half of the columns); NF4: eight that dequantise.
-  static constexpr int kThreads = 64 + 256 + (NF4 ? 256 : 0);
+  // Prob: two more, for the labels' logits.
+  static constexpr int kLabelWarp = 2 + 8 + (NF4 ? 8 : 0);
+  static constexpr int kLabelWarps = MODE == kHeadProb ? 2 : 0;
+  static constexpr int kThreads = 32 * (kLabelWarp + kLabelWarps);
   // The dequantisers as groups that take the stages in turn, a 64-weight block
   // a thread; the ring is a multiple of the groups, so a slot's earlier stages
   // are the same group's and its parity waits cannot run a phase ahead.
@@ -262,24 +265,25 @@ __device__ __forceinline__ void load_head_row(const qlora_head& h, const Nf4Tabl
   }
 }
 
-// A lane's share of the logit of label `label` for the row h: runs of 8
-// columns, `parts` warps in turn.  fp32 sums rounded to nearest.
+// A lane's share of the logit of label `label` for the row h: columns 8 first ..
+// and every 8 lanes-th run of 8 on.  fp32 sums rounded to nearest, four a lane
+// (shorter chains, smaller errors).
 __device__ __forceinline__ float label_dot(const qlora_head& head, const Nf4Tables& tab, const uint16_t* h,
-                                           int64_t label, int part, int parts, int lane) {
-  float z = 0.0f;
+                                           int64_t label, int first, int lanes) {
+  float z[4] = {};
   const int dim = static_cast<int>(head.dim);
   auto add = [&z](const uint4& x, const uint4& y) {
     const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      z = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), z);
-      z = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), z);
+      z[i] = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), z[i]);
+      z[i] = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), z[i]);
     }
   };
-  const int d0 = (part * 32 + lane) * 8, step = parts * 256;
+  const int d0 = first * 8, step = lanes * 8;
   if (head.w) {
     const uint16_t* w = head.w + label * head.ld;
-#pragma unroll 4
+#pragma unroll 8
     for (int d = d0; d < dim; d += step)
       add(__ldcg(reinterpret_cast<const uint4*>(h + d)), __ldg(reinterpret_cast<const uint4*>(w + d)));
   } else {
@@ -292,7 +296,7 @@ __device__ __forceinline__ float label_dot(const qlora_head& head, const Nf4Tabl
           nf4_lookup8(__ldg(reinterpret_cast<const uint32_t*>(head.codes + (e >> 1))), lut));
     }
   }
-  return z;
+  return (z[0] + z[1]) + (z[2] + z[3]);
 }
 
 // Columns d .. d + 31 (`n` of them valid) of dH's row t from its sums l.
@@ -527,6 +531,30 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         mbar_drain(done, 0, a.status);
       }
       __syncwarp();
+    }
+  } else if (MODE == kHeadProb && warp >= P::kLabelWarp) {
+    // ------------------------------------------------------------- label's term
+    // p_label - 1 = expm1(l_label - lse) of the tokens that count, with the
+    // label's logit in fp32 rounded to nearest, as the losses and so lse have it
+    // (head_combine_kernel); eight lanes a token.  Beside the products they
+    // cost nothing; a launch of their own took 4-20 us.
+    if (a.p_label_out) {
+      const int stride = 4 * P::kLabelWarps * gridDim.x;
+      for (int r0 = 4 * (blockIdx.x * P::kLabelWarps + warp - P::kLabelWarp); r0 < T; r0 += stride) {
+        const int row = r0 + (lane >> 3);
+        float z = 0.0f;
+        int t = 0;
+        bool counted = false;
+        if (row < T) {
+          t = a.rows ? __ldcg(a.rows + row) : row;
+          const int64_t label = __ldg(a.labels + t);
+          counted = counts(label, a.ignore, a.vocab);
+          if (counted) z = label_dot(a.head, a.tab, a.h + row * a.ldh, label, lane & 7, 8);
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+        if (counted && (lane & 7) == 0) a.p_label_out[t] = expm1f(z - __ldcg(a.lse + t));
+      }
     }
   } else if (NF4 && warp >= 2 + kEpiWarps) {
     // ----------------------------------------------------------- dequantisers
@@ -835,35 +863,6 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const __grid_co
   if (end == T && threadIdx.x == 0) *a.nrows = at;
 }
 
-// ---------------------------------------------------------------- label's term
-//
-// Backward: p_label - 1 = expm1(l_label - lse), with the label's logit in fp32
-// rounded to nearest, as the losses and so lse have it (head_combine_kernel).
-// Launched behind the last piece's probabilities, of which it reads nothing.
-constexpr int kLabelWarps = 8;
-
-__global__ void __launch_bounds__(kLabelWarps * 32) head_label_kernel(const __grid_constant__ HeadLabelArgs a) {
-  __shared__ float dot[kLabelWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kLabelWarps / a.parts) + warp / a.parts;
-  float z = 0.0f;
-  if (t < a.T) {
-    const int64_t label = a.labels[t];
-    if (counts(label, a.ignore, a.vocab))
-      z = label_dot(a.head, a.tab, a.h + t * a.ldh, label, warp % a.parts, a.parts, lane);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-  if (lane == 0) dot[warp] = z;
-  __syncthreads();
-  grid_dependency_wait();
-  grid_dependents_launch();
-  if (lane == 0 && warp % a.parts == 0 && t < a.T) {
-    for (int i = 1; i < a.parts; ++i) z += dot[warp + i];
-    a.p_label[t] = expm1f(z - a.lse[t]);
-  }
-}
-
 // ------------------------------------------------------------------- finish
 //
 // The parts of a tile joined in order, and dH's rows from them.  blockIdx.x:
@@ -959,7 +958,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
       const int64_t row = blockIdx.x * TB + i, label = a.labels[row];
       float z = 0.0f;
       if (counts(label, a.ignore, a.vocab))
-        z = label_dot(a.head, a.tab, a.h + row * a.ldh, label, warp % kDotParts, kDotParts, lane);
+        z = label_dot(a.head, a.tab, a.h + row * a.ldh, label, warp % kDotParts * 32 + lane, kDotParts * 32);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
       if (lane == 0) dot[i][warp % kDotParts] = z;
@@ -1144,13 +1143,6 @@ cudaError_t launch_head_gemm(int mode, const CUtensorMap& tm_a, const CUtensorMa
 cudaError_t launch_head_finish(const HeadArgs& a, int tiles, cudaStream_t stream) {
   return launch_kernel(head_finish_kernel, dim3((a.pair ? 2 : 1) * tiles, kSumCols / 32), dim3(kSumStride), 0, stream,
                        dim3(1, 1, 1), a);
-}
-
-cudaError_t launch_head_label(HeadLabelArgs a, cudaStream_t stream) {
-  a.parts = a.T <= 4096 ? 4 : 1;  // warps on a token: few tokens wait for a row's loads
-  const int64_t per = kLabelWarps / a.parts;
-  return launch_kernel(head_label_kernel, dim3(static_cast<unsigned>((a.T + per - 1) / per)), dim3(kLabelWarps * 32), 0,
-                       stream, dim3(1, 1, 1), a);
 }
 
 cudaError_t launch_head_rows(HeadRowsArgs a, cudaStream_t stream) {

@@ -110,6 +110,9 @@ struct HeadArgs {
   int64_t ignore;
   float2* part;         // Loss, Exp: (reference, sum of the others' exponentials) [half tile][T], from the piece's first
   const float* lse;       // Prob: [T]
+  float* p_label_out;     // Prob: [T] probability of the label less 1, or null
+  const uint16_t* h;      //   from the operand's rows, stride ldh
+  int64_t ldh;
   uint16_t* g;            // Prob, Exp: [rows, ldg]
   int64_t ldg;
   uint32_t* zero;         // Loss, Exp: words cleared by the first CTA (combine's counters)
@@ -150,20 +153,6 @@ struct HeadRowsArgs {
   int64_t ldd;
 };
 cudaError_t launch_head_rows(HeadRowsArgs a, cudaStream_t stream);
-
-// Backward: p_label [T], the label's probability less 1 (of tokens that count).
-struct HeadLabelArgs {
-  const int64_t* labels;
-  int64_t ignore, vocab, T;
-  const uint16_t* h;
-  int64_t ldh;
-  qlora_head head;
-  Nf4Tables tab;
-  const float* lse;
-  float* p_label;
-  int parts;
-};
-cudaError_t launch_head_label(HeadLabelArgs a, cudaStream_t stream);
 
 // Joins the parts of Grad's tiles after the last piece; `tiles`: an upper bound
 // of those in parts.
