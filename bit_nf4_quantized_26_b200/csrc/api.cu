@@ -1352,7 +1352,7 @@ struct HeadPlanHost {
   int64_t kfull = 0;             // 64-deep stages of a piece's dH contraction
   int64_t tails = 0;             // dH's tiles that may be in parts
   int64_t cost = 0;              // of the products: waves x 64-deep stages x columns
-  size_t off_cnt = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_sum = 0, off_pl = 0;
+  size_t off_cnt = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_root = 0, off_pl = 0;
   size_t off_g = 0, off_acc = 0, off_w = 0, off_rows = 0, off_place = 0, off_nrows = 0, off_h = 0, total = 0;
   // dH's products take the rows that count only (the backward's both, the
   // step's second; losses need every row's lse).  Listing and gathering them
@@ -1430,7 +1430,7 @@ static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, i
   if (op == QLORA_HEAD_STEP) {
     p.off_run = take(8 * t);
     p.off_alpha = take(4 * t);
-    p.off_sum = take(4 * t);
+    p.off_root = take(4 * t);
   }
   if (op != QLORA_HEAD_FWD) {
     p.off_pl = take(4 * t);
@@ -1654,7 +1654,7 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
       if (op == QLORA_HEAD_STEP) {
         cb.run = reinterpret_cast<float2*>(at(p.off_run));
         cb.alpha = reinterpret_cast<float*>(at(p.off_alpha));
-        cb.row_sum = reinterpret_cast<float*>(at(p.off_sum));
+        cb.row_root = reinterpret_cast<float*>(at(p.off_root));
         cb.p_label = reinterpret_cast<float*>(at(p.off_pl));
         cb.e = g;
         cb.lde = p.ldg;
@@ -1686,7 +1686,7 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
       d.p_label = reinterpret_cast<float*>(at(p.off_pl));
       if (op == QLORA_HEAD_STEP) {
         d.alpha = cb.alpha;
-        d.row_sum = cb.row_sum;
+        d.row_root = cb.row_root;
         d.weight = c.weight;
         d.scale = c.scale;
         d.count = cb.counters;

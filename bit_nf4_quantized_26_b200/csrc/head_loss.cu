@@ -224,14 +224,17 @@ struct HeadItems {
   }
 };
 
-// dH_t = ca * (the row's sum over the vocabulary but the label) + cl * W[label].
-__device__ __forceinline__ void grad_row_factors(const HeadArgs& a, int t, float& ca, float& cl) {
+// dH_t = cs * (cn * the row's sum over the vocabulary but the label) + cl *
+// W[label].  Step: cn is the root of the sum's normalisation (head_combine_kernel).
+__device__ __forceinline__ void grad_row_factors(const HeadArgs& a, int t, float& cn, float& cs, float& cl) {
   float g;
-  if (a.row_sum) {
+  if (a.row_root) {
     g = a.weight ? a.scale * __ldcg(a.weight + t) : a.scale / static_cast<float>(__ldcg(a.count));
-    ca = g / __ldcg(a.row_sum + t);
+    cn = __ldcg(a.row_root + t);
+    cs = g * cn;
   } else {
-    g = ca = a.stats ? __ldcg(a.dloss) / __ldcg(a.stats + 1) : __ldcg(a.dloss + t);
+    g = cs = a.stats ? __ldcg(a.dloss) / __ldcg(a.stats + 1) : __ldcg(a.dloss + t);
+    cn = 1.0f;
   }
   cl = g * __ldcg(a.p_label + t);
 }
@@ -300,8 +303,8 @@ __device__ __forceinline__ float label_dot(const qlora_head& head, const Nf4Tabl
 }
 
 // Columns d .. d + 31 (`n` of them valid) of dH's row t from its sums l.
-__device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t label, bool counted, float ca, float cl,
-                                             int d, int n, float (&l)[32]) {
+__device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t label, bool counted, float cn, float cs,
+                                             float cl, int d, int n, float (&l)[32]) {
   if (!counted) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) l[j] = 0.0f;
@@ -309,7 +312,7 @@ __device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t l
     float w[32];
     load_head_row(a.head, a.tab, label, d, n, w);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) l[j] = fmaf(cl, w[j], ca * l[j]);
+    for (int j = 0; j < 32; ++j) l[j] = fmaf(cl, w[j], cs * (cn * l[j]));
   }
   store_bf16x32(a.dh + static_cast<int64_t>(t) * a.ldd + d, l, n);
 }
@@ -683,8 +686,8 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         float4* sum = reinterpret_cast<float4*>(a.acc) + (static_cast<int64_t>(it.slot) * kCtas + rank) * kSumBlock + et;
         const float al = (!a.first && a.alpha && rok) ? __ldcg(a.alpha + t) : 1.0f;
         const bool out = a.last && it.whole;
-        float ca = 0.0f, cl = 0.0f;
-        if (out && counted) grad_row_factors(a, t, ca, cl);
+        float cn = 0.0f, cs = 0.0f, cl = 0.0f;
+        if (out && counted) grad_row_factors(a, t, cn, cs, cl);
         for (int cb = 0; cb < kSumCols / 32; ++cb) {
           float l[32] = {};
           if (kn > 0) {
@@ -710,7 +713,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
             for (int j = 0; j < 8; ++j)
               __stcg(at + j * kSumStride, make_float4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]));
           } else if (rok && cb * 32 < nv) {
-            store_grad32(a, t, label, counted, ca, cl, n0 + cb * 32, min(32, nv - cb * 32), l);
+            store_grad32(a, t, label, counted, cn, cs, cl, n0 + cb * 32, min(32, nv - cb * 32), l);
           }
         }
         if (kn > 0) {
@@ -902,9 +905,9 @@ __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_co
   }
   const int64_t label = __ldg(a.labels + t);
   const bool counted = counts(label, a.ignore, a.vocab);
-  float ca = 0.0f, cl = 0.0f;
-  if (counted) grad_row_factors(a, t, ca, cl);
-  store_grad32(a, t, label, counted, ca, cl, d, min(32, a.ncols - d), l);
+  float cn = 0.0f, cs = 0.0f, cl = 0.0f;
+  if (counted) grad_row_factors(a, t, cn, cs, cl);
+  store_grad32(a, t, label, counted, cn, cs, cl, d, min(32, a.ncols - d), l);
 }
 
 // ------------------------------------------------------------------ combine
@@ -1020,12 +1023,15 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
           float z = dot[lane][0];
           for (int i = 1; i < kDotParts; ++i) z += dot[lane][i];
           const float top = fmaxf(R, z);
-          // exp(l - l_label) over the others; where that is near overflow, its log is log S + R - l_label
-          const float x = S * expf(R - z);
+          // exp(l - l_label) over the others; where that is near overflow, its log is log S + R - l_label.
+          // The reference may lie far below the others' maximum (0 for 40), so S exp(R - z) can be large
+          // where exp(R - z) is not a number of fp32: the exponential in two halves.
+          const float e = expf(0.5f * (R - z));
+          const float x = (S * e) * e;
           loss = x < 1e30f ? log1pf(x) : (R - z) + logf(S);
           lse = top + logf(S * expf(R - top) + expf(z - top));  // (no others: R = -inf, S = 0)
-          if (a.row_sum) {
-            a.row_sum[t] = S + expf(z - R);  // inf: the others' share is below 1e-38
+          if (a.row_root) {  // and the root of 1 / (S + exp(z - R)), which overflows no earlier than it should
+            a.row_root[t] = z > R ? e / sqrtf(1.0f + x) : 1.0f / sqrtf(S + expf(z - R));
             a.p_label[t] = expm1f(-loss);
           }
         }

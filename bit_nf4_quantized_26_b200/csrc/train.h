@@ -125,7 +125,7 @@ struct HeadArgs {
   int64_t ldd;
   const float* dloss;     // per-token gradients, or one number with `stats` (backward)
   const float* stats;
-  const float* row_sum;   // [T] softmax denominators (step), null in the backward
+  const float* row_root;  // [T] 1 / root of the softmax denominators (step), null in the backward
   const float* p_label;   // [T] probability of the label less 1
   const float* weight;    // [T] or null (step)
   float scale;
@@ -178,7 +178,7 @@ struct HeadCombineArgs {
   const int32_t* place;    // step: row of a token in e or -1, or null; then, with the last piece,
   uint16_t* dh;            //   the other rows of dH become zero
   int64_t ldd, dim;
-  float* row_sum;          // step: [T]
+  float* row_root;         // step: [T] 1 / root of the softmax denominator
   float* p_label;          // step: [T]
   int32_t* counters;       // [2]: tokens that count, blocks done; cleared before
   double* block_sum;       // [blocks]

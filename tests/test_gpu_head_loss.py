@@ -529,3 +529,31 @@ def test_refusals_on_device_tensors():
               lambda: q.qlora_head_loss_step(H, W, Y, ws=torch.zeros(64, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(q.QloraError):
             f()
+
+
+@pytest.mark.parametrize("T,V,D", [(40, 3000, 64), (300, 9000, 320)])
+def test_label_logits_far_above_others_near_forty(T, V, D):
+    """The others' logits 39 each, the label's 85 to 120: their share of the sum
+    is 1e-17 to 1e-32, which fp32 and bf16 hold, and it is all there is of the
+    gradient.  Every logit is exact, so x = (V - 1) exp(39 - l_label) is off by the
+    exponential's argument (2^-23 of it, below 128 in two halves) and a few
+    roundings, below 2^-15; the operand's and dH's roundings are 2^-9 each."""
+    g = torch.Generator().manual_seed(16)
+    w = torch.randn(V, D, generator=g) * 0.5
+    w[:, 0], w[:, 1], w[V // 2, 1] = 1.0, 0.0, 1.0
+    w = w.to(torch.bfloat16)
+    h = torch.zeros(T, D)
+    top = torch.linspace(85, 120, T).round()
+    h[:, 0], h[:, 1] = 39.0, top - 39.0
+    y = torch.full((T,), V // 2)
+    share = np.exp(39.0 - top.double().numpy())
+    others = w.double().numpy().sum(0) - w[V // 2].double().numpy()
+    loss = np.log1p((V - 1) * share)
+    ref = share[:, None] * (others - (V - 1) * w[V // 2].double().numpy()) / (1 + (V - 1) * share)[:, None]
+    size = share[:, None] * (np.abs(w.double().numpy()).sum(0) + V * np.abs(w[V // 2].double().numpy()))
+    H, W, Y = h.to(torch.bfloat16).cuda(), w.cuda(), y.cuda()
+    got = q.qlora_head_loss_step(H, W, Y, weight=torch.ones(T, device="cuda"))
+    for out in (q.qlora_head_loss_fwd(H, W, Y), got):
+        assert np.all(np.abs(out[0].double().cpu().numpy() - loss) <= 2.0 ** -15 * loss)
+    err = np.abs(got[3].double().cpu().numpy() - ref)
+    assert np.all(err <= (2.0 ** -9 * 1.01 + 2.0 ** -14) * size + 2.0 ** -9 * np.abs(ref))
