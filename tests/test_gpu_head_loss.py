@@ -537,7 +537,7 @@ def test_label_logits_far_above_others_near_forty(T, V, D):
     is 1e-17 to 1e-32, which fp32 and bf16 hold, and it is all there is of the
     gradient.  Every logit is exact, so x = (V - 1) exp(39 - l_label) is off by the
     exponential's argument (2^-23 of it, below 128 in two halves) and a few
-    roundings, below 2^-15; the operand's and dH's roundings are 2^-9 each."""
+    roundings, below 2^-15; the operand's and dH's roundings are 2^-8 each."""
     g = torch.Generator().manual_seed(16)
     w = torch.randn(V, D, generator=g) * 0.5
     w[:, 0], w[:, 1], w[V // 2, 1] = 1.0, 0.0, 1.0
@@ -556,4 +556,4 @@ def test_label_logits_far_above_others_near_forty(T, V, D):
     for out in (q.qlora_head_loss_fwd(H, W, Y), got):
         assert np.all(np.abs(out[0].double().cpu().numpy() - loss) <= 2.0 ** -15 * loss)
     err = np.abs(got[3].double().cpu().numpy() - ref)
-    assert np.all(err <= (2.0 ** -9 * 1.01 + 2.0 ** -14) * size + 2.0 ** -9 * np.abs(ref))
+    assert np.all(err <= (2.0 ** -8 * 1.01 + 2.0 ** -14) * size + 2.0 ** -8 * np.abs(ref))
