@@ -1352,8 +1352,9 @@ struct HeadPlanHost {
   int64_t kfull = 0;             // 64-deep stages of a piece's dH contraction
   int64_t tails = 0;             // dH's tiles that may be in parts
   int64_t cost = 0;              // of the products: waves x 64-deep stages x columns
-  size_t off_cnt = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_root = 0, off_pl = 0;
-  size_t off_g = 0, off_acc = 0, off_w = 0, off_rows = 0, off_place = 0, off_nrows = 0, off_h = 0, total = 0;
+  size_t off_cnt = 0, off_part = 0, off_bsum = 0, off_run = 0, off_alpha = 0, off_root = 0, off_coef = 0;
+  size_t off_rsum = 0, off_runrsum = 0, off_rounding = 0;
+  size_t off_g = 0, off_acc = 0, off_w = 0, off_rows = 0, off_coeface = 0, off_nrows = 0, off_h = 0, total = 0;
   // dH's products take the rows that count only (the backward's both, the
   // step's second; losses need every row's lse).  Listing and gathering them
   // costs 3-8 us; backward without against with it, a quarter of the tokens
@@ -1431,9 +1432,12 @@ static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, i
     p.off_run = take(8 * t);
     p.off_alpha = take(4 * t);
     p.off_root = take(4 * t);
+    p.off_rsum = take(4 * t * static_cast<size_t>(p.parts));
+    p.off_runrsum = take(4 * t);
   }
+  if (op == QLORA_HEAD_BWD) p.off_rounding = take(8 * t);
   if (op != QLORA_HEAD_FWD) {
-    p.off_pl = take(4 * t);
+    p.off_coef = take(4 * t);
     p.off_g = take(2 * t * static_cast<size_t>(p.ldg));
   }
   p.compact = op != QLORA_HEAD_FWD && T > 256 && 4.0 * T * V * D >= 1e11;
@@ -1449,7 +1453,7 @@ static HeadPlanHost plan_head_tiles(int64_t T, int64_t V, int64_t D, bool nf4, i
   }
   if (p.compact) {
     p.off_rows = take(4 * t);
-    p.off_place = take(4 * t);
+    p.off_coeface = take(4 * t);
     p.off_nrows = take(4);
     if (op == QLORA_HEAD_BWD) p.off_h = take(2 * t * static_cast<size_t>(D));
   }
@@ -1582,18 +1586,21 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
   const uint32_t abox = static_cast<uint32_t>(std::min<int64_t>(128, cdiv(T, 8) * 8));
   a.arows = static_cast<int>(abox);
   int32_t* rows = reinterpret_cast<int32_t*>(at(p.off_rows));
-  int32_t* place = reinterpret_cast<int32_t*>(at(p.off_place));
+  int32_t* place = reinterpret_cast<int32_t*>(at(p.off_coeface));
   int32_t* nrows = reinterpret_cast<int32_t*>(at(p.off_nrows));
   const bool gather = p.compact && op == QLORA_HEAD_BWD;
   uint16_t* hrows = reinterpret_cast<uint16_t*>(at(p.off_h));
   if (!(gather ? map_bf16_ld(&mh, hrows, T, D, D, 64, abox) : map_bf16_ld(&mh, c.H, T, D, c.ldh, 64, abox)))
     return QLORA_ERR_CUDA;
-  if (p.compact) {
+  unsigned long long* rounding =
+      op == QLORA_HEAD_BWD ? reinterpret_cast<unsigned long long*>(at(p.off_rounding)) : nullptr;
+  if (p.compact || rounding) {
     ProfScope ps(kKHeadRows, cs);
-    const HeadRowsArgs r{c.labels, c.ignore, V,   T,     0, rows, place, nrows, d_status,
-                         c.H,      c.ldh,    D,   gather ? hrows : nullptr,     c.dH,  c.lddh};
-    if (qlora_status st = from_cuda(launch_head_rows(r, cs))) return st;
+    const HeadRowsArgs r{c.labels, c.ignore, V,        T,     0, rows,   place, nrows,  d_status,
+                         rounding, c.H,      c.ldh,    D,     gather ? hrows : nullptr, c.dH, c.lddh};
+    if (qlora_status st = from_cuda(p.compact ? launch_head_rows(r, cs) : launch_head_clear(rounding, T, cs))) return st;
   }
+  a.rounding = rounding;
   a.h = gather ? hrows : c.H;
   a.ldh = gather ? D : c.ldh;
   if (gather) {
@@ -1640,8 +1647,9 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     a.kchunk = op == QLORA_HEAD_BWD ? 16 : (p.pair ? 12 : 4);
     float2* part = reinterpret_cast<float2*>(at(p.off_part));
     a.part = op == QLORA_HEAD_FWD ? part + i * p.parts * T : part;
+    a.rsum = reinterpret_cast<float*>(at(p.off_rsum));
     {
-      a.p_label_out = op == QLORA_HEAD_BWD && last ? reinterpret_cast<float*>(at(p.off_pl)) : nullptr;
+      a.coef_out = op == QLORA_HEAD_BWD && last ? reinterpret_cast<float*>(at(p.off_coef)) : nullptr;
       const int mode = op == QLORA_HEAD_FWD ? kHeadLoss : op == QLORA_HEAD_BWD ? kHeadProb : kHeadExp;
       ProfScope ps(kKHeadLogits, cs);
       if (qlora_status st = from_cuda(launch_head_gemm(mode, mh, mw, a, cs))) return st;
@@ -1652,10 +1660,12 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
       cb.first = op == QLORA_HEAD_FWD || first;
       cb.last = last;
       if (op == QLORA_HEAD_STEP) {
+        cb.rsum = reinterpret_cast<const float*>(at(p.off_rsum));
         cb.run = reinterpret_cast<float2*>(at(p.off_run));
+        cb.run_rsum = reinterpret_cast<float*>(at(p.off_runrsum));
         cb.alpha = reinterpret_cast<float*>(at(p.off_alpha));
         cb.row_root = reinterpret_cast<float*>(at(p.off_root));
-        cb.p_label = reinterpret_cast<float*>(at(p.off_pl));
+        cb.coef = reinterpret_cast<float*>(at(p.off_coef));
         cb.e = g;
         cb.lde = p.ldg;
       }
@@ -1683,7 +1693,7 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
         d.nrows = nrows;
         d.rows = rows;
       }
-      d.p_label = reinterpret_cast<float*>(at(p.off_pl));
+      d.coef = reinterpret_cast<float*>(at(p.off_coef));
       if (op == QLORA_HEAD_STEP) {
         d.alpha = cb.alpha;
         d.row_root = cb.row_root;

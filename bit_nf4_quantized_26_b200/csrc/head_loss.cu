@@ -27,10 +27,18 @@
 //
 // The label's column stays apart: loss = log1p(sum over the others of exp(l -
 // l_label)), which keeps its digits where the label dominates (lse - l_label
-// would leave 1e-6 of a logit of 14, whatever the loss), and its term of dH is
-// added after the last piece in fp32, (p_label - 1) W[label] with p_label - 1 =
-// expm1(-loss), in the backward expm1(l_label - lse): rounding p to bf16 first
-// would lose the gradient of a well-predicted token.
+// would leave 1e-6 of a logit of 14, whatever the loss), and its term of dH,
+// (p_label - 1) W[label], is added after the last piece in fp32: rounding p to
+// bf16 first would lose the gradient of a well-predicted token.
+//
+// A row's coefficients sum to zero, and so have the rounded ones to: what all of
+// W's rows share (a head's rows have a mean) cancels in dH, and would come
+// through with what the roundings leave, 2^-9 of the large ones (a mean of 10
+// times the rows' own part: dH 2.5% off).  The label's coefficient therefore
+// takes the others' roundings up: in the step it is minus the sum of the
+// others as rounded, in the backward (whose lse is the caller's, so that the
+// others need not sum to 1 - p_label) expm1(l_label - lse) less the sum of the
+// roundings.
 #include <algorithm>
 
 #include "train.h"
@@ -40,6 +48,10 @@ namespace qnf4 {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// The backward's sums of roundings are integers in units of 2^-40, added by
+// atomics: in any order the same.  (A half tile's is below 2^-9; of something
+// that is no probability, 1 and more, nothing is added.)
+constexpr float kRoundingUnit = 1.0f / static_cast<float>(int64_t(1) << 40);
 constexpr float kRefRange = 40.0f;  // tile maxima within +-kRefRange share the reference 0
 
 // PAIR: tiles of 256 tokens on CTA pairs; otherwise of 128 on single CTAs.
@@ -146,19 +158,37 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32
                      pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
 }
 
-// `cols` bf16 (a multiple of 16; 32-byte aligned) from fp32, whole sectors a store.
-template <int N>
-__device__ __forceinline__ void store_bf16(uint16_t* dst, int cols, const float (&v)[N]) {
+// Two fp32 sums in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 c;
+  asm("{.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(c.x), "=f"(c.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return c;
+}
+
+// `cols` bf16 (a multiple of 16; 32-byte aligned) from fp32, whole sectors a
+// store; returns the sum of the rounded values (RESIDUE: less the values').
+template <bool RESIDUE, int N>
+__device__ __forceinline__ float store_bf16(uint16_t* dst, int cols, const float (&v)[N]) {
+  float2 d[2] = {};
 #pragma unroll
   for (int j = 0; j < N; j += 16) {
     if (j >= cols) break;
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[j + 2 * i], v[j + 2 * i + 1]);
+    for (int i = 0; i < 8; ++i) {
+      w[i] = pack_bf16x2(v[j + 2 * i], v[j + 2 * i + 1]);
+      float2 r = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+      if (RESIDUE) r = add2(r, make_float2(-v[j + 2 * i], -v[j + 2 * i + 1]));
+      d[i & 1] = add2(d[i & 1], r);
+    }
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + j), "r"(w[0]), "r"(w[1]),
                  "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
   }
+  return (d[0].x + d[0].y) + (d[1].x + d[1].y);
 }
 
 // fp32 sums between pieces and of parts of a contraction: per tile or part and
@@ -224,19 +254,19 @@ struct HeadItems {
   }
 };
 
-// dH_t = cs * (cn * the row's sum over the vocabulary but the label) + cl *
-// W[label].  Step: cn is the root of the sum's normalisation (head_combine_kernel).
+// dH_t = cs * cn * (the row's sum over the vocabulary but the label + cl *
+// W[label]).  Step: cn is the root of the sum's normalisation (head_combine_kernel).
 __device__ __forceinline__ void grad_row_factors(const HeadArgs& a, int t, float& cn, float& cs, float& cl) {
-  float g;
+  cl = __ldcg(a.coef + t);
   if (a.row_root) {
-    g = a.weight ? a.scale * __ldcg(a.weight + t) : a.scale / static_cast<float>(__ldcg(a.count));
+    const float g = a.weight ? a.scale * __ldcg(a.weight + t) : a.scale / static_cast<float>(__ldcg(a.count));
     cn = __ldcg(a.row_root + t);
     cs = g * cn;
   } else {
-    g = cs = a.stats ? __ldcg(a.dloss) / __ldcg(a.stats + 1) : __ldcg(a.dloss + t);
+    cs = a.stats ? __ldcg(a.dloss) / __ldcg(a.stats + 1) : __ldcg(a.dloss + t);
     cn = 1.0f;
+    cl -= static_cast<float>(static_cast<long long>(__ldcg(a.rounding + t))) * kRoundingUnit;
   }
-  cl = g * __ldcg(a.p_label + t);
 }
 
 // Columns d .. d + 31 of row `row` of the head as fp32 (`n` valid, a multiple of 8).
@@ -302,18 +332,12 @@ __device__ __forceinline__ float label_dot(const qlora_head& head, const Nf4Tabl
   return (z[0] + z[1]) + (z[2] + z[3]);
 }
 
-// Columns d .. d + 31 (`n` of them valid) of dH's row t from its sums l.
-__device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, int64_t label, bool counted, float cn, float cs,
-                                             float cl, int d, int n, float (&l)[32]) {
-  if (!counted) {
+// Columns d .. d + 31 (`n` of them valid) of dH's row t from its sums l and the
+// label's row of W.
+__device__ __forceinline__ void store_grad32(const HeadArgs& a, int t, bool counted, float cn, float cs, float cl,
+                                             int d, int n, const float (&w)[32], float (&l)[32]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) l[j] = 0.0f;
-  } else {
-    float w[32];
-    load_head_row(a.head, a.tab, label, d, n, w);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) l[j] = fmaf(cl, w[j], cs * (cn * l[j]));
-  }
+  for (int j = 0; j < 32; ++j) l[j] = counted ? cs * (cn * fmaf(cl, w[j], l[j])) : 0.0f;
   store_bf16x32(a.dh + static_cast<int64_t>(t) * a.ldd + d, l, n);
 }
 
@@ -541,7 +565,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
     // label's logit in fp32 rounded to nearest, as the losses and so lse have it
     // (head_combine_kernel); eight lanes a token.  Beside the products they
     // cost nothing; a launch of their own took 4-20 us.
-    if (a.p_label_out) {
+    if (a.coef_out) {
       const int stride = 4 * P::kLabelWarps * gridDim.x;
       for (int r0 = 4 * (blockIdx.x * P::kLabelWarps + warp - P::kLabelWarp); r0 < T; r0 += stride) {
         const int row = r0 + (lane >> 3);
@@ -556,7 +580,7 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-        if (counted && (lane & 7) == 0) a.p_label_out[t] = expm1f(z - __ldcg(a.lse + t));
+        if (counted && (lane & 7) == 0) a.coef_out[t] = expm1f(z - __ldcg(a.lse + t));
       }
     }
   } else if (NF4 && warp >= 2 + kEpiWarps) {
@@ -713,7 +737,10 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
             for (int j = 0; j < 8; ++j)
               __stcg(at + j * kSumStride, make_float4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]));
           } else if (rok && cb * 32 < nv) {
-            store_grad32(a, t, label, counted, cn, cs, cl, n0 + cb * 32, min(32, nv - cb * 32), l);
+            const int d = n0 + cb * 32, nd = min(32, nv - cb * 32);
+            float w[32] = {};
+            if (counted) load_head_row(a.head, a.tab, label, d, nd, w);
+            store_grad32(a, t, counted, cn, cs, cl, d, nd, w, l);
           }
         }
         if (kn > 0) {
@@ -768,7 +795,9 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
         if (rok) {
           a.part[static_cast<int64_t>(2 * n + half) * a.T + t] = make_float2(ref, (p[0] + p[1]) + (p[2] + p[3]));
           const int at = a.place ? __ldcg(a.place + t) : t;
-          if (at >= 0) store_bf16(a.g + static_cast<int64_t>(at) * a.ldg + n0, hw, l);
+          if (at >= 0)
+            a.rsum[static_cast<int64_t>(2 * n + half) * a.T + t] =
+                store_bf16<false>(a.g + static_cast<int64_t>(at) * a.ldg + n0, hw, l);
         }
       } else if (MODE == kHeadProb) {
         const float lse = rok ? __ldcg(a.lse + t) : 0.0f;
@@ -776,7 +805,9 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < kCols; ++j) l[j] = counted ? exp2_fast(fmaf(l[j], kLog2e, -base)) : 0.0f;
         if (rok) {
-          store_bf16(a.g + static_cast<int64_t>(row) * a.ldg + n0, hw, l);
+          const float d = store_bf16<true>(a.g + static_cast<int64_t>(row) * a.ldg + n0, hw, l);
+          if (counted && fabsf(d) < 1.0f)  // (no NaN either)
+            atomicAdd(a.rounding + t, static_cast<unsigned long long>(__float2ll_rn(d / kRoundingUnit)));
           if (n0 == 0 && a.v0 == 0 && !counted && label != a.ignore && a.status) atomicOr(a.status, QLORA_DEV_LABEL);
         }
       }
@@ -840,6 +871,7 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const __grid_co
     if (warp == 0 && t0 + lane < end) {
       const int mine = at + __popc(mask & ((1u << lane) - 1));
       a.place[t0 + lane] = in ? mine : -1;
+      if (a.rounding) a.rounding[t0 + lane] = 0;
       if (in) a.rows[mine] = static_cast<int32_t>(t0 + lane);
       if (!in && label != a.ignore && a.status) atomicOr(a.status, QLORA_DEV_LABEL);
     }
@@ -866,6 +898,14 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const __grid_co
   if (end == T && threadIdx.x == 0) *a.nrows = at;
 }
 
+// The backward's sums of roundings, cleared where the rows are not listed.
+__global__ void __launch_bounds__(kRowsThreads) head_clear_kernel(unsigned long long* rounding, int64_t T) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRowsThreads + threadIdx.x;
+  if (t < T) rounding[t] = 0;
+}
+
 // ------------------------------------------------------------------- finish
 //
 // The parts of a tile joined in order, and dH's rows from them.  blockIdx.x:
@@ -890,8 +930,29 @@ __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_co
   if (row >= T || d >= a.ncols) return;
   const int t = a.rows ? __ldcg(a.rows + row) : row;
   const int at_row = static_cast<int>(blockIdx.y) * 8 * kSumStride + et;
-  float l[32] = {};
-  for (int part = 0; part < tail.parts; ++part) {
+  // the first part's sums on their way beside the chain of token, label and its row of W
+  const float4* part0 = reinterpret_cast<const float4*>(a.acc) +
+                        (static_cast<int64_t>(slot) * ctas + rank) * kSumBlock + at_row;
+  float4 o0[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o0[j] = __ldcg(part0 + j * kSumStride);
+  const int64_t label = __ldg(a.labels + t);
+  const bool counted = counts(label, a.ignore, a.vocab);
+  const int nd = min(32, a.ncols - d);
+  float cn = 0.0f, cs = 0.0f, cl = 0.0f;
+  float l[32] = {}, wr[32] = {};
+  if (counted) {
+    load_head_row(a.head, a.tab, label, d, nd, wr);
+    grad_row_factors(a, t, cn, cs, cl);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    l[4 * j] = o0[j].x;
+    l[4 * j + 1] = o0[j].y;
+    l[4 * j + 2] = o0[j].z;
+    l[4 * j + 3] = o0[j].w;
+  }
+  for (int part = 1; part < tail.parts; ++part) {
     const float4* at = reinterpret_cast<const float4*>(a.acc) +
                        (static_cast<int64_t>(slot + part) * ctas + rank) * kSumBlock + at_row;
 #pragma unroll
@@ -903,19 +964,16 @@ __global__ void __launch_bounds__(kSumStride) head_finish_kernel(const __grid_co
       l[4 * j + 3] += o.w;
     }
   }
-  const int64_t label = __ldg(a.labels + t);
-  const bool counted = counts(label, a.ignore, a.vocab);
-  float cn = 0.0f, cs = 0.0f, cl = 0.0f;
-  if (counted) grad_row_factors(a, t, cn, cs, cl);
-  store_grad32(a, t, label, counted, cn, cs, cl, d, min(32, a.ncols - d), l);
+  store_grad32(a, t, counted, cn, cs, cl, d, nd, wr, l);
 }
 
 // ------------------------------------------------------------------ combine
 //
 // Joins the (reference, sum) pairs of a row's parts (half tiles): R = max ref,
-// S = sum of s exp(ref - R), of all columns but the label's.  Step: R and S run over the pieces, exponentials of
-// parts whose reference is not R are rescaled in place (rows with logits beyond
-// +-40 only), and alpha = exp(R_old - R).  With the last piece: lse, loss, and
+// S = sum of s exp(ref - R), of all columns but the label's.  Step: R, S and the
+// sum of the roundings run over the pieces, exponentials of parts whose
+// reference is not R are rescaled in place (rows with logits beyond +-40 only),
+// and alpha = exp(R_old - R).  With the last piece: lse, loss, and
 // the mean in fp64 (per-block sums, added in block order by the block that
 // finishes last).  The label's logit is made here, in fp32 rounded to nearest:
 // the tensor core's drift grows with a logit, and the label's is the one that
@@ -931,12 +989,25 @@ namespace {
 
 constexpr int kCombineWarps = 16;
 
-__device__ __forceinline__ void join(float& R, float& S, float ref, float s) {
-  if (s == 0.0f) return;  // (a NaN is not equal and joins)
-  const float top = fmaxf(R, ref);
-  // R = -inf (nothing yet): the factor is 0
-  S = S * (R == top ? 1.0f : expf(R - top)) + s * (ref == top ? 1.0f : expf(ref - top));
-  R = top;
+// Reference, sum of exponentials, and their sum as rounded to bf16.
+struct Part {
+  float ref, sum, rsum;
+};
+
+template <bool STEP>
+__device__ __forceinline__ void join(Part& a, const Part& b) {
+  if (b.sum == 0.0f) return;          // (a NaN is not equal and joins)
+  if (!STEP || a.ref != b.ref) {      // (the step's ordinary rows: all 0)
+    const float top = fmaxf(a.ref, b.ref);
+    // a.ref = -inf (nothing yet): the factor is 0
+    const float fa = a.ref == top ? 1.0f : expf(a.ref - top), fb = b.ref == top ? 1.0f : expf(b.ref - top);
+    a.sum = a.sum * fa + b.sum * fb;
+    if (STEP) a.rsum = a.rsum * fa + b.rsum * fb;
+    a.ref = top;
+  } else {
+    a.sum += b.sum;
+    a.rsum += b.rsum;
+  }
 }
 
 __device__ __forceinline__ void store_mean(const HeadCombineArgs& a, double sum, int count) {
@@ -946,9 +1017,11 @@ __device__ __forceinline__ void store_mean(const HeadCombineArgs& a, double sum,
 
 }  // namespace
 
-template <int TB>
+template <int TB, bool STEP>
 __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const HeadCombineArgs a) {
   __shared__ float2 sm[kCombineWarps][TB];
+  __shared__ float sm_rsum[STEP ? kCombineWarps : 1][TB];
+  __shared__ float again[STEP ? kCombineWarps : 1][TB];  // what a second rounding added
   __shared__ float ref_s[TB];
   __shared__ bool last_block;
   __shared__ double sums[kCombineWarps];
@@ -973,51 +1046,61 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
   const int t0 = blockIdx.x * TB, t = t0 + tok;
   const bool rok = t < a.T;
 
-  float R = -INFINITY, S = 0.0f;
+  Part all{-INFINITY, 0.0f, 0.0f};
   float lo = INFINITY;  // smallest reference of a part with a sum
   if (rok) {
     for (int j0 = slice; j0 < a.nparts; j0 += 8 * kSlices) {
       float2 p[8];
+      float d[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int j = j0 + i * kSlices;
-        p[i] = j < a.nparts ? __ldcg(a.part + static_cast<int64_t>(j) * a.T + t) : make_float2(0.0f, 0.0f);
+        const int64_t at = static_cast<int64_t>(j) * a.T + t;
+        p[i] = j < a.nparts ? __ldcg(a.part + at) : make_float2(0.0f, 0.0f);
+        d[i] = STEP && j < a.nparts ? __ldcg(a.rsum + at) : 0.0f;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        join(R, S, p[i].x, p[i].y);
+        join<STEP>(all, {p[i].x, p[i].y, d[i]});
         if (p[i].y != 0.0f) lo = fminf(lo, p[i].x);
       }
     }
   }
 #pragma unroll
   for (int o = 16; o >= TB; o >>= 1) {  // lanes of the same token
-    const float r = __shfl_xor_sync(0xFFFFFFFFu, R, o), s = __shfl_xor_sync(0xFFFFFFFFu, S, o);
+    const Part other{__shfl_xor_sync(0xFFFFFFFFu, all.ref, o), __shfl_xor_sync(0xFFFFFFFFu, all.sum, o),
+                     STEP ? __shfl_xor_sync(0xFFFFFFFFu, all.rsum, o) : 0.0f};
     // the lower lane's value first, so that both get the same bits
-    float r2 = (lane & o) ? r : R, s2 = (lane & o) ? s : S;
-    join(r2, s2, (lane & o) ? R : r, (lane & o) ? S : s);
-    R = r2;
-    S = s2;
+    Part both = (lane & o) ? other : all;
+    join<STEP>(both, (lane & o) ? all : other);
+    all = both;
   }
-  if (lane < TB) sm[warp][lane] = make_float2(R, S);
+  if (lane < TB) {
+    sm[warp][lane] = make_float2(all.ref, all.sum);
+    if (STEP) {
+      sm_rsum[warp][lane] = all.rsum;
+      again[warp][lane] = 0.0f;
+    }
+  }
   __syncthreads();
   if (warp == 0) {
     bool counted = false;
     double sum = 0.0;
     if (lane < TB) {
-      for (int w = 1; w < kCombineWarps; ++w) join(R, S, sm[w][lane].x, sm[w][lane].y);
-      if (a.run && rok) {
-        if (!a.first) {
-          const float2 old = __ldcg(a.run + t);
-          join(R, S, old.x, old.y);
-          a.alpha[t] = (old.y == 0.0f || old.x == R) ? 1.0f : expf(old.x - R);
-        }
-        a.run[t] = make_float2(R, S);
+      for (int w = 1; w < kCombineWarps; ++w) {
+        const float2 v = sm[w][lane];
+        join<STEP>(all, {v.x, v.y, STEP ? sm_rsum[w][lane] : 0.0f});
       }
-      ref_s[lane] = R;
+      if (STEP && rok && !a.first) {
+        const float2 old = __ldcg(a.run + t);
+        join<STEP>(all, {old.x, old.y, __ldcg(a.run_rsum + t)});
+        a.alpha[t] = (old.y == 0.0f || old.x == all.ref) ? 1.0f : expf(old.x - all.ref);
+      }
+      ref_s[lane] = all.ref;
       if (a.last && rok) {
         const int64_t label = a.labels[t];
         counted = counts(label, a.ignore, a.vocab);
+        const float R = all.ref, S = all.sum;
         float lse = R + logf(S), loss = 0.0f;
         if (counted) {
           float z = dot[lane][0];
@@ -1030,10 +1113,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
           const float x = (S * e) * e;
           loss = x < 1e30f ? log1pf(x) : (R - z) + logf(S);
           lse = top + logf(S * expf(R - top) + expf(z - top));  // (no others: R = -inf, S = 0)
-          if (a.row_root) {  // and the root of 1 / (S + exp(z - R)), which overflows no earlier than it should
-            a.row_root[t] = z > R ? e / sqrtf(1.0f + x) : 1.0f / sqrtf(S + expf(z - R));
-            a.p_label[t] = expm1f(-loss);
-          }
+          // and the root of 1 / (S + exp(z - R)), which overflows no earlier than it should
+          if (STEP) a.row_root[t] = z > R ? e * rsqrtf(1.0f + x) : rsqrtf(S + expf(z - R));
         }
         a.lse[t] = lse;
         a.loss[t] = loss;
@@ -1064,10 +1145,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
     }
   }
   __syncthreads();
-  if (a.e) {
+  if constexpr (STEP) {
     const float ref = ref_s[tok];
     // (no part of this thread: lo = inf)
-    if (__syncthreads_or(rok && lo < ref)) {
+    const bool rescale = __syncthreads_or(rok && lo < ref);
+    if (rescale) {
       for (int j = slice; j - slice < a.nparts; j += kSlices) {
         const float2 p = rok && j < a.nparts ? __ldcg(a.part + static_cast<int64_t>(j) * a.T + t)
                                              : make_float2(0.0f, 0.0f);
@@ -1079,14 +1161,32 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
           const float fr = __shfl_sync(0xFFFFFFFFu, f, src);
           const int js = __shfl_sync(0xFFFFFFFFu, j, src), ts = __shfl_sync(0xFFFFFFFFu, t, src);
           const int row = a.place ? __ldcg(a.place + ts) : ts;
-          if (row < 0 || 4 * lane >= a.part_cols) continue;
-          uint2* at = reinterpret_cast<uint2*>(a.e + static_cast<int64_t>(row) * a.lde +
-                                               static_cast<int64_t>(js) * a.part_cols) + lane;
-          const uint2 v = __ldcg(at);
-          *at = make_uint2(pack_bf16x2(__uint_as_float(v.x << 16) * fr, __uint_as_float(v.x & 0xFFFF0000u) * fr),
-                           pack_bf16x2(__uint_as_float(v.y << 16) * fr, __uint_as_float(v.y & 0xFFFF0000u) * fr));
+          if (row < 0) continue;
+          float d = 0.0f;
+          if (4 * lane < a.part_cols) {
+            uint2* at = reinterpret_cast<uint2*>(a.e + static_cast<int64_t>(row) * a.lde +
+                                                 static_cast<int64_t>(js) * a.part_cols) + lane;
+            const uint2 v = __ldcg(at);
+            const float x[4] = {__uint_as_float(v.x << 16) * fr, __uint_as_float(v.x & 0xFFFF0000u) * fr,
+                                __uint_as_float(v.y << 16) * fr, __uint_as_float(v.y & 0xFFFF0000u) * fr};
+            const uint2 y = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+            *at = y;
+            d = ((__uint_as_float(y.x << 16) - x[0]) + (__uint_as_float(y.x & 0xFFFF0000u) - x[1])) +
+                ((__uint_as_float(y.y << 16) - x[2]) + (__uint_as_float(y.y & 0xFFFF0000u) - x[3]));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+          if (lane == 0) again[warp][ts - t0] += d;
         }
       }
+      __syncthreads();
+    }
+    if (warp == 0 && lane < TB && rok) {
+#pragma unroll 1
+      for (int w = 0; rescale && w < kCombineWarps; ++w) all.rsum += again[w][lane];
+      a.run[t] = make_float2(all.ref, all.sum);
+      a.run_rsum[t] = all.rsum;
+      if (a.last) a.coef[t] = -all.rsum;
     }
   }
   if (a.last && a.place) {  // rows of dH that no product writes
@@ -1151,6 +1251,11 @@ cudaError_t launch_head_finish(const HeadArgs& a, int tiles, cudaStream_t stream
                        dim3(1, 1, 1), a);
 }
 
+cudaError_t launch_head_clear(unsigned long long* rounding, int64_t T, cudaStream_t stream) {
+  return launch_kernel(head_clear_kernel, dim3(static_cast<unsigned>((T + kRowsThreads - 1) / kRowsThreads)),
+                       dim3(kRowsThreads), 0, stream, dim3(1, 1, 1), rounding, T);
+}
+
 cudaError_t launch_head_rows(HeadRowsArgs a, cudaStream_t stream) {
   a.chunk = (a.T + 591) / 592;  // four blocks an SM
   return launch_kernel(head_rows_kernel, dim3(static_cast<unsigned>((a.T + a.chunk - 1) / a.chunk)),
@@ -1166,7 +1271,9 @@ int head_combine_blocks(int64_t T) {
 }
 
 cudaError_t launch_head_combine(const HeadCombineArgs& a, cudaStream_t stream) {
-  return launch_kernel(combine_tokens(a.T) == 32 ? head_combine_kernel<32> : head_combine_kernel<4>,
+  const bool wide = combine_tokens(a.T) == 32;
+  return launch_kernel(a.run ? (wide ? head_combine_kernel<32, true> : head_combine_kernel<4, true>)
+                             : (wide ? head_combine_kernel<32, false> : head_combine_kernel<4, false>),
                        dim3(head_combine_blocks(a.T)), dim3(kCombineWarps * 32), 0, stream, dim3(1, 1, 1), a);
 }
 

@@ -108,9 +108,12 @@ struct HeadArgs {
   int tw;                 // columns of a tile: a multiple of 32 up to 256, NF4 128 (Grad: 256)
   const int64_t* labels;
   int64_t ignore;
-  float2* part;         // Loss, Exp: (reference, sum of the others' exponentials) [half tile][T], from the piece's first
+  float2* part;           // Loss, Exp: (reference, sum of the others' exponentials) [half tile][T], from the piece's first
+  float* rsum;            // Exp: their sum as rounded to bf16, [half tile][T]
+  // Prob, Grad (backward): what rounding the probabilities added to their sum, [T] integers, cleared before
+  unsigned long long* rounding;
   const float* lse;       // Prob: [T]
-  float* p_label_out;     // Prob: [T] probability of the label less 1, or null
+  float* coef_out;        // Prob: [T] probability of the label less 1, or null
   const uint16_t* h;      //   from the operand's rows, stride ldh
   int64_t ldh;
   uint16_t* g;            // Prob, Exp: [rows, ldg]
@@ -126,7 +129,7 @@ struct HeadArgs {
   const float* dloss;     // per-token gradients, or one number with `stats` (backward)
   const float* stats;
   const float* row_root;  // [T] 1 / root of the softmax denominators (step), null in the backward
-  const float* p_label;   // [T] probability of the label less 1
+  const float* coef;      // [T] coefficient of W[label] beside the sum: backward, probability of the label less 1
   const float* weight;    // [T] or null (step)
   float scale;
   const int32_t* count;   // tokens that count (step, weight null)
@@ -147,12 +150,14 @@ struct HeadRowsArgs {
   const int64_t* labels;
   int64_t ignore, vocab, T, chunk;
   int32_t *rows, *place, *nrows, *status;
+  unsigned long long* rounding;  // [T] to be cleared, or null
   const uint16_t* h;
   int64_t ldh, dim;
   uint16_t *out, *dh;
   int64_t ldd;
 };
 cudaError_t launch_head_rows(HeadRowsArgs a, cudaStream_t stream);
+cudaError_t launch_head_clear(unsigned long long* rounding, int64_t T, cudaStream_t stream);
 
 // Joins the parts of Grad's tiles after the last piece; `tiles`: an upper bound
 // of those in parts.
@@ -171,7 +176,9 @@ struct HeadCombineArgs {
   int64_t ignore;
   int64_t vocab;
   int first, last;         // of the pieces (the forward combines once: both)
-  float2* run;             // step: running (reference, sum) [T]
+  const float* rsum;       // step: [nparts][T] sum of the exponentials as rounded
+  float2* run;             // step: running (reference, sum) [T], and of the rounded
+  float* run_rsum;
   float* alpha;            // step: [T]
   uint16_t* e;             // step: the piece's exponentials [rows, lde], or null
   int64_t lde;
@@ -179,7 +186,7 @@ struct HeadCombineArgs {
   uint16_t* dh;            //   the other rows of dH become zero
   int64_t ldd, dim;
   float* row_root;         // step: [T] 1 / root of the softmax denominator
-  float* p_label;          // step: [T]
+  float* coef;             // step: [T] coefficient of the label's row of W
   int32_t* counters;       // [2]: tokens that count, blocks done; cleared before
   double* block_sum;       // [blocks]
   float* loss;

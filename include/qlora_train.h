@@ -17,7 +17,8 @@
  * enqueue work on `stream`; errors are reported before any work is enqueued;
  * pointers are 16-byte aligned; device-side conditions are OR-ed into the
  * optional device word d_status.  Results do not depend on the timing of the
- * GPU: sums run in a fixed order, and repeated calls are bitwise identical.
+ * GPU: sums run in a fixed order or are of integers, and repeated calls are
+ * bitwise identical.
  */
 #ifndef QLORA_TRAIN_H
 #define QLORA_TRAIN_H
@@ -149,17 +150,24 @@ typedef struct {
  * their type's alignment only (a shifted view of the labels is fine).
  * Workspaces: qlora_head_loss_workspace_size(T, vocab, dim, nf4, op) bytes with
  * nf4 nonzero for an NF4 head and op one of QLORA_HEAD_FWD / _BWD / _STEP.
- * Beside per-token words it holds 8 bytes per half tile of logits (128, or
- * fewer columns where that fills the GPU; forward, step), a piece of the
+ * Beside per-token words it holds per half tile of logits (128, or fewer
+ * columns where that fills the GPU) 8 bytes (forward) or 12 (step), a piece of the
  * probabilities (backward, step: about 128 MB in bf16, at least 2048 columns),
  * the rows of H that count (backward of larger calls: bf16 [T, dim]), fp32 sums
  * [T, dim] (with several pieces) and of tiles of dH whose contraction is
  * divided (at most 39 MB), and, for more than 128 tokens, a dequantised piece of an
  * NF4 head (at most 128 MB, at least 2048 rows).
  * Accuracy: exact bf16 inputs, fp32 accumulation and softmax; a small loss keeps
- * its digits (the label's logit stays out of the sum); the probabilities
- * enter the second product as bf16 (the label's term is added in fp32); dH
- * within 5e-3 relative Frobenius error of the fp64 gradient.
+ * its digits (the label's logit stays out of the sum).  The probabilities of the
+ * others enter the second product as bf16, the label's coefficient in fp32 with
+ * their roundings in it, so that what W's rows share cancels in dH.  Beside what
+ * the logits' fp32 errors make of p, an element of dH is off by at most
+ *   |g_t| (2^-8 sum_v p_tv |W_vd - W_label,d| + e sum_v p_tv |W_vd|) + 2^-8 |dH_td|
+ * (2 2^-8 in a row of the step that has logits beyond +-40), with e = 2^-23 for
+ * every 16 columns of a piece (measured: about 2^-26): the fp32 sum.  On random
+ * data that is 1.7e-3 relative (Frobenius).  The backward's label coefficient,
+ * expm1(l_label - lse), has the rounding of the lse that it is given, 2^-24
+ * |lse| absolute, the step's has not: it keeps its digits for any token.
  */
 #define QLORA_HEAD_FWD 0
 #define QLORA_HEAD_BWD 1

@@ -557,3 +557,49 @@ def test_label_logits_far_above_others_near_forty(T, V, D):
         assert np.all(np.abs(out[0].double().cpu().numpy() - loss) <= 2.0 ** -15 * loss)
     err = np.abs(got[3].double().cpu().numpy() - ref)
     assert np.all(err <= (2.0 ** -8 * 1.01 + 2.0 ** -14) * size + 2.0 ** -8 * np.abs(ref))
+
+
+@pytest.mark.parametrize("T,V,D,nf4,std", [(64, 3000, 256, False, 2.0), (300, 9000, 320, False, 2.0),
+                                           (1000, 70000, 64, False, 2.0), (2000, 12500, 1024, False, 2.0),
+                                           (64, 3000, 256, False, 15.0), (2000, 12500, 1024, False, 15.0),
+                                           (64, 3000, 256, True, 2.0), (520, 5000, 256, True, 2.0)])
+def test_what_the_heads_rows_share_cancels(T, V, D, nf4, std):
+    """Rows of W with a common part of 30 times their own: the coefficients of a
+    row of dH sum to zero, rounded or not, so an error of p_v, whatever its cause,
+    moves dH by W_v - W_label.  H has 8 columns, so a logit is off by at most
+    d = 2 8 2^-24 sum |h w| (the others add zeros), p relatively by rel = 2 d +
+    2^-20 (4 + max|l|), and by its rounding, 2^-8 (twice for a rescaled row).  What
+    does not cancel: the fp32 sum over the vocabulary, at most 2^-23 of it a step of
+    16 columns, and in the backward the error of expm1(l - lse), rel."""
+    g = torch.Generator().manual_seed(17)
+    w = 0.6 * torch.randn(D, generator=g) + 0.02 * torch.randn(V, D, generator=g)
+    w[:, :8] = torch.randn(V, 8, generator=g)
+    h = torch.zeros(T, D)
+    h[:, :8] = std * torch.randn(T, 8, generator=g)
+    H, W = h.to(torch.bfloat16).cuda(), w.to(torch.bfloat16).cuda()
+    if nf4:
+        N = q.quantize_weight(W)
+        W = q.nf4_dequantize(N.codes, N.c8, N.s2, V * D).view(V, D)
+    y = torch.topk(H.double() @ W.double().t(), 4, dim=1)[1][:, 1].clone()  # a likely token
+    y[::4] = torch.randint(0, V, (T,), generator=g)[::4].cuda()
+    y[1::8] = -100
+    gr = torch.linspace(-1, 2, T, device="cuda")
+    lse = q.qlora_head_loss_fwd(H, N if nf4 else W, y)[1]
+    back = q.qlora_head_loss_bwd(H, N if nf4 else W, y, lse, gr)
+    step = q.qlora_head_loss_step(H, N if nf4 else W, y, weight=gr)[3]
+
+    rows = torch.nonzero(y != -100)[:, 0]
+    rows = rows[torch.linspace(0, rows.numel() - 1, min(150, rows.numel()), device="cuda").long()]
+    x, v, t = H[rows].double(), W.double(), gr[rows].double()[:, None]
+    z = x @ v.t()
+    p = torch.softmax(z, 1).scatter(1, y[rows, None], 0.0)
+    wy = v[y[rows]]
+    ref = t * (p @ v - p.sum(1, keepdim=True) * wy)
+    apart = torch.stack([(p[i, :, None] * (v - wy[i]).abs()).sum(0) for i in range(len(rows))])
+    size = p @ v.abs() + p.sum(1, keepdim=True) * wy.abs()
+    rel = 2 * 16 * 2.0 ** -24 * (x.abs() @ v.abs().t()).amax(1) + 2.0 ** -20 * (4 + z.abs().amax(1))
+    for d, rounds, leak in ((back, 1, rel[:, None] * wy.abs()), (step, 2 if std > 2 else 1, 0)):
+        tol = t.abs() * ((rounds * 2.0 ** -8 * 1.01 + 2 * rel[:, None]) * apart + (V / 16 + 8) * 2.0 ** -23 * size
+                         + leak) + 2.0 ** -8 * ref.abs() + 1e-37
+        assert bool(((d[rows].double() - ref).abs() <= tol).all())
+        assert not d[y == -100].any()
