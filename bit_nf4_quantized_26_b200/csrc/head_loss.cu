@@ -808,7 +808,10 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
           const float d = store_bf16<true>(a.g + static_cast<int64_t>(row) * a.ldg + n0, hw, l);
           if (counted && fabsf(d) < 1.0f)  // (no NaN either)
             atomicAdd(a.rounding + t, static_cast<unsigned long long>(__float2ll_rn(d / kRoundingUnit)));
-          if (n0 == 0 && a.v0 == 0 && !counted && label != a.ignore && a.status) atomicOr(a.status, QLORA_DEV_LABEL);
+          if (n0 == 0 && a.v0 == 0 && a.status) {
+            if (!counted && label != a.ignore) atomicOr(a.status, QLORA_DEV_LABEL);
+            if (counted && !isfinite(lse)) atomicOr(a.status, QLORA_DEV_NONFINITE);
+          }
         }
       }
     }

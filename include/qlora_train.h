@@ -107,7 +107,8 @@ QLORA_API qlora_status qlora_linear_bwd_dropout_act8(const uint16_t* dY, const u
  * included: its loss and its row of dH are exactly 0 (its lse is that of the
  * row as it stands).  Larger calls leave ignored rows out of the products that
  * make dH: a batch whose prompts are ignored costs that much less.  A
- * non-finite lse of a token that counts sets QLORA_DEV_NONFINITE.
+ * non-finite lse of a token that counts, made by the forward or the step or
+ * given to the backward, sets QLORA_DEV_NONFINITE.
  *
  * The head: W [vocab, dim], either bf16 rows (`w`, row stride ld elements,
  * ld % 8 == 0, dim % 8 == 0) or, with w == NULL, NF4 (codes, c8, s2 and an

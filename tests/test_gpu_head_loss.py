@@ -603,3 +603,22 @@ def test_what_the_heads_rows_share_cancels(T, V, D, nf4, std):
                          + leak) + 2.0 ** -8 * ref.abs() + 1e-37
         assert bool(((d[rows].double() - ref).abs() <= tol).all())
         assert not d[y == -100].any()
+
+
+@pytest.mark.parametrize("T,V,D", [(40, 300, 64), (300, 5000, 128), (600, 20000, 2304)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_backward_reports_a_non_finite_lse(T, V, D, bad):
+    """Of a token that counts; its row only is lost.  The last size lists its rows."""
+    h, w, y = _case(T, V, D, seed=18, ignored=0.0)
+    y[5] = -100
+    H, W, Y, g = h.cuda(), w.cuda(), y.cuda(), torch.ones(T, device="cuda")
+    lse = q.qlora_head_loss_fwd(H, W, Y)[1]
+    want = q.qlora_head_loss_bwd(H, W, Y, lse, g)
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    lse[5] = bad                                          # an ignored token's is not read
+    assert torch.equal(q.qlora_head_loss_bwd(H, W, Y, lse, g, status=status), want) and int(status[0]) == 0
+    lse[T - 2] = bad
+    got = q.qlora_head_loss_bwd(H, W, Y, lse, g, status=status)
+    assert int(status[0]) == q.DEV_NONFINITE
+    keep = torch.arange(T, device="cuda") != T - 2
+    assert torch.equal(got[keep], want[keep])
