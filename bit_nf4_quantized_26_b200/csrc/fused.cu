@@ -750,13 +750,8 @@ __global__ void __launch_bounds__(192, 1)
 template <bool DX>
 static cudaError_t launch_fused2x_impl(const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& m2,
                                        const CUtensorMap& m3, const FusedArgs& a, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(fused2x_kernel<DX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Plan2x::kSmem));
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static uint64_t done = 0;
+  if (cudaError_t e = allow_smem(fused2x_kernel<DX>, Plan2x::kSmem, done)) return e;
   dim3 grid((a.rows + 127) / 128, (a.M + 511) / 512, 1);
   return launch_kernel(fused2x_kernel<DX>, grid, dim3(192), Plan2x::kSmem, stream, dim3(1, 1, 1), m0, m1, m2, m3, a);
 }
@@ -771,13 +766,8 @@ template <int BN, bool DX, int DQW>
 static cudaError_t launch_fused_impl(const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& m2,
                                      const CUtensorMap& m3, const FusedArgs& a, int splits, cudaStream_t stream) {
   using P = FusedPlan<BN>;
-  static bool attr_set = false;  // benign race: setting the same value twice is harmless
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(fused_kernel<BN, DX, DQW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(P::kSmem));
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static uint64_t done = 0;
+  if (cudaError_t e = allow_smem(fused_kernel<BN, DX, DQW>, P::kSmem, done)) return e;
   if (splits < 1 || splits > 8) return cudaErrorInvalidValue;
   dim3 grid((a.rows + 127) / 128, (a.M + BN - 1) / BN, splits);
   // A split contraction runs as a cluster of its slices (reduced in-cluster).

@@ -378,13 +378,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 template <bool DX>
 static cudaError_t launch_pair_impl(const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& m2,
                                     const CUtensorMap& m3, const FusedArgs& a, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(fused_pair_kernel<DX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(PlanPair::kSmem));
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static uint64_t done = 0;
+  if (cudaError_t e = allow_smem(fused_pair_kernel<DX>, PlanPair::kSmem, done)) return e;
   return launch_kernel(fused_pair_kernel<DX>, dim3(2 * ((a.rows + 255) / 256), (a.M + 511) / 512, 1), dim3(kPairThreads),
                        PlanPair::kSmem, stream, dim3(2, 1, 1), m0, m1, m2, m3, a);
 }

@@ -371,13 +371,8 @@ static cudaError_t launch_pair_fwd_impl(const CUtensorMap& tm_b, const CUtensorM
                                         cudaStream_t stream) {
   using P = PlanPairT<ASLOTS>;
   if (a.r / 16 > static_cast<int>(P::kExtBufs)) return cudaErrorInvalidValue;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(fused_pair_fwd_kernel<ASLOTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(P::kSmem));
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static uint64_t done = 0;
+  if (cudaError_t e = allow_smem(fused_pair_fwd_kernel<ASLOTS>, P::kSmem, done)) return e;
   const int tok = 2 * P::kN;
   return launch_kernel(fused_pair_fwd_kernel<ASLOTS>, dim3(2 * ((a.rows + 255) / 256), (a.M + tok - 1) / tok, 1),
                        dim3(320), P::kSmem, stream, dim3(2, 1, 1), tm_b, tm_codes, tm_uc, tm_ext, a);

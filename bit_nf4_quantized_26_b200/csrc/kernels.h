@@ -7,6 +7,7 @@
 #include <utility>
 
 #include "nf4_lut.cuh"
+#include "smem_limit.h"
 
 namespace qnf4 {
 

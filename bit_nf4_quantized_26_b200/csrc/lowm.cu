@@ -398,13 +398,8 @@ __global__ void __launch_bounds__(kLowmThreads, 2)
 template <int NT>
 static cudaError_t launch_lowm_impl(const CUtensorMap& tm_codes, const CUtensorMap& tm_x, const LowmArgs& a,
                                     cudaStream_t stream) {
-  static bool attr_set = false;  // benign race: setting the same value twice is harmless
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(lowm_fwd_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(LowmPlan<NT>::kSmem));
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static uint64_t done = 0;
+  if (cudaError_t e = allow_smem(lowm_fwd_kernel<NT>, LowmPlan<NT>::kSmem, done)) return e;
   return launch_kernel(lowm_fwd_kernel<NT>, dim3(a.ctas), dim3(kLowmThreads), LowmPlan<NT>::kSmem, stream,
                        dim3(1, 1, 1), tm_codes, tm_x, a);
 }

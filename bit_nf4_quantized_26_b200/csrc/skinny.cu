@@ -437,13 +437,8 @@ template <int MODE, bool SUMMED = false>
 static cudaError_t launch_skinny_impl(const CUtensorMap& tmA, const CUtensorMap& tmB, const SkinnyArgs& a,
                                       int grid_rows, int splits, cudaStream_t stream) {
   using P = SkPlan<MODE, SUMMED>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(skinny_kernel<MODE, SUMMED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(P::kSmem));
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static uint64_t done = 0;
+  if (cudaError_t e = allow_smem(skinny_kernel<MODE, SUMMED>, P::kSmem, done)) return e;
   if (splits < 1 || splits > 8) return cudaErrorInvalidValue;
   // Unsplit products run beside a CTA-pair GEMM: launched as clusters of two
   // row tiles they sit on both SMs of a TPC, rather than on one SM of many

@@ -8,20 +8,6 @@
 
 namespace qnf4 {
 
-// Raises a kernel's dynamic shared-memory limit once per device (a kernel's
-// attributes belong to the device that is current when they are set).
-template <typename F>
-inline cudaError_t allow_smem(F kernel, uint32_t bytes, uint64_t& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (__atomic_load_n(&done, __ATOMIC_RELAXED) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess) __atomic_fetch_or(&done, bit, __ATOMIC_RELAXED);
-  return e;
-}
-
 // ------------------------------------------------------------------ act8.cu
 
 cudaError_t launch_act8_quantize(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, uint8_t* codes, uint8_t* exps,
