@@ -613,15 +613,15 @@ def _refuse(code, where, what):
     raise QloraError(code, f"{where}: {what}")
 
 
-def _tensor(t, dtype, shape, dev, where, name):
-    """A contiguous tensor of this type and shape on this device."""
+def _tensor(t, dtype, shape, dev, where, name, dense=True):
+    """A tensor of this type and shape on this device, contiguous if ``dense``."""
     if t.dtype != dtype:
         _refuse(ERR_DTYPE, where, f"{name} is {t.dtype}, not {dtype}")
     if t.shape != shape:
         _refuse(ERR_SHAPE, where, f"{name} is {tuple(t.shape)}, not {shape}")
     if t.device != dev:
         _refuse(ERR_SHAPE, where, f"{name} is on {t.device}, not {dev}")
-    if not t.is_contiguous():
+    if dense and not t.is_contiguous():
         _refuse(ERR_SHAPE, where, f"{name} is not contiguous")
     return t
 
@@ -888,20 +888,24 @@ def qlora_head_loss_bwd(H, head, labels, lse, dloss, stats=None, ignore_index=IG
                         status=None, stream=None):
     """Gradient of the losses of :func:`qlora_head_loss_fwd` towards ``H`` (bf16
     [T, dim]): ``dloss`` [T] holds the gradient of every token's loss, or, with
-    the forward's ``stats`` given, ``dloss`` [1] the gradient of the mean."""
+    the forward's ``stats`` given, ``dloss`` (one element, of no or one dimension)
+    the gradient of the mean.  It may have any strides, as autograd hands over
+    the gradient of a sum (one element expanded): a dense copy is made then."""
     where = "qlora_head_loss_bwd"
     T, D, ldh, dev, h, size = _head_call(where, HEAD_BWD, H, head, labels)
     _tensor(lse, torch.float32, (T,), dev, where, "lse")
-    _tensor(dloss, torch.float32, (T if stats is None else 1,), dev, where, "dloss")
+    if stats is not None and dloss.dim() == 0:
+        dloss = dloss.view(1)
+    _tensor(dloss, torch.float32, (T if stats is None else 1,), dev, where, "dloss", dense=False)
     if stats is not None:
         _tensor(stats, torch.float32, (2,), dev, where, "stats")
     ldd, grad = _grad_out(H, dH, T, D, dev, where)
 
     def call(st):
-        g = grad()
+        g, dl = grad(), dloss.contiguous()
         at, bytes_, keep = _workspace(ws, size, H, where)
         _check(_lib.qlora_head_loss_bwd(H.data_ptr(), ldh, T, h, labels.data_ptr(), int(ignore_index), lse.data_ptr(),
-                                        dloss.data_ptr(), None if stats is None else stats.data_ptr(), g.data_ptr(),
+                                        dl.data_ptr(), None if stats is None else stats.data_ptr(), g.data_ptr(),
                                         ldd, at, bytes_, _word(status, dev, where), st), where)
         return g
     return _run(dev, stream, call)

@@ -622,3 +622,44 @@ def test_backward_reports_a_non_finite_lse(T, V, D, bad):
     assert int(status[0]) == q.DEV_NONFINITE
     keep = torch.arange(T, device="cuda") != T - 2
     assert torch.equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("T,V,D", [(40, 300, 64), (600, 20000, 2304)])
+def test_gradients_of_the_losses_as_autograd_gives_them(T, V, D):
+    """Of a sum (one element expanded), of a mean (no dimension), and a column of a
+    matrix; the loss as a node of autograd."""
+    h, w, y = _case(T, V, D, seed=19)
+    H, W, Y = h.cuda(), w.cuda(), y.cuda()
+    loss, lse, stats = q.qlora_head_loss_fwd(H, W, Y)
+    two = torch.full((1,), 2.0, device="cuda")
+    want = q.qlora_head_loss_bwd(H, W, Y, lse, two.repeat(T))
+    assert torch.equal(q.qlora_head_loss_bwd(H, W, Y, lse, two.expand(T)), want)
+    g = torch.rand(T, 3, device="cuda")
+    assert torch.equal(q.qlora_head_loss_bwd(H, W, Y, lse, g[:, 1]),
+                       q.qlora_head_loss_bwd(H, W, Y, lse, g[:, 1].contiguous()))
+    mean = q.qlora_head_loss_bwd(H, W, Y, lse, two, stats=stats)
+    assert torch.equal(q.qlora_head_loss_bwd(H, W, Y, lse, two[0], stats=stats), mean)
+
+    class Loss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, reduce):
+            loss, lse, stats = q.qlora_head_loss_fwd(x, W, Y)
+            ctx.save_for_backward(x, lse, stats)
+            ctx.reduce = reduce
+            return stats[0].clone() if reduce else loss
+
+        @staticmethod
+        def backward(ctx, grad):
+            x, lse, stats = ctx.saved_tensors
+            return q.qlora_head_loss_bwd(x, W, Y, lse, grad, stats=stats if ctx.reduce else None), None
+
+    for reduce, ref in ((False, want), (True, mean)):
+        x = H.clone().requires_grad_()
+        (2 * Loss.apply(x, reduce).sum()).backward()
+        assert torch.equal(x.grad, ref)
+    for bad in (two.expand(T + 1), two[0], two.double().expand(T), two.cpu().expand(T)):
+        with pytest.raises(q.QloraError):
+            q.qlora_head_loss_bwd(H, W, Y, lse, bad)
+    for bad in (two.repeat(2), two.view(1, 1), two[0].double()):
+        with pytest.raises(q.QloraError):
+            q.qlora_head_loss_bwd(H, W, Y, lse, bad, stats=stats)
