@@ -66,7 +66,9 @@ QLORA_API qlora_status act8_dequantize(const uint8_t* codes, const uint8_t* exps
  * zeros): dA = dU^T X', everything else by the same formulas.  The rank-r
  * products (dU, dB, dA) take dU and s U as three bf16 parts (24 bits) and join
  * their accumulator's sums every 512 terms in fp32 with rounding to nearest: dA
- * and dB within 4e-6 relative Frobenius error, whatever the number of tokens.
+ * and dB within 4e-6 of the sums of their terms' absolute values, whatever the
+ * number of tokens (dA_jk: s sum_mn |dY_mn B_nj X'_mk|, dB_nj: s sum_m |dY_mn
+ * U_mj|), and of random data within 4e-6 relative Frobenius error.
  * Arguments, constraints and errors as for qlora_linear_bwd, qlora_group_bwd
  * and qlora_linear_bwd_dropout; the workspace is
  * qlora_bwd_act8_workspace_size(M, N, K, members, r, dropout) bytes (members 1

@@ -188,3 +188,27 @@ def test_refusals_on_device_tensors():
                  (dY, q.Act8(x8.codes[:2], x8.exps), U, W, A, B), (dY.t().contiguous().t(), x8, U, W, A, B)):
         with pytest.raises(q.QloraError):
             q.qlora_linear_bwd_act8(*args, 1.0)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(64, 512, 512, 16), (1000, 384, 448, 64), (4096, 1024, 256, 64)])
+def test_sums_that_cancel(M, N, K, r):
+    """Tokens in pairs whose terms of dA and dB nearly cancel: the errors stay within
+    4e-6 of the sums of the terms' absolute values (the derivation at the top)."""
+    gen = torch.Generator().manual_seed(M)
+
+    def rnd(*s, std=1.0):
+        return torch.randn(*s, generator=gen) * std
+    X, dY = rnd(M, K), rnd(M, N)
+    X[1::2] = X[::2]
+    dY[1::2] = -dY[::2] * (1 + 2.0 ** -6 * (rnd(M // 2, 1) > 0))
+    X, dY, A, B = (t.to(torch.bfloat16).cuda() for t in (X, dY, rnd(r, K, std=K ** -0.5), rnd(N, r, std=0.1)))
+    W = q.quantize_weight(rnd(N, K, std=0.02).to(torch.bfloat16).cuda())
+    U = X.float() @ A.float().t()
+    x8 = q.act8_quantize(X)
+    _, dA, dB = q.qlora_linear_bwd_act8(dY, x8, U, W, A, B, 0.5)
+    x = torch.from_numpy(act8.dequantize(x8.codes.cpu().numpy(), x8.exps.cpu().numpy())).cuda()
+    dY, B, U = dY.double(), B.double(), U.double()
+    for a, ref, size in ((dA, (0.5 * (dY @ B)).t() @ x, 0.5 * (dY.abs() @ B.abs()).t() @ x.abs()),
+                         (dB, 0.5 * (dY.t() @ U), 0.5 * (dY.abs().t() @ U.abs()))):
+        assert float(ref.norm()) < 0.1 * float(size.norm())
+        assert bool(((a.double() - ref).abs() <= 4e-6 * size).all())
