@@ -190,6 +190,43 @@ def test_refusals_on_device_tensors():
             q.qlora_linear_bwd_act8(*args, 1.0)
 
 
+@pytest.mark.parametrize("M,N,K,r,p,centred", [(16, 320, 512, 16, 0.05, False), (600, 512, 768, 64, 0.5, True),
+                                               (150, 384, 448, 144, 0.1, False), (1153, 768, 256, 256, 0.3, True)])
+def test_dropout_bwd_act8_against_the_formulas(M, N, K, r, p, centred):
+    """dA = dU^T X_drop', dB = s dY^T U, dX = dY W' + keep / (1 - p) (dU A), dU = s dY B."""
+    d = synth.linear_inputs(synth.Linear("a8f", N, K), M, r, 4)
+    g = {k: v.cuda() for k, v in d.items()}
+    W = (q.quantize_weight_centered if centred else q.quantize_weight)(g["W"])
+    dense = (q.nf4_dequantize_centered(W.codes, W.c8, W.s2, W.mean, N * K) if centred
+             else q.nf4_dequantize(W.codes, W.c8, W.s2, N * K)).view(N, K).double()
+    _, U, Xd = q.qlora_linear_fwd_dropout(g["X"], W, g["A"], g["B"], 0.25, p, 12)
+    x8 = q.act8_quantize(Xd)
+    got = q.qlora_linear_bwd_dropout_act8(g["dY"], x8, U, W, g["A"], g["B"], 0.25, p, 12)
+    x = torch.from_numpy(act8.dequantize(x8.codes.cpu().numpy(), x8.exps.cpu().numpy())).cuda()
+    dY, A, B = (g[k].double() for k in ("dY", "A", "B"))
+    dU = 0.25 * (dY @ B)
+    keep = ((Xd != 0) | (g["X"] == 0)).double()
+    want = (dY @ dense + keep / (1 - p) * (dU @ A), dU.t() @ x, 0.25 * (dY.t() @ U.double()))
+    for a, ref, tol in zip(got, want, (2e-3, 4e-6, 4e-6)):
+        assert float((a.double() - ref).norm() / ref.norm()) <= tol
+
+
+@pytest.mark.parametrize("M,members,K,r", [(40, (320,), 192, 16), (700, (512,), 768, 64), (1030, (512, 256), 768, 32)])
+def test_bwd_act8_of_a_centred_weight(M, members, K, r):
+    G, N = len(members), sum(members)
+    gen = torch.Generator().manual_seed(M)
+
+    def rnd(*s, std=1.0):
+        return (torch.randn(*s, generator=gen) * std).to(torch.bfloat16).cuda()
+    W = q.quantize_weight_centered(rnd(N, K, std=0.02))
+    A, B, X, dY = rnd(G * r, K, std=K ** -0.5), rnd(N, r, std=0.1), rnd(M, K), rnd(M, N)
+    U = X.float() @ A.float().t()
+    x8 = q.act8_quantize(X)
+    got = (q.qlora_group_bwd_act8(dY, x8, U, W, members, A, B, 0.5) if G > 1
+           else q.qlora_linear_bwd_act8(dY, x8, U, W, A, B, 0.5))
+    _check(dY, x8, U, q.nf4_dequantize_centered(W.codes, W.c8, W.s2, W.mean, N * K).view(N, K), members, A, B, 0.5, got)
+
+
 @pytest.mark.parametrize("M,N,K,r", [(64, 512, 512, 16), (1000, 384, 448, 64), (4096, 1024, 256, 64)])
 def test_sums_that_cancel(M, N, K, r):
     """Tokens in pairs whose terms of dA and dB nearly cancel: the errors stay within
