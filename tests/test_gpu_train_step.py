@@ -204,3 +204,41 @@ def test_shared_dirty_workspace_and_order_of_calls():
         st.run()
         torch.cuda.synchronize()
         assert _same(st.outputs(), want)
+
+
+@pytest.mark.parametrize("nf4", [False, True])
+@pytest.mark.parametrize("M,K,D,V,r", SIZES)
+def test_chain_gradients_against_differences(M, K, D, V, r, nf4):
+    """dA, dB and dX of the chain along a direction E against the mean loss in fp64
+    at two points Y +- h (dY/dparameter E) around the chain's own Y.  Off by dY's
+    errors, of which an element's is at most 2^-8 of itself and 2^-8 of g sum p_v
+    |W_v - W_label|; by dX's own rounding, 2^-8, dU's bf16 pair and the GEMM's sum
+    (2^-16 each at most); and the difference's third-order term, below 1e-5 as h
+    moves a logit by 2e-3 at most."""
+    st = Step(M, K, D, V, r, nf4, 10)
+    st.run()
+    out = st.outputs()
+    Y, head, y = out["Y"].double(), st.dense.double(), st.y
+    c = torch.nonzero(y != -100)[:, 0]
+
+    def mean_loss(Y):
+        z = Y @ head.t()
+        return (torch.logsumexp(z[c], 1) - z[c, y[c]]).mean()
+    z = Y[c] @ head.t()
+    p = torch.softmax(z, 1)
+    ref = (p.scatter_add(1, y[c, None], -torch.ones_like(p[:, :1])) @ head) / len(c)
+    apart = torch.stack([(p[i, :, None] * (head - head[y[t]]).abs()).sum(0) for i, t in enumerate(c)]) / len(c)
+    off = torch.zeros_like(Y)
+    off[c] = 2.0 ** -8 * 1.02 * (ref.abs() + apart)
+    W = q.nf4_dequantize(st.W.codes, st.W.c8, st.W.s2, D * K).view(D, K).double()
+    A, B, U, x = st.A.double(), st.B.double(), out["U"].double(), q.act8_dequantize(st.x8).double()
+    for grad, own, move in ((out["dA"], 1e-5, lambda E: st.s * (x @ E.t()) @ B.t()),
+                            (out["dB"], 1e-5, lambda E: st.s * U @ E.t()),
+                            (out["dX"], 2.0 ** -8 * 1.02, lambda E: E @ W.t() + st.s * (E @ A.t()) @ B.t())):
+        E = torch.sign(grad.double())
+        dy = move(E)
+        h = 1e-3 / float((dy.abs() @ head.abs().t()).max())
+        slope = float(mean_loss(Y + h * dy) - mean_loss(Y - h * dy)) / (2 * h)
+        pred = float((grad.double() * E).sum())
+        tol = float((off * dy.abs()).sum()) + (own + 1e-5) * pred
+        assert abs(pred - slope) <= tol and tol < 0.2 * pred
