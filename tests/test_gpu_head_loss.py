@@ -663,3 +663,33 @@ def test_gradients_of_the_losses_as_autograd_gives_them(T, V, D):
     for bad in (two.repeat(2), two.view(1, 1), two[0].double()):
         with pytest.raises(q.QloraError):
             q.qlora_head_loss_bwd(H, W, Y, lse, bad, stats=stats)
+
+
+@pytest.mark.parametrize("T,V,D,nf4", [(600, 20000, 2304, False), (2000, 12500, 1024, False), (1153, 5000, 4416, True)])
+def test_rows_that_count_are_rounded_once(T, V, D, nf4):
+    """Logits within +-40: no exponential is rescaled, in the backward none ever."""
+    assert T > 256 and 4.0 * T * V * D >= 1e11
+    h, w, y = _case(T, V, D, seed=20, lean=5.0)
+    H, Y, W = h.cuda(), y.cuda(), w.cuda()
+    if nf4:
+        W = q.quantize_weight(W)
+        w = q.nf4_dequantize(W.codes, W.c8, W.s2, V * D).view(V, D).cpu()
+    count = torch.nonzero(y != -100)[:, 0]
+    rows = count[torch.linspace(0, count.numel() - 1, 100).long()]
+    r, sel, g = Ref(h[rows], w, y[rows]), rows.cuda(), torch.linspace(-1, 2, T)
+    _, lse, _, dH = q.qlora_head_loss_step(H, W, Y, weight=g.cuda())
+    r.check_grad(dH[sel], g.numpy()[rows], roundings=1)
+    r.check_grad(q.qlora_head_loss_bwd(H, W, Y, lse, g.cuda())[sel], g.numpy()[rows], roundings=1)
+
+
+@pytest.mark.parametrize("T,V,D", [(5, 600001, 64), (130, 300000, 128)])
+def test_few_tokens_and_a_large_vocabulary(T, V, D):
+    """A contraction over several hundred thousand columns."""
+    h, w, y = _case(T, V, D, seed=21, lean=10.0)
+    n = min(T, 40)
+    r = Ref(h[:n], w, y[:n])
+    H, W, Y, g = h.cuda(), w.cuda(), y.cuda(), torch.linspace(-1, 2, T)
+    loss, lse, _, dH = q.qlora_head_loss_step(H, W, Y, weight=g.cuda())
+    assert np.all(np.abs(loss[:n].cpu().numpy() - r.loss) <= r.loss_tol)
+    r.check_grad(dH[:n], g.numpy()[:n])
+    r.check_grad(q.qlora_head_loss_bwd(H, W, Y, lse, g.cuda())[:n], g.numpy()[:n])
