@@ -1112,9 +1112,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32) head_combine_kernel(const 
           // exp(l - l_label) over the others; where that is near overflow, its log is log S + R - l_label.
           // The reference may lie far below the others' maximum (0 for 40), so S exp(R - z) can be large
           // where exp(R - z) is not a number of fp32: the exponential in two halves.
-          const float e = expf(0.5f * (R - z));
+          // (A label logit that overflowed: no number, as lse.)
+          const float e = z == INFINITY ? NAN : expf(0.5f * (R - z));
           const float x = (S * e) * e;
-          loss = x < 1e30f ? log1pf(x) : (R - z) + logf(S);
+          loss = x >= 1e30f ? (R - z) + logf(S) : log1pf(x);
           lse = top + logf(S * expf(R - top) + expf(z - top));  // (no others: R = -inf, S = 0)
           // and the root of 1 / (S + exp(z - R)), which overflows no earlier than it should
           if (STEP) a.row_root[t] = z > R ? e * rsqrtf(1.0f + x) : rsqrtf(S + expf(z - R));

@@ -693,3 +693,26 @@ def test_few_tokens_and_a_large_vocabulary(T, V, D):
     assert np.all(np.abs(loss[:n].cpu().numpy() - r.loss) <= r.loss_tol)
     r.check_grad(dH[:n], g.numpy()[:n])
     r.check_grad(q.qlora_head_loss_bwd(H, W, Y, lse, g.cuda())[:n], g.numpy()[:n])
+
+
+@pytest.mark.parametrize("T,V,D", [(40, 300, 64), (600, 20000, 2304)])
+def test_label_logit_that_overflows(T, V, D):
+    """lse - l of infinities is no number: neither is the loss, nor the row of dH."""
+    h, w, y = _case(T, V, D, seed=22, ignored=0.0)
+    h[3], w[7], y[3] = 0.0, 0.0, 7
+    y[y == 7], y[3] = 8, 7
+    H, W, Y, g = h.cuda(), w.cuda(), y.cuda(), torch.ones(T, device="cuda")
+    want = q.qlora_head_loss_step(H, W, Y, weight=g)
+    H[3, 1] = W[7, 1] = 1e30
+    W[:7, 1], W[8:, 1] = 0.0, 0.0
+    H[torch.arange(T, device="cuda") != 3, 1] = 0.0
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    step = q.qlora_head_loss_step(H, W, Y, weight=g, status=status)
+    assert int(status[0]) == q.DEV_NONFINITE
+    loss, lse, stats = q.qlora_head_loss_fwd(H, W, Y)
+    for v in (step[0][3], step[1][3], step[2][0], loss[3], lse[3], stats[0]):
+        assert not torch.isfinite(v)
+    assert torch.isnan(step[0][3]) and torch.isnan(loss[3]) and torch.isnan(step[3][3]).all()
+    keep = torch.arange(T, device="cuda") != 3
+    assert bool(torch.isfinite(step[0][keep]).all()) and bool(torch.isfinite(step[3][keep].float()).all())
+    assert bool(torch.isfinite(want[0]).all())
