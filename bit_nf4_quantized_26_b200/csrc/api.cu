@@ -1642,8 +1642,7 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     a.ncols = static_cast<int>(pv);
     a.ntiles = static_cast<int>(cdiv(pv, p.tw));
     a.kst = static_cast<int>(cdiv(D, 64));
-    // 64-deep stages per accumulator (head_loss.cu): a product of few tokens
-    // waits for the weight, and short chunks cost it nothing
+    // 64-deep stages per accumulator (measurements in head_loss.cu)
     a.kchunk = op == QLORA_HEAD_BWD ? 16 : (p.pair ? 12 : 4);
     float2* part = reinterpret_cast<float2*>(at(p.off_part));
     a.part = op == QLORA_HEAD_FWD ? part + i * p.parts * T : part;

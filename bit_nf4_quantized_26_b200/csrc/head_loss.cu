@@ -366,15 +366,17 @@ struct Ring {
 // per TPC, or one CTA per SM.
 //
 // The tensor core truncates when it adds to its fp32 accumulator: the sum
-// drifts towards zero by about 2^-24 of itself per K = 16 step (measured:
+// drifts towards zero by about 2^-26 of itself per K = 16 step (measured:
 // -8e-7 relative at dim 1024, -8e-6 at 8192, on random data).  A tile's
-// contraction of a loss is therefore cut into chunks (768 deep: 48 steps, a
-// drift of 6e-7) that alternate between two accumulators, and the epilogue
-// threads add each finished one to their registers, rounding to nearest, while
-// the next runs.  (512 deep costs the products 2-3%, 1024 nothing; 256 is free
-// for few tokens, whose products wait for W.)  Results rounded to bf16 take
-// longer ones: the backward's probabilities 1024, dH all of its
-// tile's or part's contraction.
+// contraction of a loss is therefore cut into chunks that alternate between two
+// accumulators, and the epilogue threads add each finished one to their
+// registers, rounding to nearest, while the next runs.  Pairs: 768 deep (48
+// steps, a drift of 6e-7; 512 deep costs the products 2-3%, 1024 nothing).
+// Single CTAs: 256 deep, which is free where the products wait for W (64 x 32000
+// x 4096, forward: 56.5 us, with 768 56.4) and costs 3% above (300 x 32000 x 4096:
+// 95.1 against 92.2; step 192 against 187), for losses 3e-7 instead of 8e-7
+// off.  Results rounded to bf16 take longer ones: the backward's probabilities
+// 1024, dH all of its tile's or part's contraction.
 //
 // Barriers (leader: the pair's first CTA, or the single one): full[s] (leader:
 // the stage's copies landed, and its dequantised tiles are written), empty[s]
