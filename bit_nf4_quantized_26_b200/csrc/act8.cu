@@ -431,16 +431,16 @@ cudaError_t launch_act8_quantize(const uint16_t* x, int64_t M, int64_t K, int64_
                                  int32_t* status, cudaStream_t stream) {
   const int64_t units = M * (K / 16);
   const int64_t ctas = (units + kActThreads - 1) / kActThreads;
-  return launch_kernel(wide_rows(x, ldx) ? act8_quantize_kernel<true> : act8_quantize_kernel<false>, dim3(static_cast<unsigned>(ctas)), dim3(kActThreads), 0, stream,
-                       dim3(1, 1, 1), x, units, K / 16, K, ldx, codes, exps, status);
+  return launch_kernel(wide_rows(x, ldx) ? act8_quantize_kernel<true> : act8_quantize_kernel<false>,
+                       dim3(static_cast<unsigned>(ctas)), dim3(kActThreads), 0, stream, dim3(1, 1, 1), x, units, K / 16, K, ldx, codes, exps, status);
 }
 
 cudaError_t launch_act8_dequantize(const uint8_t* codes, const uint8_t* exps, int64_t M, int64_t K, uint16_t* x,
                                    int64_t ldx, cudaStream_t stream) {
   const int64_t units = M * (K / 16);
   const int64_t ctas = (units + kActThreads - 1) / kActThreads;
-  return launch_kernel(wide_rows(x, ldx) ? act8_dequantize_kernel<true> : act8_dequantize_kernel<false>, dim3(static_cast<unsigned>(ctas)), dim3(kActThreads), 0, stream,
-                       dim3(1, 1, 1), codes, exps, units, K / 16, K, x, ldx);
+  return launch_kernel(wide_rows(x, ldx) ? act8_dequantize_kernel<true> : act8_dequantize_kernel<false>,
+                       dim3(static_cast<unsigned>(ctas)), dim3(kActThreads), 0, stream, dim3(1, 1, 1), codes, exps, units, K / 16, K, x, ldx);
 }
 
 cudaError_t launch_act8_da(const CUtensorMap& tm_du, const CUtensorMap& tm_du3, const CUtensorMap& tm_x,
@@ -451,8 +451,8 @@ cudaError_t launch_act8_da(const CUtensorMap& tm_du, const CUtensorMap& tm_du3, 
   // unsplit products as clusters of two tiles, as in skinny.cu: they run
   // beside a CTA-pair GEMM and then sit on both SMs of a TPC
   const dim3 cluster = (splits == 1 && grid_rows % 2 == 0) ? dim3(2, 1, 1) : dim3(1, static_cast<unsigned>(splits), 1);
-  return launch_kernel(act8_da_kernel, dim3(grid_rows, splits, 1), dim3(kActDaThreads), ActDaPlan::kSmem, stream, cluster,
-                       tm_du, tm_du3, tm_x, exps, a);
+  return launch_kernel(act8_da_kernel, dim3(grid_rows, splits, 1), dim3(kActDaThreads), ActDaPlan::kSmem, stream,
+                       cluster, tm_du, tm_du3, tm_x, exps, a);
 }
 
 }  // namespace qnf4

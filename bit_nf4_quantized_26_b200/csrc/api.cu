@@ -917,8 +917,8 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
   if (M == 0) return QLORA_OK;
   if (!dY || (!X.x && (!X.codes || !X.exps)) || !U || !A || !B || !dX || !dA || !dB) return QLORA_ERR_NULL;
   if (qlora_status st = check_weight_ptrs(W)) return st;
-  if (!aligned16(dY) || !aligned16(X.x) || !aligned16(X.codes) || !aligned16(X.exps) || !aligned16(U) || !aligned16(A) || !aligned16(B) || !aligned16(dX) ||
-      !aligned16(dA) || !aligned16(dB) || (d_status && !aligned16(d_status)))
+  if (!aligned16(dY) || !aligned16(X.x) || !aligned16(X.codes) || !aligned16(X.exps) || !aligned16(U) ||
+      !aligned16(A) || !aligned16(B) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) || (d_status && !aligned16(d_status)))
     return QLORA_ERR_ALIGN;
   const int64_t N = W.n_out, K = W.k_in;
   const int G = grp.G;
@@ -1092,8 +1092,8 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
 qlora_status qlora_linear_bwd(const uint16_t* dY, const uint16_t* X, const float* U, int64_t M, nf4_weight W,
                               const uint16_t* A, const uint16_t* B, int32_t r, float s, void* dX, int32_t dx_dtype,
                               float* dA, float* dB, void* ws, size_t ws_bytes, int32_t* d_status, void* stream) {
-  return linear_bwd_impl(dY, {X, nullptr, nullptr}, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes,
-                         d_status, stream, nullptr);
+  return linear_bwd_impl(dY, {X, nullptr, nullptr}, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA, dB,
+                         ws, ws_bytes, d_status, stream, nullptr);
 }
 
 // ------------------------------------------------------------ grouped linears
@@ -1126,8 +1126,8 @@ qlora_status qlora_group_bwd(const uint16_t* dY, const uint16_t* X, const float*
   if (members > 1 && r > kChunkRank) return QLORA_ERR_SHAPE;  // members' ranks are at most 64
   Group grp;
   if (qlora_status st = make_group(members, n_member, W.n_out, &grp)) return st;
-  return linear_bwd_impl(dY, {X, nullptr, nullptr}, U, M, W, grp, A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes, d_status, stream,
-                         nullptr);
+  return linear_bwd_impl(dY, {X, nullptr, nullptr}, U, M, W, grp, A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes,
+                         d_status, stream, nullptr);
 }
 
 qlora_status qlora_selftest_timeout(int32_t* d_status, int64_t limit_ns, void* stream) {
@@ -1192,8 +1192,8 @@ qlora_status qlora_linear_bwd_dropout(const uint16_t* dY, const uint16_t* X_drop
                                       size_t ws_bytes, int32_t* d_status, void* stream) {
   DropoutArgs d{};
   if (!dropout_args(p, seed, &d)) return QLORA_ERR_SHAPE;
-  return linear_bwd_impl(dY, {X_drop, nullptr, nullptr}, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA, dB, ws, ws_bytes,
-                         d_status, stream, &d);
+  return linear_bwd_impl(dY, {X_drop, nullptr, nullptr}, U, M, W, single_group(W.n_out), A, B, r, s, dX, dx_dtype, dA,
+                         dB, ws, ws_bytes, d_status, stream, &d);
 }
 
 // ------------------------------------------------------------------ optimizer
@@ -1598,7 +1598,8 @@ static qlora_status head_loss_impl(int op, const HeadCall& c, void* ws, size_t w
     ProfScope ps(kKHeadRows, cs);
     const HeadRowsArgs r{c.labels, c.ignore, V,        T,     0, rows,   place, nrows,  d_status,
                          rounding, c.H,      c.ldh,    D,     gather ? hrows : nullptr, c.dH, c.lddh};
-    if (qlora_status st = from_cuda(p.compact ? launch_head_rows(r, cs) : launch_head_clear(rounding, T, cs))) return st;
+    if (qlora_status st = from_cuda(p.compact ? launch_head_rows(r, cs) : launch_head_clear(rounding, T, cs)))
+      return st;
   }
   a.rounding = rounding;
   a.h = gather ? hrows : c.H;

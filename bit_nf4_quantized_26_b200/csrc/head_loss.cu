@@ -709,7 +709,8 @@ __global__ void __launch_bounds__(HeadPlan<MODE, PAIR, NF4>::kThreads, 1)
           if (!mbar_wait_warp(&accf[buf], (acc >> 1) & 1, wc)) break;
           tc_fence_after();
         }
-        float4* sum = reinterpret_cast<float4*>(a.acc) + (static_cast<int64_t>(it.slot) * kCtas + rank) * kSumBlock + et;
+        float4* sum =
+            reinterpret_cast<float4*>(a.acc) + (static_cast<int64_t>(it.slot) * kCtas + rank) * kSumBlock + et;
         const float al = (!a.first && a.alpha && rok) ? __ldcg(a.alpha + t) : 1.0f;
         const bool out = a.last && it.whole;
         float cn = 0.0f, cs = 0.0f, cl = 0.0f;

@@ -444,8 +444,8 @@ static cudaError_t launch_skinny_impl(const CUtensorMap& tmA, const CUtensorMap&
   // row tiles they sit on both SMs of a TPC, rather than on one SM of many
   // TPCs, each of which could then hold no GEMM pair.
   const dim3 cluster = (splits == 1 && grid_rows % 2 == 0) ? dim3(2, 1, 1) : dim3(1, static_cast<unsigned>(splits), 1);
-  return launch_kernel(skinny_kernel<MODE, SUMMED>, dim3(grid_rows, splits, 1), dim3(192), P::kSmem, stream, cluster, tmA,
-                       tmB, a);
+  return launch_kernel(skinny_kernel<MODE, SUMMED>, dim3(grid_rows, splits, 1), dim3(192), P::kSmem, stream, cluster,
+                       tmA, tmB, a);
 }
 
 cudaError_t launch_skinny(int mode, const CUtensorMap& tmA, const CUtensorMap& tmB, const SkinnyArgs& a,

@@ -94,7 +94,7 @@ struct HeadArgs {
   int tw;                 // columns of a tile: a multiple of 32 up to 256, NF4 128 (Grad: 256)
   const int64_t* labels;
   int64_t ignore;
-  float2* part;           // Loss, Exp: (reference, sum of the others' exponentials) [half tile][T], from the piece's first
+  float2* part;           // Loss, Exp: (reference, sum of the others' exponentials) [half tile][T] of the piece
   float* rsum;            // Exp: their sum as rounded to bf16, [half tile][T]
   // Prob, Grad (backward): what rounding the probabilities added to their sum, [T] integers, cleared before
   unsigned long long* rounding;
