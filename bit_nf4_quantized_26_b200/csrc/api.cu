@@ -1069,7 +1069,7 @@ static qlora_status linear_bwd_impl(const uint16_t* dY, const SavedInput& X, con
 
   // dA = dU^T X per member (contraction over M split over a cluster)
   CUtensorMap mduc, mduc3, mx;
-  if (!map_bf16(&mduc, ducat, M, 2 * ra, 64, 64) || !map_bf16(&mduc3, ducat3, M, 2 * ra, 64, 64) ||
+  if (!map_bf16(&mduc, ducat, M, 2 * ra, 64, 64) || (summed && !map_bf16(&mduc3, ducat3, M, 2 * ra, 64, 64)) ||
       !(X.x ? map_bf16(&mx, X.x, M, K, 64, 64) : map_u8(&mx, X.codes, M, K, 128, 64)))
     return QLORA_ERR_CUDA;
   {
